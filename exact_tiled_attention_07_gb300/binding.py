@@ -25,7 +25,8 @@ __all__ = [
     "fa_selftest_bounded_wait", "fa_fwd_bwd_host", "fa_fwd_bwd_host_workspace_size",
     "attention_forward", "attention_backward", "attention_decode",
     "attention_forward_fp8", "quantize_fp8", "EXPORTED_SYMBOLS", "NOALLOC_SCRATCH_BYTES",
-    "fa_sm_clock_sample",
+    "fa_sm_clock_sample", "kv4_cache", "fa_kv4_append", "fa_kv4_read", "kv4_read", "fa_decode_kv4",
+    "fa_decode_kv4_workspace_size", "attention_decode_kv4", "fa_kv4_evict",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -40,7 +41,8 @@ EXPORTED_SYMBOLS = (
     "fa_last_error_message", "fa_bwd_noalloc", "fa_fwd_gqa", "fa_bwd_gqa", "fa_decode", "fa_decode_workspace_size",
     "fa_quantize_fp8", "fa_fwd_fp8", "fa_fwd_fp8_gqa", "fa_fwd_masked", "fa_bwd_masked",
     "fa_selftest_bounded_wait", "fa_fwd_bwd_host", "fa_fwd_bwd_host_workspace_size", "fa_sm_clock_sample",
-    "fa_debug_build", "fa_selftest_debug_check",
+    "fa_debug_build", "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4",
+    "fa_decode_kv4_workspace_size", "fa_kv4_evict",
 )
 
 _lib = None
@@ -96,6 +98,13 @@ def load_library(path=None):
         lib.fa_fwd_bwd_host_workspace_size.argtypes = [i, i, i, i, i, i, i]
         lib.fa_fwd_bwd_host_workspace_size.restype = sz
         lib.fa_fwd_bwd_host.argtypes = [vp] * 10 + [sz, i, i, i, i, i, f, i, i, i, vp]
+        i64 = ctypes.c_int64
+        lib.fa_kv4_append.argtypes = [vp] * 6 + [i] * 5 + [i64] * 4 + [i, vp]
+        lib.fa_kv4_read.argtypes = [vp] * 5 + [i] * 5 + [i64] * 4 + [i, vp]
+        lib.fa_decode_kv4_workspace_size.argtypes = [i] * 7
+        lib.fa_decode_kv4_workspace_size.restype = sz
+        lib.fa_decode_kv4.argtypes = [vp] * 7 + [i] * 6 + [f, i, i, vp, sz, vp]
+        lib.fa_kv4_evict.argtypes = [vp] * 3 + [i, i] + [vp] * 4 + [i] * 5 + [vp]
         lib.fa_check_device_error.argtypes = [vp]
         lib.fa_sm_clock_sample.argtypes = [vp, i, vp]
         lib.fa_debug_build.argtypes = []
@@ -113,7 +122,7 @@ def load_library(path=None):
                      "fa_bwd_noalloc", "fa_bwd_preprocess",
                      "fa_bwd_main", "fa_bwd_dq_convert",
                      "fa_check_device_error", "fa_tile_counter", "fa_uses_tensor_cores", "fa_sm_clock_sample",
-                     "fa_selftest_debug_check"):
+                     "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_kv4_evict"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -153,17 +162,18 @@ def _dt(t):
         raise ValueError(f"unsupported dtype {t.dtype}") from None
 
 
-def _on_device(*ts):
+def _on_device(*ts, strided=()):
     """Every tensor given (None is skipped) is a contiguous CUDA tensor on the current device:
     the library takes raw device pointers and launches on the current device, so a host tensor
-    or one on another GPU would hand the kernels an address they cannot use."""
+    or one on another GPU would hand the kernels an address they cannot use.  Those in `strided`
+    (the first ones, checked by _packed) need not be contiguous."""
     dev = None
-    for t in ts:
+    for n, t in enumerate((*strided, *ts)):
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError("device arguments must be CUDA tensors (the library takes device pointers)")
-        if not t.is_contiguous():
+        if n >= len(strided) and not t.is_contiguous():
             raise ValueError("device arguments must be contiguous")
         if dev is None:
             dev, cur = t.device.index, torch.cuda.current_device()
@@ -411,6 +421,116 @@ def fa_bwd_masked(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, causal, windo
                                         int(window), mp, mh, _dt(Q), _stream(stream)))
 
 
+def _packed(t, what):
+    """(T, heads, d, token stride, head stride) of a packed [T, heads, d] tensor whose rows are
+    contiguous; strides of one-sized dimensions, which torch leaves open, as if contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{what}: expected a packed [T, heads, d] tensor, got shape {tuple(t.shape)}")
+    T, h, d = t.shape
+    ts, hs, es = t.stride()
+    if d > 1 and es != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return T, h, d, (ts if T > 1 else h * d), (hs if h > 1 else d)
+
+
+def _int32(t, n, what):
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"{what} must be an int32 tensor of {n} elements")
+
+
+def _kv4_shape(cache):
+    """(B, Hkv, capacity, d) of a 4-bit cache tensor (kv4_cache)."""
+    if cache.dtype != torch.uint8 or cache.dim() != 4 or cache.shape[3] % 72:
+        raise ValueError("a 4-bit cache is a uint8 tensor [B, Hkv, capacity / 64, 72 d]")
+    B, Hkv, nb, nbytes = cache.shape
+    return B, Hkv, nb * 64, nbytes // 72
+
+
+def _kv4_weights(t, B, Hkv, capacity, what):
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (B, Hkv, capacity)):
+        raise ValueError(f"{what} must be an fp32 tensor [{B}, {Hkv}, {capacity}]")
+
+
+def kv4_cache(B, Hkv, capacity, d, device="cuda"):
+    """An empty 4-bit key/value cache for B sequences of up to `capacity` tokens (rounded up to a
+    multiple of 64): a uint8 tensor [B, Hkv, capacity / 64, 72 d] (block layout: include/fa.h)."""
+    if d not in (64, 128, 256):
+        raise ValueError(f"the 4-bit cache supports d in {{64, 128, 256}}, got {d}")
+    return torch.zeros((B, Hkv, (capacity + 63) // 64, 72 * d), dtype=torch.uint8, device=device)
+
+
+def _kv4_rows(K, V, cu_seqlens, lens, cache, weights):
+    B, Hkv, capacity, d = _kv4_shape(cache)
+    T, hk, dk, k_ts, k_hs = _packed(K, "K")
+    _, _, _, v_ts, v_hs = _packed(V, "V")
+    _on_device(cu_seqlens, lens, cache, weights, strided=(K, V))
+    if (hk, dk) != (Hkv, d) or V.shape != K.shape or V.dtype != K.dtype:
+        raise ValueError("K, V must be [T, Hkv, d] of one dtype with the cache's heads and head dimension")
+    _int32(cu_seqlens, B + 1, "cu_seqlens")
+    _int32(lens, B, "lens")
+    _kv4_weights(weights, B, Hkv, capacity, "weights")
+    return (B, T, Hkv, capacity, d, k_ts, k_hs, v_ts, v_hs, _dt(K))
+
+
+def fa_kv4_append(K, V, cu_seqlens, lens, cache, weights=None, stream=None):
+    """Packed rows K, V [T, Hkv, d] (rows cu_seqlens[b] .. cu_seqlens[b + 1] of sequence b) into the
+    newest slots of a 4-bit cache; lens [B] counts them already. weights [B, Hkv, capacity]: set
+    to 0 at the new slots."""
+    args = _kv4_rows(K, V, cu_seqlens, lens, cache, weights)
+    _check(load_library().fa_kv4_append(_p(K), _p(V), _p(cu_seqlens), _p(lens), _p(cache), _p(weights), *args,
+                                        _stream(stream)))
+
+
+def fa_kv4_read(cache, cu_seqlens, lens, K, V, stream=None):
+    """The values of the newest slots into packed K, V [T, Hkv, d]: the inverse of fa_kv4_append."""
+    args = _kv4_rows(K, V, cu_seqlens, lens, cache, None)
+    _check(load_library().fa_kv4_read(_p(cache), _p(cu_seqlens), _p(lens), _p(K), _p(V), *args, _stream(stream)))
+
+
+def fa_decode_kv4_workspace_size(B, H, Hkv, Nq, capacity, d, weights=False) -> int:
+    return int(load_library().fa_decode_kv4_workspace_size(B, H, Hkv, Nq, capacity, d, int(bool(weights))))
+
+
+def fa_decode_kv4(Q, cache, lens, O, L, scale, causal=False, weights_in=None, weights_out=None, workspace=None,
+                  stream=None):
+    """Decode: Q, O [B, H, Nq, d] over a 4-bit cache with lens [B] slots in use; L [B, H, Nq].
+    weights_out [B, Hkv, capacity] = weights_in + the attention each slot got (slots in use)."""
+    B, H, Nq, d = _shape4(Q)
+    Bc, Hkv, capacity, dc = _kv4_shape(cache)
+    _on_device(Q, cache, lens, O, L, weights_in, weights_out, workspace)
+    if (Bc, dc) != (B, d):
+        raise ValueError("the cache must have Q's batch and head dimension")
+    _same(Q, O)
+    _rows(L, B * H * Nq)
+    _int32(lens, B, "lens")
+    _kv4_weights(weights_in, B, Hkv, capacity, "weights_in")
+    _kv4_weights(weights_out, B, Hkv, capacity, "weights_out")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().fa_decode_kv4(_p(Q), _p(cache), _p(lens), _p(O), _p(L), _p(weights_in), _p(weights_out), B, H,
+                                        Hkv, Nq, capacity, d, float(scale), int(bool(causal)), _dt(Q), _p(workspace),
+                                        nbytes, _stream(stream)))
+
+
+def fa_kv4_evict(cache, weights, lens, keep, recent, out_cache, out_weights, out_lens, kept, stream=None):
+    """The `recent` newest and the heaviest other slots of each sequence and head, `keep` in all, in
+    their order into another cache (with weights and lens); kept [B, Hkv, keep]: where they were."""
+    B, Hkv, capacity, d = _kv4_shape(cache)
+    Bo, ho, out_capacity, do = _kv4_shape(out_cache)
+    _on_device(cache, weights, lens, out_cache, out_weights, out_lens, kept)
+    if (Bo, ho, do) != (B, Hkv, d):
+        raise ValueError("out_cache must have the cache's batch, heads and head dimension")
+    if weights is None or out_weights is None:
+        raise ValueError("eviction needs weights and out_weights")
+    _kv4_weights(weights, B, Hkv, capacity, "weights")
+    _kv4_weights(out_weights, B, Hkv, out_capacity, "out_weights")
+    _int32(lens, B, "lens")
+    _int32(out_lens, B, "out_lens")
+    _int32(kept, B * Hkv * int(keep), "kept")
+    _check(load_library().fa_kv4_evict(_p(cache), _p(weights), _p(lens), int(keep), int(recent), _p(out_cache),
+                                       _p(out_weights), _p(out_lens), _p(kept), B, Hkv, capacity, out_capacity, d,
+                                       _stream(stream)))
+
+
 def fa_selftest_bounded_wait(timeout_ms=20, arrive=False, stream=None):
     """Launch the bounded-wait self-test (see include/fa.h); read the outcome with fa_check_device_error."""
     _check(load_library().fa_selftest_bounded_wait(int(timeout_ms), int(bool(arrive)), _stream(stream)))
@@ -517,6 +637,43 @@ def attention_decode(q, k, v, scale=None, splits=0, stream=None):
     nbytes = fa_decode_workspace_size(B, H, Hkv, Nq, Nk, d, splits)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     fa_decode(q, k, v, o, lse, scale, splits, ws, stream)
+    return o, lse
+
+
+def _used_on(stream, *ts):
+    """Tensors allocated here on the current stream and used on `stream`: their memory must not go
+    to another tensor of the current stream before that use is over."""
+    if stream is None:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    for t in ts:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def kv4_read(cache, cu_seqlens, lens, total, dtype=torch.bfloat16, stream=None):
+    """k, v [total, Hkv, d] = fa_kv4_read(...): the values of the newest slots, packed."""
+    _, Hkv, _, d = _kv4_shape(cache)
+    k = torch.empty((total, Hkv, d), dtype=dtype, device=cache.device)
+    v = torch.empty_like(k)
+    fa_kv4_read(cache, cu_seqlens, lens, k, v, stream)
+    _used_on(stream, k, v)
+    return k, v
+
+
+def attention_decode_kv4(q, cache, lens, causal=False, scale=None, weights_in=None, weights_out=None, stream=None):
+    """O, L = fa_decode_kv4(...) for q [B, H, Nq, d] over a 4-bit cache; outputs and workspace
+    allocated with torch."""
+    B, H, Nq, d = _shape4(q)
+    _, Hkv, capacity, _ = _kv4_shape(cache)
+    scale = d ** -0.5 if scale is None else scale
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    nbytes = fa_decode_kv4_workspace_size(B, H, Hkv, Nq, capacity, d, weights_out is not None)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    fa_decode_kv4(q, cache, lens, o, lse, scale, causal, weights_in, weights_out, ws, stream)
+    _used_on(stream, o, lse, ws)
     return o, lse
 
 

@@ -136,6 +136,40 @@ fa_status carve(BwdArgs* a, void* ws, size_t ws_bytes, int B, int H, int N, int 
   return FA_OK;
 }
 
+// 4-bit cache arguments (include/fa.h).
+fa_status check_kv4(int B, int Hkv, int capacity, int d, bool* empty) {
+  *empty = false;
+  if (B < 0) return fail(FA_ERR_INVALID_ARG, "negative size B=%d", B);
+  if (Hkv < 1) return fail(FA_ERR_INVALID_ARG, "Hkv=%d key/value heads: at least one", Hkv);
+  if (d != 64 && d != 128 && d != 256)
+    return fail(FA_ERR_UNSUPPORTED, "the 4-bit cache supports d in {64, 128, 256}, got %d", d);
+  if (capacity < 64 || capacity % 64 != 0)
+    return fail(FA_ERR_INVALID_ARG, "capacity=%d is not a positive multiple of 64", capacity);
+  if ((int64_t)B * Hkv > INT32_MAX / 4 || (int64_t)Hkv * (capacity / 64) > INT32_MAX ||
+      (double)B * Hkv * capacity * d > 4.0e15)
+    return fail(FA_ERR_INVALID_ARG, "cache too large: B=%d Hkv=%d capacity=%d", B, Hkv, capacity);
+  if (B == 0) *empty = true;
+  return FA_OK;
+}
+
+// Arrays of 32-bit integers or floats that need their natural alignment only.
+fa_status check_words(std::initializer_list<const void*> ptrs, const char* what) {
+  for (const void* p : ptrs)
+    if (!p || (reinterpret_cast<uintptr_t>(p) & 3u) != 0)
+      return fail(FA_ERR_INVALID_ARG, "%s: a 32-bit array is null or not 4-byte aligned", what);
+  return FA_OK;
+}
+
+// Token and head strides of a packed [T][heads][d] tensor: rows may lie apart (a slice of a fused
+// projection) but each starts on 16 bytes.
+fa_status check_strides(std::initializer_list<int64_t> strides, int elem_bytes, const char* what) {
+  for (int64_t s : strides)
+    if (s < 0 || s >= ((int64_t)1 << 38) || (s * elem_bytes) % 16 != 0)
+      return fail(FA_ERR_INVALID_ARG, "%s: a stride of %lld elements is negative, too large or not a multiple of 16 bytes",
+                  what, (long long)s);
+  return FA_OK;
+}
+
 }  // namespace
 
 unsigned long long current_context_id() {
@@ -533,6 +567,124 @@ fa_status fa_fwd_fp8(const void* Q8, const void* K8, const void* V8, const float
                      fa_dtype out_dtype, void* stream) {
   return fa_fwd_fp8_gqa(Q8, K8, V8, q_scales, k_scales, v_scales, O, L, B, H, H, N, d, scale, causal, out_dtype,
                         stream);
+}
+
+static fa_status kv4_rows(bool read, const void* K, const void* V, const int32_t* cu_seqlens, const int32_t* lens,
+                          void* cache, float* weights, int B, int T, int Hkv, int capacity, int d,
+                          int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                          int64_t v_head_stride, fa_dtype dtype, void* stream, const char* name) {
+  bool empty;
+  fa_status st = check_kv4(B, Hkv, capacity, d, &empty);
+  if (st != FA_OK) return st;
+  if (dtype != FA_BF16 && dtype != FA_FP16 && dtype != FA_FP32)
+    return fail(FA_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  if (T < 0) return fail(FA_ERR_INVALID_ARG, "%s: negative row count T=%d", name, T);
+  if (empty || T == 0) return FA_OK;
+  if ((st = check_ptrs({K, V, cache}, name)) != FA_OK) return st;
+  if ((st = check_words({cu_seqlens, lens}, name)) != FA_OK) return st;
+  if (weights && (st = check_words({weights}, name)) != FA_OK) return st;
+  const int eb = dtype == FA_FP32 ? 4 : 2;
+  if ((st = check_strides({k_token_stride, k_head_stride, v_token_stride, v_head_stride}, eb, name)) != FA_OK) return st;
+  if ((int64_t)T * Hkv * (d / 8) > (int64_t)INT32_MAX * 256)
+    return fail(FA_ERR_INVALID_ARG, "%s: T=%d rows of %d heads are too many for one call", name, T, Hkv);
+  DeviceSyms syms;
+  if ((st = device_syms(&syms)) != FA_OK) return st;
+  Kv4RowArgs a{K, V, cu_seqlens, lens, static_cast<uint8_t*>(cache), weights, B, T, Hkv, capacity, d,
+               k_token_stride, k_head_stride, v_token_stride, v_head_stride, (int)dtype, syms.err,
+               static_cast<cudaStream_t>(stream)};
+  return launched(read ? launch_kv4_read(a) : launch_kv4_append(a), name);
+}
+
+fa_status fa_kv4_append(const void* K, const void* V, const int32_t* cu_seqlens, const int32_t* lens, void* cache,
+                        float* weights, int B, int T, int Hkv, int capacity, int d, int64_t k_token_stride,
+                        int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, fa_dtype dtype,
+                        void* stream) {
+  return kv4_rows(false, K, V, cu_seqlens, lens, cache, weights, B, T, Hkv, capacity, d, k_token_stride, k_head_stride,
+                  v_token_stride, v_head_stride, dtype, stream, "fa_kv4_append");
+}
+
+fa_status fa_kv4_read(const void* cache, const int32_t* cu_seqlens, const int32_t* lens, void* K, void* V, int B, int T,
+                      int Hkv, int capacity, int d, int64_t k_token_stride, int64_t k_head_stride,
+                      int64_t v_token_stride, int64_t v_head_stride, fa_dtype dtype, void* stream) {
+  return kv4_rows(true, K, V, cu_seqlens, lens, const_cast<void*>(cache), nullptr, B, T, Hkv, capacity, d,
+                  k_token_stride, k_head_stride, v_token_stride, v_head_stride, dtype, stream, "fa_kv4_read");
+}
+
+static fa_status check_decode_kv4(int B, int H, int Hkv, int Nq, int capacity, int d, bool* empty) {
+  fa_status st = check_kv4(B, Hkv, capacity, d, empty);
+  if (st != FA_OK) return st;
+  if (H < 0 || Nq < 0) return fail(FA_ERR_INVALID_ARG, "negative size H=%d Nq=%d", H, Nq);
+  if (*empty || H == 0 || Nq == 0) {
+    *empty = true;
+    return FA_OK;
+  }
+  if ((st = check_heads(H, Hkv)) != FA_OK) return st;
+  // rows of one key/value head, and its blocks times groups of eight of them, are counted in 32 bits
+  const int64_t rows = (int64_t)(H / Hkv) * Nq;
+  if (rows > INT32_MAX / 64 || (double)B * Hkv * ((rows + 7) / 8) > 1.0e9 ||
+      (double)Hkv * ((rows + 7) / 8) * (capacity / 64) > 2.0e9 || (double)B * Hkv * (capacity / 64) > 2.0e9 ||
+      (double)B * Hkv * rows * capacity > 2.0e18)
+    return fail(FA_ERR_INVALID_ARG, "problem too large");
+  return FA_OK;
+}
+
+size_t fa_decode_kv4_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d, int weights) {
+  bool empty;
+  if (check_decode_kv4(B, H, Hkv, Nq, capacity, d, &empty) != FA_OK || empty) return 0;
+  return decode_kv4_workspace_bytes(B, H, Hkv, Nq, capacity, d, weights != 0);
+}
+
+fa_status fa_decode_kv4(const void* Q, const void* cache, const int32_t* lens, void* O, float* L,
+                        const float* weights_in, float* weights_out, int B, int H, int Hkv, int Nq, int capacity, int d,
+                        float scale, int causal, fa_dtype dtype, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  bool empty;
+  fa_status st = check_decode_kv4(B, H, Hkv, Nq, capacity, d, &empty);
+  if (st != FA_OK) return st;
+  if (dtype != FA_BF16 && dtype != FA_FP16)
+    return fail(FA_ERR_UNSUPPORTED, "fa_decode_kv4 takes bf16 or fp16 queries, not dtype %d", (int)dtype);
+  if (empty) return FA_OK;
+  if ((st = check_ptrs({Q, cache, O, workspace}, "fa_decode_kv4")) != FA_OK) return st;
+  if ((st = check_words({lens, L}, "fa_decode_kv4")) != FA_OK) return st;
+  if (weights_in && !weights_out)
+    return fail(FA_ERR_INVALID_ARG, "fa_decode_kv4: weights_in without weights_out");
+  if (weights_out && (st = check_words({weights_out}, "fa_decode_kv4")) != FA_OK) return st;
+  if (weights_in && (st = check_words({weights_in}, "fa_decode_kv4")) != FA_OK) return st;
+  if ((st = check_scale(scale)) != FA_OK) return st;
+  const size_t need = decode_kv4_workspace_bytes(B, H, Hkv, Nq, capacity, d, weights_out != nullptr);
+  if (workspace_bytes < need)
+    return fail(FA_ERR_INVALID_ARG, "fa_decode_kv4: workspace of %zu bytes < %zu required", workspace_bytes, need);
+  DeviceSyms syms;
+  if ((st = device_syms(&syms)) != FA_OK) return st;
+  DecodeKv4Args a{Q, static_cast<const uint8_t*>(cache), lens, O, L, weights_in, weights_out, workspace, B, H, Hkv, Nq,
+                  capacity, d, scale, causal ? 1 : 0, (int)dtype, syms.err, static_cast<cudaStream_t>(stream)};
+  return launched(launch_decode_kv4(a), "fa_decode_kv4");
+}
+
+fa_status fa_kv4_evict(const void* cache, const float* weights, const int32_t* lens, int keep, int recent,
+                       void* out_cache, float* out_weights, int32_t* out_lens, int32_t* kept, int B, int Hkv,
+                       int capacity, int out_capacity, int d, void* stream) {
+  bool empty;
+  fa_status st = check_kv4(B, Hkv, capacity, d, &empty);
+  if (st != FA_OK) return st;
+  if ((st = check_kv4(B, Hkv, out_capacity, d, &empty)) != FA_OK) return st;
+  if (keep < 1 || keep > out_capacity)
+    return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: keep=%d outside [1, out_capacity=%d]", keep, out_capacity);
+  if (recent < 0 || recent > keep)
+    return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: recent=%d outside [0, keep=%d]", recent, keep);
+  if (empty) return FA_OK;
+  if ((st = check_ptrs({cache, out_cache}, "fa_kv4_evict")) != FA_OK) return st;
+  if ((st = check_words({weights, lens, out_weights, out_lens, kept}, "fa_kv4_evict")) != FA_OK) return st;
+  if (cache == out_cache || weights == out_weights)
+    return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: the kept rows go into another cache, not into their own");
+  if ((double)B * Hkv * keep * (d / 16) > 256.0 * INT32_MAX)
+    return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: too many rows for one call");
+  DeviceSyms syms;
+  if ((st = device_syms(&syms)) != FA_OK) return st;
+  Kv4EvictArgs a{static_cast<const uint8_t*>(cache), weights, lens, static_cast<uint8_t*>(out_cache), out_weights,
+                 out_lens, kept, B, Hkv, capacity, out_capacity, d, keep, recent, syms.err,
+                 static_cast<cudaStream_t>(stream)};
+  return launched(launch_kv4_evict(a), "fa_kv4_evict");
 }
 
 fa_status fa_check_device_error(void* stream) {

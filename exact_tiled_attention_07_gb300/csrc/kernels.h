@@ -184,6 +184,60 @@ cudaError_t launch_sm_clock_sample(unsigned long long* out, int blocks, cudaStre
 // returns `status`.
 int set_last_error(int status, const char* fmt, ...);
 
+// 4-bit cache (layout: kv4.cuh) rows: packed K, V rows [t][hkv][d] with the given element strides
+// (rows of sequence b: [cu[b], cu[b + 1])) and the last of the lens[b] cached slots of sequence b.
+struct Kv4RowArgs {
+  const void* k;  // written by the read
+  const void* v;
+  const int32_t* cu;    // [b + 1]
+  const int32_t* lens;  // [b]
+  uint8_t* cache;       // [b][hkv][capacity / 64] blocks
+  float* weights;       // append: [b][hkv][capacity] set to 0 at the new slots (may be null)
+  int b, t, hkv, capacity, d;
+  int64_t k_ts, k_hs, v_ts, v_hs;  // token and head strides, elements
+  int dtype;
+  unsigned long long* err;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv4_append(const Kv4RowArgs& a);
+cudaError_t launch_kv4_read(const Kv4RowArgs& a);
+
+// Decode over the 4-bit cache: Q, O [b][h][nq][d], L [b][h][nq], lens [b] on the device.
+struct DecodeKv4Args {
+  const void* q;
+  const uint8_t* cache;
+  const int32_t* lens;
+  void* o;
+  float* lse;
+  const float* w_in;  // accumulated weights [b][hkv][capacity]; w_out null: none
+  float* w_out;
+  void* ws;
+  int b, h, hkv, nq, capacity, d;
+  float scale;
+  int causal;
+  int dtype;
+  unsigned long long* err;
+  cudaStream_t stream;
+};
+size_t decode_kv4_workspace_bytes(int b, int h, int hkv, int nq, int capacity, int d, bool weights);
+cudaError_t launch_decode_kv4(const DecodeKv4Args& a);
+
+// Eviction: the `recent` newest and the heaviest other slots of each sequence and key/value head,
+// `keep` in all, in their order, from one cache into another.
+struct Kv4EvictArgs {
+  const uint8_t* cache;
+  const float* weights;  // [b][hkv][capacity]
+  const int32_t* lens;   // [b]
+  uint8_t* out_cache;
+  float* out_weights;  // [b][hkv][out_capacity]
+  int32_t* out_lens;   // [b] (may be lens)
+  int32_t* kept;       // [b][hkv][keep] source slots, -1 behind the last
+  int b, hkv, capacity, out_capacity, d, keep, recent;
+  unsigned long long* err;
+  cudaStream_t stream;
+};
+cudaError_t launch_kv4_evict(const Kv4EvictArgs& a);
+
 bool fwd_tc_supported(int dtype, int d);
 bool bwd_tc_supported(int dtype, int d);
 bool bwd_masked_fits(int group, int n, int d);  // masked backward's step list fits (tensor-core path)

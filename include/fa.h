@@ -286,6 +286,82 @@ FA_API fa_status fa_fwd_fp8_gqa(const void* Q8, const void* K8, const void* V8, 
                                 int Hkv, int N, int d, float scale, int causal, fa_dtype out_dtype, void* stream);
 
 /*
+ * A key/value cache held in 4 bits an element (as the FP8 quantiser's block scales, "Lecture 8"
+ * §8.1, with one step and one middle per 64 channels of a row; the cache and its decode of §8.2).
+ *   cache     [B][Hkv][capacity / 64] blocks of 72 d bytes, 16-byte aligned; capacity (slots of a
+ *             sequence) a positive multiple of 64; d in {64, 128, 256}. A block holds 64
+ *             consecutive slots of one key/value head:
+ *               K codes [64][d / 2], V codes [64][d / 2]   channel 2i in bits 0-3 of a byte, 2i + 1
+ *                                                          in bits 4-7
+ *               K, then V parameters [64][d / 64][2] fp16  step and middle of each 64 channels
+ *             and a code c stands for middle + step (c - 8). For a group x of 64 channels, in fp32
+ *             rounded to nearest: step = fp16((max x - min x) / 15) rounded up, middle =
+ *             fp16(min x + 8 step), c = clamp(rint((x - middle) / step), -8, 7) + 8 (8 when step is
+ *             0), so a value is off by at most max(step / 2, 2^-11 |middle|) and fp32 roundings. A
+ *             group with a NaN or a magnitude above 32768 is held as NaN.
+ *   lens      device int32 [B]: slots in use, slots [0, lens[b]) of sequence b. The cache itself keeps
+ *             no length: the caller owns lens, counts it up and may change it between calls on the
+ *             stream. (The lengths are read on the device, so one captured graph serves any lengths.)
+ *   rows      K, V of several sequences packed one behind the other, [T][Hkv][d] with the last
+ *             dimension contiguous and any token and head strides that are multiples of 16 bytes;
+ *             cu_seqlens, device int32 [B + 1], non-decreasing: rows [cu_seqlens[b], cu_seqlens[b + 1]) belong
+ *             to sequence b. Rows outside [cu_seqlens[0], cu_seqlens[B]) are neither read nor written.
+ * fa_kv4_append writes a sequence's rows into its newest slots: n_b rows go to slots lens[b] - n_b ..
+ * lens[b] - 1 (lens counts them already), and sets their weights (may be NULL; [B][Hkv][capacity] fp32)
+ * to 0. fa_kv4_read is the inverse: it writes the values of those slots to K and V, in fp32 rounded once
+ * to dtype (bf16, fp16 or fp32; need not be the dtype they were appended in). One kernel launch each.
+ * A row whose slot lies outside [0, capacity) is skipped and recorded as a device error
+ * (fa_check_device_error: FA_ERR_DEVICE).
+ */
+FA_API fa_status fa_kv4_append(const void* K, const void* V, const int32_t* cu_seqlens, const int32_t* lens,
+                               void* cache, float* weights, int B, int T, int Hkv, int capacity, int d,
+                               int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                               int64_t v_head_stride, fa_dtype dtype, void* stream);
+FA_API fa_status fa_kv4_read(const void* cache, const int32_t* cu_seqlens, const int32_t* lens, void* K, void* V, int B,
+                             int T, int Hkv, int capacity, int d, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, fa_dtype dtype, void* stream);
+
+/*
+ * Decode attention over the 4-bit cache (fa_decode over quantised keys and values of different
+ * lengths): exact attention of the values that the codes stand for.
+ *   Q, O      [B][H][Nq][d] dtype (bf16 or fp16), the new query rows; L [B][H][Nq] fp32
+ *   lens      as above; a row sees slots [0, lens[b]), or with causal != 0 row i of the Nq sees slots
+ *             [0, lens[b] - Nq + i + 1): the Nq rows are then the newest slots' own. A row that sees
+ *             nothing gets O = 0, L = -inf. A length outside [0, capacity] is clamped to it and
+ *             recorded as a device error.
+ *   weights   weights_out non-NULL: weights_out[b][hkv][j] = weights_in[b][hkv][j] + the sum of the probabilities
+ *             that slot j got from the H / Hkv x Nq rows of its key/value head, for j < lens[b]; the other
+ *             slots of weights_out are left as they were. weights_in may be NULL (zeros) or weights_out itself.
+ *   workspace fa_decode_kv4_workspace_size(...) bytes for the same arguments (weights: whether
+ *             weights_out is given); its contents on entry do not matter. Calls that may overlap on the
+ *             GPU need workspaces of their own.
+ * Keys and their scores are never rounded to 16 bits; values and probabilities enter the second product
+ * rounded to fp16 (relative 2^-11). The work is cut into equal runs of blocks on the device, whatever
+ * the lengths. Results do not depend on timing: two calls with the same arguments give the same bits.
+ */
+FA_API size_t fa_decode_kv4_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d, int weights);
+FA_API fa_status fa_decode_kv4(const void* Q, const void* cache, const int32_t* lens, void* O, float* L,
+                               const float* weights_in, float* weights_out, int B, int H, int Hkv, int Nq, int capacity,
+                               int d, float scale, int causal, fa_dtype dtype, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * Eviction from the 4-bit cache by accumulated attention weight (the weights of fa_decode_kv4).
+ * Of each sequence and key/value head, min(lens[b], keep) slots stay: the `recent` newest ones and,
+ * of the others, those of the largest weight (ties go to the lowest slot; NaN counts as the
+ * largest). They go, in their order, to slots 0, 1, ... of another cache, with their weights.
+ *   keep      1 .. out_capacity; recent 0 .. keep
+ *   kept      out: int32 [B][Hkv][keep], the slot that each kept one came from, -1 behind the last
+ *   out_lens  out: int32 [B], min(lens[b], keep) (may be lens)
+ *   out_cache, out_weights: of out_capacity slots, not the source; slots behind the kept ones are left
+ *             as they were.
+ * A length outside [0, capacity] is clamped to it and recorded as a device error.
+ */
+FA_API fa_status fa_kv4_evict(const void* cache, const float* weights, const int32_t* lens, int keep, int recent,
+                              void* out_cache, float* out_weights, int32_t* out_lens, int32_t* kept, int B, int Hkv,
+                              int capacity, int out_capacity, int d, void* stream);
+
+/*
  * Synchronises `stream` and reports device-side failures of earlier calls on the
  * current device: FA_ERR_CUDA for a CUDA error, FA_ERR_TIMEOUT / FA_ERR_DEVICE for a
  * failure a kernel recorded. The recorded failure is cleared.
