@@ -3,33 +3,37 @@
 // For the R = (H / Hkv) Nq query rows that read one key/value head, with x_hat the value that a
 // cached code stands for (x_hat = middle + step (code - 8), one step and middle per 64 channels):
 //   S_rj = tau log2e sum_g [ step_K(j, g) (q_r . (code_K(j) - 8))_g + middle_K(j, g) sum_g q_r ]
-//   O_r  = sum_j 2^(S_rj - m_r) v_hat_j / l_r,   L_r = (m_r + log2 l_r) ln 2,
-//   weights_j += sum_r 2^(S_rj - m_r) / l_r      (when asked for)
-// The step and middle of a key enter behind the dot product, in fp32, so keys are never rounded.
+//   O_r  = sum_g [ sum_j P_rj step_V(j, g) (code_V(j) - 8) + sum_j P_rj middle_V(j, g) ] / l_r
+//   P_rj = 2^(S_rj - m_r), l_r = sum_j P_rj, L_r = (m_r + log2 l_r) ln 2
+//   weights_j += sum_r P_rj / l_r      (when asked for)
+// Steps and middles never touch the codes: those of a key enter behind the dot product, those of a
+// value in front of it, in fp32, so keys and values are not rounded.
 //
-// Bound: HBM (72 d / 64 bytes for d keys and d values, 9 bits per channel pair), then the
-// instructions that turn codes into numbers.  So codes go from shared memory straight into the
-// registers of mma.sync operands (m16n8k16): tcgen05 would want them as 16-bit tiles in shared
-// or tensor memory, four times the bytes written and read again, for query tiles of 8 rows of
-// which it would use 8 in 128.
+// Bound: HBM (9/16 byte a channel of a key or value), then the instructions that turn codes into
+// numbers.  So codes go from shared memory straight into the registers of mma.sync (m16n8k16, fp16,
+// fp32 sums) operands: tcgen05 would want them as 8- or 16-bit tiles in shared or tensor memory, two to
+// four times the bytes written and read again, for a tile of 128 rows where a head has 8.  A nibble
+// or-ed into fp16 1024 counts 1 or 16, in place or after a shift by 8, and one addition or
+// fused multiply-add brings the pair to code - 8 (exact): 9 instructions for 8 codes.  (E4M3
+// holds the bytes 0000cccc as they are, but its mma.sync runs as conversions and fp16 products here:
+// 523 instructions for 16 tokens of 128 channels against 441 for a version with 13 per 8 codes.)
 //
-//   S^T = K Q^T: K is the A operand (16 tokens x 16 channels), Q^T the B operand (8 query rows).
-//     A 32-bit word of codes holds channels 8w .. 8w + 7; (w >> 4n) & 0x000F000F is channels
-//     8w + n and 8w + n + 4 in the two halves of a register: an operand register, once the bits
-//     of 128 (bf16) or 1024 (fp16) are or-ed in and that plus 8 is subtracted (exact).  Channels
-//     may come in any order in a dot product, so Q is laid out in registers to match.
-//   O^T = V^T P^T: V^T is the A operand (16 channels x 16 tokens): a register holds one channel of
-//     two tokens, so the words of two tokens are interleaved by halves first.  v_hat is computed in
-//     fp16 (one fused multiply-add, rounded once, 2^-11); P is rounded to fp16 (2^-11) scaled by
-//     2^8, so that probabilities down to 2^-22 of the row's largest keep their full precision.
-//     P^T comes out of the S^T accumulators by movmatrix.
+//   S^T = K Q^T: K is the A operand (16 tokens x 16 channels).  Channels may come in any order in a
+//     dot product, so Q is laid out to match; it is scaled by a power of two that puts the row's
+//     largest element in [2^14, 2^15), so a bf16 q is exact in fp16 down to 2^-29 of that.
+//   O^T = V^T P^T: V^T is the A operand (16 channels x 16 tokens): a register holds one channel of two
+//     tokens, so the words of two tokens are interleaved by halves first.  P step_V is rounded to
+//     fp16 (2^-11); for fp16 queries the rounding error is a second operand, so that only O's own
+//     rounding is left.  P^T comes out of the S^T accumulators by movmatrix.
+//     Range: P step_V is kept below 2^9 by a running exponent E of the steps met so far, which is part of the
+//     reference of the exponentials just as the running maximum is: P = 2^(S - m - E + 8).
 //
 // Work split: the 64-slot blocks of all (sequence, key/value head, group of 8 NT query rows) form one list;
 // each CTA takes an equal run of it, whatever the lengths of the sequences, found on the device
 // from lens.  A head that lies inside one CTA's run is finished there; one that is cut leaves a
 // partial (unnormalised O, m, l) per CTA in the workspace, at most two per CTA, and
-// decode_kv4_merge joins them in the CTAs' order.  Inside a CTA each warp takes every NW-th block
-// through a ring of its own, filled by one bulk copy per block.
+// decode_kv4_merge joins them in the CTAs' order.  Inside a CTA each team of warps takes every TEAMS-th
+// block through a ring of its own, filled by one bulk copy per block.
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cstdint>
@@ -51,11 +55,12 @@ struct Kv4Cfg {
   static constexpr int ROWS = 8 * NT;     // query rows of a CTA
   static constexpr int GROUPS = D / 64;   // parameter groups of a row
   static constexpr int BLOCK = kv4_block_bytes(D);
-  static constexpr int NW = 8;            // warps
-  static constexpr int TEAM = D == 256 ? 2 : 1;  // warps that share a block
+  // 16 warps where 128 registers a thread hold a row tile's accumulators, else 8
+  static constexpr int NW = NT == 1 && D <= 128 ? 16 : 8;
+  static constexpr int TEAM = D == 256 || (D == 128 && NW == 16) ? 2 : 1;  // warps that share a block
   static constexpr int TEAMS = NW / TEAM;
   static constexpr int TOK = 64 / TEAM;   // tokens of a block for one warp
-  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr int STAGES = D == 64 && NW == 8 ? 4 : 2;
   static constexpr int THREADS = NW * 32;
   static constexpr int OSTRIDE = 64 + 4;  // floats of a row in the exchange buffer
   static constexpr int OFF_RING = 0;
@@ -68,20 +73,25 @@ struct Kv4Cfg {
   static_assert(BLOCK % 16 == 0 && OFF_O % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 };
 
-template <bool BF16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
-        "%2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the first product of a sum
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+      "%10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // 8x8 matrix of 16-bit elements transposed across the warp
@@ -91,31 +101,31 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   return r;
 }
 
-// code - 8 of nibbles n and n + 4 of w (n = 0..3), as a pair of 16-bit numbers
-template <bool BF16>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int n) {
-  const uint32_t bits = (w >> (4 * n)) & 0x000F000Fu;
-  if constexpr (BF16) {
-    const uint32_t u = bits | 0x43004300u;  // 128 + code
-    const uint32_t bias = 0x43084308u;      // 136
-    const __nv_bfloat162 r =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&bias));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    const uint32_t u = bits | 0x64006400u;  // 1024 + code
-    const uint32_t bias = 0x64086408u;      // 1032
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&bias));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// Constants of code_pairs, read through volatile moves so that they stay in registers: as immediates each
+// mask-and-or becomes two instructions (an instruction has room for one immediate).
+struct CodeConsts {
+  uint32_t magic, bias, sixteenth, bias16;
+  __device__ __forceinline__ CodeConsts() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));      // 1024
+    asm volatile("mov.b32 %0, 0xE408E408;" : "=r"(bias));       // -1032
+    asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(sixteenth));  // 1/16
+    asm volatile("mov.b32 %0, 0xD480D480;" : "=r"(bias16));     // -72
   }
-}
+};
 
-// the two tokens' channel n + 4 * hi of words a, b as v_hat pairs: x holds the 16-bit halves of
-// both words side by side
-__device__ __forceinline__ uint32_t value_pair(uint32_t x, int n, uint32_t step2, uint32_t mid2) {
-  const uint32_t c = code_pair<false>(x, n);
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&c), *reinterpret_cast<const __half2*>(&step2),
-                            *reinterpret_cast<const __half2*>(&mid2));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// The four nibbles of each half of x as four pairs of fp16, code - 8 (exact): 1024 + c - 1032, and
+// (1024 + 16 c) / 16 - 72
+__device__ __forceinline__ void code_pairs(uint32_t x, const CodeConsts& k, uint32_t (&out)[4]) {
+  const uint32_t y = x >> 8;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(out[0]) : "r"(x), "r"(k.magic));
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(out[1]) : "r"(x), "r"(k.magic));
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(out[2]) : "r"(y), "r"(k.magic));
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(out[3]) : "r"(y), "r"(k.magic));
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(out[i]) : "r"(k.bias));
+    asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(out[i + 1]) : "r"(k.sixteenth), "r"(k.bias16));
+  }
 }
 
 __device__ __forceinline__ int clamp_len(int n, int capacity) { return min(max(n, 0), capacity); }
@@ -232,22 +242,32 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
   uint8_t* ring = smem + C::OFF_RING + team * C::STAGES * C::BLOCK;
   Cursor ahead = wl.find(u0);
   Cursor here = ahead;
-  int64_t next_load = u0 + team;  // list position of the next block to load
+  const int run = (int)(u1 - u0);
+  int next_load = team;  // position in the run of the next block to load
   int loads = 0, uses = 0;
   const bool loader = half == 0 && lane == 0;
   bool ok = true;
+  const uint8_t* load_src = nullptr;  // the block loaded last, and how many blocks of its segment follow it
+  int load_left = 0;
   auto load_next = [&]() {
-    if (next_load < u1 && ok) {
-      if (C::TEAM > 1 && loader && loads >= C::STAGES)
-        ok = mbar_wait(empty + loads % C::STAGES, (uint32_t)(loads / C::STAGES - 1) & 1, ctx, kSiteKv4Empty);
-      if (loader && ok) {
-        const Place p = wl.at(ahead, next_load);
-        const int hk = p.hr / row_groups;
-        const uint8_t* src =
-            a.cache + (((int64_t)p.b * a.hkv + hk) * (a.capacity / kKv4Block) + p.blk) * C::BLOCK;
+    if (next_load < run && ok) {
+      if (loader) {
         const int s = loads % C::STAGES;
-        mbar_arrive_expect_tx(full + s, C::BLOCK);
-        bulk_load(ring + s * C::BLOCK, src, C::BLOCK, full + s);
+        if (C::TEAM > 1 && loads >= C::STAGES)
+          ok = mbar_wait(empty + s, (uint32_t)(loads / C::STAGES - 1) & 1, ctx, kSiteKv4Empty);
+        if (load_left >= C::TEAMS) {
+          load_src += C::TEAMS * C::BLOCK;
+          load_left -= C::TEAMS;
+        } else {
+          const Place p = wl.at(ahead, u0 + next_load);
+          const int hk = p.hr / row_groups;
+          load_src = a.cache + (((int64_t)p.b * a.hkv + hk) * (a.capacity / kKv4Block) + p.blk) * C::BLOCK;
+          load_left = p.nb - 1 - p.blk;
+        }
+        if (ok) {
+          mbar_arrive_expect_tx(full + s, C::BLOCK);
+          bulk_load(ring + s * C::BLOCK, load_src, C::BLOCK, full + s);
+        }
       }
       loads += ok;
     }
@@ -255,10 +275,13 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
   };
   for (int s = 0; s < C::STAGES; ++s) load_next();
 
-  float o_acc[D / 16][NT][4];
-  float m_run[NT][2], l_run[NT][2];
+  float o_acc[D / 16][NT][4];  // tile 4 gr + i: channels 64 gr + 8 g + 2 i (+ 1), rows 2t (+ 1)
+  float m_run[NT][2], l_run[NT][2], corr[C::GROUPS][NT][2];
+  int e_run;  // exponent of the largest V step so far
   uint32_t qf[D / 16][NT][2];
-  float qsum[C::GROUPS][NT][2];
+  float qsum[C::GROUPS][NT][2], cf[NT][2];
+  const CodeConsts kc;
+  const int kap = (g >> 1) + (g & 1) * 4;  // token of operand row g: rows 2t, 2t + 1 are tokens t, t + 4
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* obuf = reinterpret_cast<float*>(smem + C::OFF_O);
 
@@ -276,19 +299,44 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
       const int row = nt * 8 + g;
       const bool there = row0 + row < R;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (q_row0 + row) * D);
+      uint4 raw[D / 32];
+      float top = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 32; ++ks) {
+        // channels (ks / 2) * 64 + t * 16 + (ks % 2) * 8 .. + 8
+        raw[ks] = there ? src[(ks / 2) * 8 + t * 2 + (ks % 2)] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {raw[ks].x, raw[ks].y, raw[ks].z, raw[ks].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = unpack2<BF16>(w[i]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // scaled by 2^(14 - ex), the row's largest element lies in [2^14, 2^15)
+      const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
+      const float up = __uint_as_float((uint32_t)(141 - ex) << 23);
+      const float factor = __uint_as_float((uint32_t)(113 + ex) << 23) * scale_log2;
+      cf[nt][0] = __shfl_sync(0xffffffffu, factor, (2 * t) * 4);
+      cf[nt][1] = __shfl_sync(0xffffffffu, factor, (2 * t + 1) * 4);
 #pragma unroll
       for (int gr = 0; gr < C::GROUPS; ++gr) {
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          // channels gr * 64 + t * 16 + j * 8 .. + 8
-          const uint4 u = there ? src[gr * 8 + t * 2 + j] : make_uint4(0u, 0u, 0u, 0u);
-          qf[gr * 4 + j * 2][nt][0] = __byte_perm(u.x, u.z, 0x5410);      // channels 0, 4
-          qf[gr * 4 + j * 2][nt][1] = __byte_perm(u.x, u.z, 0x7632);      // 1, 5
-          qf[gr * 4 + j * 2 + 1][nt][0] = __byte_perm(u.y, u.w, 0x5410);  // 2, 6
-          qf[gr * 4 + j * 2 + 1][nt][1] = __byte_perm(u.y, u.w, 0x7632);  // 3, 7
-          const float2 f0 = unpack2<BF16>(u.x), f1 = unpack2<BF16>(u.y), f2 = unpack2<BF16>(u.z), f3 = unpack2<BF16>(u.w);
-          sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+          const int ks = gr * 2 + j;
+          float2 f[4] = {unpack2<BF16>(raw[ks].x), unpack2<BF16>(raw[ks].y), unpack2<BF16>(raw[ks].z),
+                         unpack2<BF16>(raw[ks].w)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[i] = fmul2(f[i], make_float2(up, up));
+            sum += f[i].x + f[i].y;
+          }
+          qf[ks * 2][nt][0] = pack2<false>(f[0].x, f[2].x);      // channels 0, 4 of the eight
+          qf[ks * 2][nt][1] = pack2<false>(f[0].y, f[2].y);      // 1, 5
+          qf[ks * 2 + 1][nt][0] = pack2<false>(f[1].x, f[3].x);  // 2, 6
+          qf[ks * 2 + 1][nt][1] = pack2<false>(f[1].y, f[3].y);  // 3, 7
         }
         // sum over the group's channels (the four t) of row g, then for this lane's rows 2t, 2t + 1
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -306,7 +354,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         last[nt][e] = a.causal ? sp.len - a.nq + row % a.nq + 1 : sp.len;
         m_run[nt][e] = -INFINITY;
         l_run[nt][e] = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt][e] = 0.f;
       }
+    e_run = -15;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -315,14 +366,15 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         for (int e = 0; e < 4; ++e) o_acc[i][nt][e] = 0.f;
 
     // this team's blocks of the segment: list positions u0 + team + uses * TEAMS while < mine_end
-    for (int64_t u = u0 + team + (int64_t)uses * C::TEAMS; ok && u < mine_end; u += C::TEAMS) {
-      const int blk = (int)(u - sp.seg);
+    const int to_blk = (int)(u0 - sp.seg);  // block of the segment at the run's start (may lie before the segment)
+    const int run_end = (int)(mine_end - u0);
+    for (int u = team + uses * C::TEAMS; ok && u < run_end; u += C::TEAMS) {
+      const int blk = u + to_blk;
       const int s = uses % C::STAGES;
       ok = __all_sync(0xffffffffu, mbar_wait(full + s, (uint32_t)(uses / C::STAGES) & 1, ctx, kSiteKv4Full));
       if (!ok) break;
       ++uses;
       uint8_t* blkp = ring + s * C::BLOCK;
-      const int slot0 = blk * kKv4Block + half * C::TOK;
       // not every slot of this block is inside every row's range
       const bool edge = blk * kKv4Block + kKv4Block > sp.len - (a.causal ? a.nq - 1 : 0);
       if (edge) {
@@ -334,6 +386,33 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         }
         __syncwarp();
       }
+      const uint32_t* kpar = reinterpret_cast<const uint32_t*>(blkp + kv4_params_at(D, 0));
+      const uint32_t* vpar = reinterpret_cast<const uint32_t*>(blkp + kv4_params_at(D, 1));
+      {
+        // the largest V step of this warp's tokens (fp16 bits of numbers >= 0 order like the numbers)
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < C::TOK * C::GROUPS / 32; ++i)
+          top = max(top, vpar[half * C::TOK * C::GROUPS + i * 32 + lane] & 0x7FFFu);
+        const int e_blk = (int)(__reduce_max_sync(0xffffffffu, top) >> 10) - 15;
+        if (e_blk > e_run) {
+          const float down = __uint_as_float((uint32_t)(127 + e_run - e_blk) << 23);
+          e_run = e_blk;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              l_run[nt][e] *= down;
+#pragma unroll
+              for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt][e] *= down;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o_acc[i][nt][e] *= down;
+          }
+        }
+      }
 #pragma unroll 1
       for (int step = 0; step < C::TOK / 32; ++step) {
         const int tok0 = half * C::TOK + step * 32;  // first of this step's 32 tokens in the block
@@ -341,152 +420,150 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         float sc[2][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const int ta = tok0 + mt * 16 + g;  // this lane's tokens: ta and ta + 8
+          const int ta = tok0 + mt * 16 + kap;  // this lane's tokens: ta and ta + 8
           const uint8_t* ka = blkp + kv4_codes_at(D, 0) + ta * (D / 2) + t * 8;
-          const uint32_t* pa = reinterpret_cast<const uint32_t*>(blkp + kv4_params_at(D, 0)) + ta * C::GROUPS;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
 #pragma unroll
           for (int gr = 0; gr < C::GROUPS; ++gr) {
             const uint2 wa = *reinterpret_cast<const uint2*>(ka + gr * 32);
             const uint2 wb = *reinterpret_cast<const uint2*>(ka + gr * 32 + 8 * (D / 2));
             float acc[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t xa = j ? wa.y : wa.x, xb = j ? wb.y : wb.x;
+              uint32_t xa[4], xb[4];
+              code_pairs(j ? wa.y : wa.x, kc, xa);
+              code_pairs(j ? wb.y : wb.x, kc, xb);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t af[4] = {code_pair<BF16>(xa, 2 * k), code_pair<BF16>(xb, 2 * k),
-                                        code_pair<BF16>(xa, 2 * k + 1), code_pair<BF16>(xb, 2 * k + 1)};
+                const uint32_t af[4] = {xa[2 * k], xb[2 * k], xa[2 * k + 1], xb[2 * k + 1]};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma16816<BF16>(acc[nt], af, qf[gr * 4 + j * 2 + k][nt][0], qf[gr * 4 + j * 2 + k][nt][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (j == 0 && k == 0)
+                    mma_f16_first(acc[nt], af, qf[gr * 4][nt][0], qf[gr * 4][nt][1]);
+                  else
+                    mma_f16(acc[nt], af, qf[gr * 4 + j * 2 + k][nt][0], qf[gr * 4 + j * 2 + k][nt][1]);
+                }
               }
             }
-            const float2 p0 = unpack2<false>(pa[gr]), p1 = unpack2<false>(pa[8 * C::GROUPS + gr]);
+            const float2 p0 = unpack2<false>(kpar[ta * C::GROUPS + gr]);
+            const float2 p1 = unpack2<false>(kpar[(ta + 8) * C::GROUPS + gr]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              sc[mt][nt][0] += fmaf(p0.x, acc[nt][0], p0.y * qsum[gr][nt][0]);
-              sc[mt][nt][1] += fmaf(p0.x, acc[nt][1], p0.y * qsum[gr][nt][1]);
-              sc[mt][nt][2] += fmaf(p1.x, acc[nt][2], p1.y * qsum[gr][nt][0]);
-              sc[mt][nt][3] += fmaf(p1.x, acc[nt][3], p1.y * qsum[gr][nt][1]);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                sc[mt][nt][e] = fmaf(e < 2 ? p0.x : p1.x, acc[nt][e],
+                                     gr == 0 ? (e < 2 ? p0.y : p1.y) * qsum[0][nt][e & 1]
+                                             : fmaf(e < 2 ? p0.y : p1.y, qsum[gr][nt][e & 1], sc[mt][nt][e]));
           }
         }
-        // ---- log2 units, mask, running maximum
-        uint32_t pf[2][NT][2];
+        // ---- log2 units, mask, running maximum, exponentials
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x = sc[mt][nt][e] * scale_log2;
-              if (edge) {
-                const int slot = blk * kKv4Block + tok0 + mt * 16 + g + (e >> 1) * 8;
-                if (slot >= last[nt][e & 1]) x = -INFINITY;
-              }
-              sc[mt][nt][e] = x;
-              mx[e & 1] = fmaxf(mx[e & 1], x);
-            }
+            for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= cf[nt][e & 1];
+          if (edge) {
+            asm volatile("");  // a branch, not eight selections for every block
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (blk * kKv4Block + tok0 + mt * 16 + kap + (e >> 1) * 8 >= last[nt][e & 1])
+                  sc[mt][nt][e] = -INFINITY;
+          }
           if constexpr (SCORES) {
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int row = nt * 8 + 2 * t + (e & 1);
-                const int slot = blk * kKv4Block + tok0 + mt * 16 + g + (e >> 1) * 8;
+                const int slot = blk * kKv4Block + tok0 + mt * 16 + kap + (e >> 1) * 8;
                 if (row0 + row < R) scores[(q_row0 + row) * a.capacity + slot] = sc[mt][nt][e];
               }
           }
+          float mx[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            mx[e] = fmaxf(max3(sc[0][nt][e], sc[0][nt][e + 2], sc[1][nt][e]), sc[1][nt][e + 2]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
             mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
           }
-          float off[2];
-          bool grow = false;
-          float alpha[2];
+          if (__any_sync(0xffffffffu, mx[0] > m_run[nt][0] || mx[1] > m_run[nt][1])) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mn = fmaxf(m_run[nt][e], mx[e]);
-            alpha[e] = mn == -INFINITY ? 1.f : ex2(m_run[nt][e] - mn);
-            grow |= mn > m_run[nt][e];
-            m_run[nt][e] = mn;
-            off[e] = mn == -INFINITY ? 0.f : kPShift - mn;
+            for (int e = 0; e < 2; ++e) {
+              const float mn = fmaxf(m_run[nt][e], mx[e]);
+              const float alpha = mn == -INFINITY ? 1.f : ex2(m_run[nt][e] - mn);
+              m_run[nt][e] = mn;
+              l_run[nt][e] *= alpha;
+#pragma unroll
+              for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt][e] *= alpha;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o_acc[i][nt][e] *= alpha;
+                o_acc[i][nt][e + 2] *= alpha;
+              }
+            }
           }
-          if (__any_sync(0xffffffffu, grow)) {
+          const float off[2] = {m_run[nt][0] == -INFINITY ? 0.f : kPShift - (float)e_run - m_run[nt][0],
+                                m_run[nt][1] == -INFINITY ? 0.f : kPShift - (float)e_run - m_run[nt][1]};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) l_run[nt][e] *= alpha[e];
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o_acc[i][nt][e] *= alpha[e & 1];
-          }
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            float p[4];
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              p[e] = ex2(sc[mt][nt][e] + off[e & 1]);
-              l_run[nt][e & 1] += p[e];
+              sc[mt][nt][e] = ex2(sc[mt][nt][e] + off[e & 1]);
+              l_run[nt][e & 1] += sc[mt][nt][e];
             }
-            pf[mt][nt][0] = movmatrix(pack2<false>(p[0], p[1]));
-            pf[mt][nt][1] = movmatrix(pack2<false>(p[2], p[3]));
-          }
         }
         // ---- O^T += V^T P^T
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const int ta = tok0 + mt * 16 + 2 * t;  // tokens ta, ta + 1, ta + 8, ta + 9
-          constexpr int VW = D / 64;              // code words of a lane's D / 8 channels
-          const uint8_t* vb = blkp + kv4_codes_at(D, 1) + ta * (D / 2) + g * (D / 16);
-          const uint32_t* pv = reinterpret_cast<const uint32_t*>(blkp + kv4_params_at(D, 1)) + ta * C::GROUPS +
-                               (g * C::GROUPS) / 8;
-          const uint32_t w0 = pv[0], w1 = pv[C::GROUPS], w2 = pv[8 * C::GROUPS], w3 = pv[9 * C::GROUPS];
-          const uint32_t s_lo = __byte_perm(w0, w1, 0x5410), m_lo = __byte_perm(w0, w1, 0x7632);
-          const uint32_t s_hi = __byte_perm(w2, w3, 0x5410), m_hi = __byte_perm(w2, w3, 0x7632);
-          uint32_t c[4][VW];
+          const int ta = tok0 + mt * 16 + kap;
+          const uint8_t* vb = blkp + kv4_codes_at(D, 1) + (tok0 + mt * 16 + t) * (D / 2) + g * 4;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint8_t* src = vb + ((q & 1) + (q >> 1) * 8) * (D / 2);
-            if constexpr (VW == 1) {
-              c[q][0] = *reinterpret_cast<const uint32_t*>(src);
-            } else if constexpr (VW == 2) {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              c[q][0] = v.x;
-              c[q][1] = v.y;
-            } else {
-              const uint4 v = *reinterpret_cast<const uint4*>(src);
-              c[q][0] = v.x;
-              c[q][1] = v.y;
-              c[q][2] = v.z;
-              c[q][3] = v.w;
-            }
-          }
+          for (int gr = 0; gr < C::GROUPS; ++gr) {
+            // tokens t, t + 4, t + 8, t + 12: operand columns 2t, 2t + 1, 2t + 8, 2t + 9
+            uint32_t c[4];
 #pragma unroll
-          for (int w = 0; w < VW; ++w)
+            for (int q = 0; q < 4; ++q) c[q] = *reinterpret_cast<const uint32_t*>(vb + q * 4 * (D / 2) + gr * 32);
+            const float2 p0 = unpack2<false>(vpar[ta * C::GROUPS + gr]);
+            const float2 p1 = unpack2<false>(vpar[(ta + 8) * C::GROUPS + gr]);
+            uint32_t pf[NT][2], pl[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float x0 = sc[mt][nt][2 * e], x1 = sc[mt][nt][2 * e + 1];
+                const float st = e ? p1.x : p0.x, md = e ? p1.y : p0.y;
+                corr[gr][nt][0] = fmaf(x0, md, corr[gr][nt][0]);
+                corr[gr][nt][1] = fmaf(x1, md, corr[gr][nt][1]);
+                const float y0 = x0 * st, y1 = x1 * st;
+                const uint32_t h = pack2<false>(y0, y1);
+                pf[nt][e] = movmatrix(h);
+                if constexpr (!BF16) {
+                  const float2 back = unpack2<false>(h);
+                  pl[nt][e] = movmatrix(pack2<false>(y0 - back.x, y1 - back.y));
+                }
+              }
 #pragma unroll
             for (int hi = 0; hi < 2; ++hi) {
               const uint32_t sel = hi ? 0x7632u : 0x5410u;
-              const uint32_t x_lo = __byte_perm(c[0][w], c[1][w], sel), x_hi = __byte_perm(c[2][w], c[3][w], sel);
+              uint32_t lo4[4], hi4[4];
+              code_pairs(__byte_perm(c[0], c[1], sel), kc, lo4);
+              code_pairs(__byte_perm(c[2], c[3], sel), kc, hi4);
 #pragma unroll
-              for (int n = 0; n < 4; n += 2) {
-                // operand rows g, g + 8: this lane's channels 8 w + 4 hi + n and + 1
-                const uint32_t af[4] = {value_pair(x_lo, n, s_lo, m_lo), value_pair(x_lo, n + 1, s_lo, m_lo),
-                                        value_pair(x_hi, n, s_hi, m_hi), value_pair(x_hi, n + 1, s_hi, m_hi)};
+              for (int k = 0; k < 2; ++k) {
+                // operand rows g, g + 8: channels 64 gr + 8 g + 4 hi + 2 k and + 1
+                const uint32_t af[4] = {lo4[2 * k], lo4[2 * k + 1], hi4[2 * k], hi4[2 * k + 1]};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma16816<false>(o_acc[w * 4 + hi * 2 + n / 2][nt], af, pf[mt][nt][0], pf[mt][nt][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_f16(o_acc[gr * 4 + hi * 2 + k][nt], af, pf[nt][0], pf[nt][1]);
+                  if constexpr (!BF16) mma_f16(o_acc[gr * 4 + hi * 2 + k][nt], af, pl[nt][0], pl[nt][1]);
+                }
               }
             }
+          }
         }
       }
       // the block is read: its slot takes the team's next one
@@ -504,6 +581,18 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         float l = l_run[nt][e];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+        for (int gr = 0; gr < C::GROUPS; ++gr) {
+          float c = corr[gr][nt][e];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o_acc[gr * 4 + i][nt][e] += c;
+            o_acc[gr * 4 + i][nt][e + 2] += c;
+          }
+        }
+        m_run[nt][e] += (float)e_run;  // the reference of this warp's exponentials
         if (g == 0) {
           ml[(warp * C::ROWS + nt * 8 + 2 * t + e) * 2] = m_run[nt][e];
           ml[(warp * C::ROWS + nt * 8 + 2 * t + e) * 2 + 1] = l;
@@ -534,14 +623,13 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
                 make_float2(o_acc[i][nt][e] * f[nt][e], o_acc[i][nt][2 + e] * f[nt][e]);
       }
       __syncthreads();
-      // columns: lane group g of the mma holds channels g * D / 8 + cc * 8 .. + 8
       for (int i = threadIdx.x; i < C::ROWS * 32; i += C::THREADS) {
         const int row = i / 32, c2 = i % 32;  // channel pair
         float2 v = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < C::NW; ++w)
           v = fadd2(v, *reinterpret_cast<const float2*>(obuf + (w * C::ROWS + row) * C::OSTRIDE + c2 * 2));
-        const int ch = (c2 / 4) * (D / 8) + cc * 8 + (c2 % 4) * 2;
+        const int ch = cc * 64 + c2 * 2;
         if (row0 + row < R) {
           float M = -INFINITY, l = 0.f;
           for (int w = 0; w < C::NW; ++w) M = fmaxf(M, ml[(w * C::ROWS + row) * 2]);
@@ -652,7 +740,9 @@ __global__ void __launch_bounds__(256) decode_kv4_weights(const DecodeKv4Args a,
   a.w_out[i] = (a.w_in ? a.w_in[i] : 0.f) + w;
 }
 
-int row_tiles(int h, int hkv, int nq) { return ((h / hkv) * nq > 8) ? 2 : 1; }
+// Groups of 8 query rows that a CTA takes together: two when there are more than 8 rows, so that the cache is
+// read once for 16; d = 256 has no registers for two (768 bytes of spills).
+int row_tiles(int h, int hkv, int nq, int d) { return ((h / hkv) * nq > 8 && d < 256) ? 2 : 1; }
 
 // CTAs of the decode kernel: one per SM, no more than there can be blocks
 int grid_size(int b, int hkv, int row_groups, int capacity) {
@@ -685,14 +775,15 @@ cudaError_t launch_nt(const DecodeKv4Args& a) {
 template <int D>
 cudaError_t launch_d(const DecodeKv4Args& a) {
   const bool bf = a.dtype == DT_BF16;
-  if (row_tiles(a.h, a.hkv, a.nq) == 1) return bf ? launch_nt<D, true, 1>(a) : launch_nt<D, false, 1>(a);
-  return bf ? launch_nt<D, true, 2>(a) : launch_nt<D, false, 2>(a);
+  if (row_tiles(a.h, a.hkv, a.nq, D) == 1) return bf ? launch_nt<D, true, 1>(a) : launch_nt<D, false, 1>(a);
+  if constexpr (D < 256) return bf ? launch_nt<D, true, 2>(a) : launch_nt<D, false, 2>(a);
+  return cudaErrorNotSupported;
 }
 
 }  // namespace
 
 size_t decode_kv4_workspace_bytes(int b, int h, int hkv, int nq, int capacity, int d, bool weights) {
-  const int rows = 8 * row_tiles(h, hkv, nq);
+  const int rows = 8 * row_tiles(h, hkv, nq, d);
   const int R = (h / hkv) * nq;
   const int row_groups = (R + rows - 1) / rows;
   size_t n = (size_t)grid_size(b, hkv, row_groups, capacity) * 2 * partial_floats(rows, d);
