@@ -32,7 +32,7 @@
 // each CTA takes an equal run of it, whatever the lengths of the sequences, found on the device
 // from lens.  A head that lies inside one CTA's run is finished there; one that is cut leaves a
 // partial (unnormalised O, m, l) per CTA in the workspace, at most two per CTA, and
-// decode_kv4_merge joins them in the CTAs' order.  Inside a CTA each team of warps takes every TEAMS-th
+// decode_kv4_finish joins them in the CTAs' order.  Inside a CTA each team of warps takes every TEAMS-th
 // block through a ring of its own, filled by one bulk copy per block.
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -65,7 +65,7 @@ struct Kv4Cfg {
   static constexpr int OSTRIDE = 64 + 4;  // floats of a row in the exchange buffer
   static constexpr int OFF_RING = 0;
   static constexpr int OFF_O = TEAMS * STAGES * BLOCK;                // [NW][ROWS][OSTRIDE] fp32
-  static constexpr int OFF_ML = OFF_O + NW * ROWS * OSTRIDE * 4;      // [NW][ROWS][2] fp32
+  static constexpr int OFF_ML = OFF_O + (NW * ROWS * OSTRIDE + NW * ROWS + ROWS * 2) * 4;  // [NW][ROWS][2] fp32
   static constexpr int OFF_BAR = OFF_ML + NW * ROWS * 2 * 4;
   static constexpr int NBAR = 2 * TEAMS * STAGES;  // full, then empty
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
@@ -131,28 +131,34 @@ __device__ __forceinline__ void code_pairs(uint32_t x, const CodeConsts& k, uint
 __device__ __forceinline__ int clamp_len(int n, int capacity) { return min(max(n, 0), capacity); }
 __device__ __forceinline__ int blocks_of(int n) { return (n + kKv4Block - 1) / kKv4Block; }
 
-// Position in the list of blocks, which runs over sequences, then heads x row groups, then blocks.
+// The list: sequences, then their heads x row groups (segments), then the segment's nb blocks, each a
+// position, behind kSegCost positions that stand for what a segment costs whatever its length (its queries, joining
+// the warps, its output: about the time of that many blocks).
+constexpr int kSegCost = 8;
+
 struct Cursor {
-  int64_t first;  // list position of sequence b's first block
+  int64_t first;  // list position of sequence b's first segment
   int b, nb, len;
 };
 struct Place {
-  int b, hr, blk, nb, len;  // hr: key/value head * row groups + row group
-  int64_t seg;              // list position of the segment's (b, hr) first block
+  int b, hr, nb, len;  // hr: key/value head * row groups + row group
+  int64_t seg;         // list position of the segment
 };
 
 struct WorkList {
   const int32_t* lens;
   int B, HR, capacity;
+  __device__ __forceinline__ static int positions(int nb) { return nb > 0 ? nb + kSegCost : 0; }
+  __device__ __forceinline__ int blocks(int b) const { return blocks_of(clamp_len(lens[b], capacity)); }
   __device__ __forceinline__ void enter(Cursor& c, int b) const {
     c.b = b;
     c.len = b < B ? clamp_len(lens[b], capacity) : 0;
     c.nb = blocks_of(c.len);
   }
-  // total number of blocks; the whole warp takes part
-  __device__ __forceinline__ int64_t total() const {
+  // positions of sequences [0, end); the whole warp takes part
+  __device__ __forceinline__ int64_t total(int end) const {
     int64_t t = 0;
-    for (int b = threadIdx.x & 31; b < B; b += 32) t += blocks_of(clamp_len(lens[b], capacity));
+    for (int b = threadIdx.x & 31; b < end; b += 32) t += positions(blocks(b));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return t * HR;
@@ -162,7 +168,7 @@ struct WorkList {
     const int lane = threadIdx.x & 31;
     int64_t first = 0;
     for (int base = 0; base < B; base += 32) {
-      const int n = base + lane < B ? blocks_of(clamp_len(lens[base + lane], capacity)) : 0;
+      const int n = base + lane < B ? positions(blocks(base + lane)) : 0;
       int64_t incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -184,20 +190,21 @@ struct WorkList {
     enter(c, B);
     return c;
   }
-  // place of list position u >= c.first (inside the list), moving the cursor along
+  // segment of list position u >= c.first (inside the list), moving the cursor along
   __device__ __forceinline__ Place at(Cursor& c, int64_t u) const {
-    while (u >= c.first + (int64_t)c.nb * HR && c.b < B) {
-      c.first += (int64_t)c.nb * HR;
+    int64_t span = (int64_t)positions(c.nb) * HR;
+    while (u >= c.first + span && c.b < B) {
+      c.first += span;
       enter(c, c.b + 1);
+      span = (int64_t)positions(c.nb) * HR;
     }
     Place p;
     p.b = c.b;
     p.nb = c.nb;
     p.len = c.len;
-    const int rel = (int)(u - c.first);
-    p.hr = rel / max(c.nb, 1);
-    p.blk = rel - p.hr * c.nb;
-    p.seg = u - p.blk;
+    const int per = max(positions(c.nb), 1);
+    p.hr = (int)(u - c.first) / per;
+    p.seg = c.first + (int64_t)p.hr * per;
     return p;
   }
 };
@@ -205,10 +212,23 @@ struct WorkList {
 // The list is cut into one run per CTA, none of them empty (CTAs beyond the list's length have none).
 __device__ __forceinline__ int runs_of(int64_t total, int ctas) { return total < ctas ? (int)total : ctas; }
 __device__ __forceinline__ int64_t run_start(int64_t total, int g, int G) { return total * g / G; }
+// CTA whose run holds list position u: the largest g with total * g / G <= u
+__device__ __forceinline__ int run_of(int64_t total, int64_t u, int G) { return (int)(((u + 1) * G - 1) / total); }
+// blocks [first, end) of a segment that lie in the run [u0, u1)
+__device__ __forceinline__ void run_blocks(int64_t seg, int nb, int64_t u0, int64_t u1, int* first, int* end) {
+  const int64_t at = seg + kSegCost;
+  *first = (int)max((int64_t)0, min((int64_t)nb, u0 - at));
+  *end = (int)max((int64_t)*first, min((int64_t)nb, u1 - at));
+}
 
 // Partials of the merge: per CTA two slots (0: a segment that began in an earlier CTA's run, 1: one that began
 // in this CTA's run and goes on), [ROWS][D] unnormalised O and [ROWS][2] (m, l).
 __host__ __device__ __forceinline__ size_t partial_floats(int rows, int d) { return (size_t)rows * (d + 2); }
+
+// Log-sum-exp in log2 units of a row's (reference, sum): -inf where it saw nothing, NaN where it saw one
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l > 0.f ? m - kPShift + log2f(l) : (isnan(l) ? l : -INFINITY);
+}
 
 template <int D, bool BF16, int NT, bool SCORES>
 __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
@@ -230,48 +250,58 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
   }
   __syncthreads();
 
+  asm volatile("griddepcontrol.launch_dependents;");
   const WorkList wl{a.lens, a.b, a.hkv * row_groups, a.capacity};
-  const int64_t total = wl.total();
+  const int64_t total = wl.total(a.b);
   const int G = runs_of(total, gridDim.x);
   if ((int)blockIdx.x >= G) return;
   const int64_t u0 = run_start(total, blockIdx.x, G), u1 = run_start(total, blockIdx.x + 1, G);
   const int R = (a.h / a.hkv) * a.nq;  // query rows of a key/value head
   const float scale_log2 = a.scale * kLog2e;
 
-  // ring of this warp's team: its i-th block is list position u0 + team + i * TEAMS, in slot i % STAGES
+  // Blocks go to the teams in turn: of a segment's blocks [first, end) in this run, team (rot + i) % TEAMS takes
+  // first + i, where rot counts the run's blocks before.  A team's i-th block of the run is in slot i % STAGES.
   uint8_t* ring = smem + C::OFF_RING + team * C::STAGES * C::BLOCK;
   Cursor ahead = wl.find(u0);
   Cursor here = ahead;
-  const int run = (int)(u1 - u0);
-  int next_load = team;  // position in the run of the next block to load
   int loads = 0, uses = 0;
   const bool loader = half == 0 && lane == 0;
   bool ok = true;
-  const uint8_t* load_src = nullptr;  // the block loaded last, and how many blocks of its segment follow it
+  int64_t load_u = u0;  // list position of the segment to load from next
+  int load_rot = 0;
+  bool load_ok = true;  // (when a wait of the loader runs out, the teams' waits for their blocks run out too)
+  const uint8_t* load_src = nullptr;  // the block loaded last, and how many blocks of its segment's part follow it
   int load_left = 0;
   auto load_next = [&]() {
-    if (next_load < run && ok) {
-      if (loader) {
-        const int s = loads % C::STAGES;
-        if (C::TEAM > 1 && loads >= C::STAGES)
-          ok = mbar_wait(empty + s, (uint32_t)(loads / C::STAGES - 1) & 1, ctx, kSiteKv4Empty);
-        if (load_left >= C::TEAMS) {
-          load_src += C::TEAMS * C::BLOCK;
-          load_left -= C::TEAMS;
-        } else {
-          const Place p = wl.at(ahead, u0 + next_load);
+    if (!loader || !load_ok) return;
+    if (load_left >= C::TEAMS) {
+      load_src += C::TEAMS * C::BLOCK;
+      load_left -= C::TEAMS;
+    } else {
+      load_left = -1;
+      while (load_left < 0 && load_u < u1) {
+        const Place p = wl.at(ahead, load_u);
+        int first, end;
+        run_blocks(p.seg, p.nb, u0, u1, &first, &end);
+        load_u = p.seg + WorkList::positions(p.nb);
+        const int mine = first + ((team - load_rot) & (C::TEAMS - 1));
+        load_rot += end - first;
+        if (mine < end) {
           const int hk = p.hr / row_groups;
-          load_src = a.cache + (((int64_t)p.b * a.hkv + hk) * (a.capacity / kKv4Block) + p.blk) * C::BLOCK;
-          load_left = p.nb - 1 - p.blk;
-        }
-        if (ok) {
-          mbar_arrive_expect_tx(full + s, C::BLOCK);
-          bulk_load(ring + s * C::BLOCK, load_src, C::BLOCK, full + s);
+          load_src = a.cache + (((int64_t)p.b * a.hkv + hk) * (a.capacity / kKv4Block) + mine) * C::BLOCK;
+          load_left = end - 1 - mine;
         }
       }
-      loads += ok;
+      if (load_left < 0) return;  // nothing left in the run
     }
-    next_load += C::TEAMS;
+    const int s = loads % C::STAGES;
+    if (C::TEAM > 1 && loads >= C::STAGES)
+      load_ok = mbar_wait(empty + s, (uint32_t)(loads / C::STAGES - 1) & 1, ctx, kSiteKv4Empty);
+    if (load_ok) {
+      mbar_arrive_expect_tx(full + s, C::BLOCK);
+      bulk_load(ring + s * C::BLOCK, load_src, C::BLOCK, full + s);
+      ++loads;
+    }
   };
   for (int s = 0; s < C::STAGES; ++s) load_next();
 
@@ -285,11 +315,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* obuf = reinterpret_cast<float*>(smem + C::OFF_O);
 
+  int rot = 0;
   for (int64_t seg_u = u0; seg_u < u1;) {
     // the segment (sequence, head, row group) at seg_u, as far as this CTA's run goes
     const Place sp = wl.at(here, seg_u);
-    const int64_t seg_end = sp.seg + sp.nb;
-    const int64_t mine_end = seg_end < u1 ? seg_end : u1;
+    seg_u = sp.seg + WorkList::positions(sp.nb);
+    int blk0, blk1;
+    run_blocks(sp.seg, sp.nb, u0, u1, &blk0, &blk1);
+    if (blk0 >= blk1) continue;
     const int hk = sp.hr / row_groups, rg = sp.hr - hk * row_groups;
     const int row0 = rg * C::ROWS;  // first query row of the group among the R
     // Q rows of this group: rows row0 .. row0 + ROWS of the key/value head, zero past R
@@ -365,11 +398,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o_acc[i][nt][e] = 0.f;
 
-    // this team's blocks of the segment: list positions u0 + team + uses * TEAMS while < mine_end
-    const int to_blk = (int)(u0 - sp.seg);  // block of the segment at the run's start (may lie before the segment)
-    const int run_end = (int)(mine_end - u0);
-    for (int u = team + uses * C::TEAMS; ok && u < run_end; u += C::TEAMS) {
-      const int blk = u + to_blk;
+    for (int blk = blk0 + ((team - rot) & (C::TEAMS - 1)); ok && blk < blk1; blk += C::TEAMS) {
       const int s = uses % C::STAGES;
       ok = __all_sync(0xffffffffu, mbar_wait(full + s, (uint32_t)(uses / C::STAGES) & 1, ctx, kSiteKv4Full));
       if (!ok) break;
@@ -593,34 +622,47 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
           }
         }
         m_run[nt][e] += (float)e_run;  // the reference of this warp's exponentials
-        if (g == 0) {
-          ml[(warp * C::ROWS + nt * 8 + 2 * t + e) * 2] = m_run[nt][e];
-          ml[(warp * C::ROWS + nt * 8 + 2 * t + e) * 2 + 1] = l;
-        }
+        if (g == 0)
+          *reinterpret_cast<float2*>(ml + (warp * C::ROWS + nt * 8 + 2 * t + e) * 2) = make_float2(m_run[nt][e], l);
       }
+    // (a warp whose team had none of these blocks has m = -inf, l = 0 and is left out of the sums of O)
+    const int nblk = blk1 - blk0;
+    auto active = [&](int w) { return ((w / C::TEAM - rot) & (C::TEAMS - 1)) < nblk; };
     __syncthreads();
-    float f[NT][2];
+    float* fac = obuf + C::NW * C::ROWS * C::OSTRIDE;  // [NW][ROWS] weight of each warp's sums, then [ROWS][2] (m, l)
+    float* mlt = fac + C::NW * C::ROWS;
+    if (threadIdx.x < C::NW * C::ROWS) {
+      const int row = threadIdx.x % C::ROWS, w = threadIdx.x / C::ROWS;
+      float M = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float M = -INFINITY;
-        for (int w = 0; w < C::NW; ++w) M = fmaxf(M, ml[(w * C::ROWS + nt * 8 + 2 * t + e) * 2]);
-        f[nt][e] = m_run[nt][e] == -INFINITY ? 1.f : ex2(m_run[nt][e] - M);
+      for (int i = 0; i < C::NW; ++i) M = fmaxf(M, ml[(i * C::ROWS + row) * 2]);
+      // (a row whose scores were all NaN has no maximum, but its sums are NaN)
+      const float m = ml[threadIdx.x / C::ROWS * C::ROWS * 2 + row * 2];
+      fac[w * C::ROWS + row] = m == -INFINITY ? 1.f : ex2(m - M);
+      if (w == 0) {
+        float l = 0.f;
+        for (int i = 0; i < C::NW; ++i) {
+          const float2 v = *reinterpret_cast<const float2*>(ml + (i * C::ROWS + row) * 2);
+          l += v.y * (v.x == -INFINITY ? 1.f : ex2(v.x - M));
+        }
+        *reinterpret_cast<float2*>(mlt + row * 2) = make_float2(M, l);
       }
-    const bool whole = sp.seg >= u0 && seg_end <= u1;
-    float* slot = part + ((size_t)blockIdx.x * 2 + (sp.seg >= u0 ? 1 : 0)) * partial_floats(C::ROWS, D);
+    }
+    const bool whole = nblk == sp.nb;
+    float* slot = part + ((size_t)blockIdx.x * 2 + (blk0 == 0 ? 1 : 0)) * partial_floats(C::ROWS, D);
 #pragma unroll 1
     for (int cc = 0; cc < D / 64; ++cc) {
+      if (active(warp)) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        if (i / 4 != cc) continue;
+        for (int i = 0; i < D / 16; ++i) {
+          if (i / 4 != cc) continue;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float2*>(obuf + (warp * C::ROWS + nt * 8 + 2 * t + e) * C::OSTRIDE + g * 8 + (i % 4) * 2) =
-                make_float2(o_acc[i][nt][e] * f[nt][e], o_acc[i][nt][2 + e] * f[nt][e]);
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<float2*>(obuf + (warp * C::ROWS + nt * 8 + 2 * t + e) * C::OSTRIDE + g * 8 +
+                                         (i % 4) * 2) = make_float2(o_acc[i][nt][e], o_acc[i][nt][2 + e]);
+        }
       }
       __syncthreads();
       for (int i = threadIdx.x; i < C::ROWS * 32; i += C::THREADS) {
@@ -628,32 +670,29 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         float2 v = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < C::NW; ++w)
-          v = fadd2(v, *reinterpret_cast<const float2*>(obuf + (w * C::ROWS + row) * C::OSTRIDE + c2 * 2));
+          if (active(w)) {
+            const float f = fac[w * C::ROWS + row];
+            const float2 x = *reinterpret_cast<const float2*>(obuf + (w * C::ROWS + row) * C::OSTRIDE + c2 * 2);
+            v.x = fmaf(x.x, f, v.x);
+            v.y = fmaf(x.y, f, v.y);
+          }
         const int ch = cc * 64 + c2 * 2;
         if (row0 + row < R) {
-          float M = -INFINITY, l = 0.f;
-          for (int w = 0; w < C::NW; ++w) M = fmaxf(M, ml[(w * C::ROWS + row) * 2]);
-          for (int w = 0; w < C::NW; ++w) {
-            const float mw = ml[(w * C::ROWS + row) * 2];
-            // (a row whose scores were all NaN has no maximum, but its sum is NaN)
-            l += ml[(w * C::ROWS + row) * 2 + 1] * (mw == -INFINITY ? 1.f : ex2(mw - M));
-          }
+          const float2 st = *reinterpret_cast<const float2*>(mlt + row * 2);
           if (whole) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = st.y > 0.f ? 1.f / st.y : 0.f;
             reinterpret_cast<uint32_t*>(a.o)[((q_row0 + row) * D + ch) / 2] = pack2<BF16>(v.x * inv, v.y * inv);
-            if (cc == 0 && c2 == 0)
-              a.lse[q_row0 + row] = l > 0.f ? (M - kPShift + log2f(l)) * kLn2 : (isnan(l) ? l : -INFINITY);
+            if (cc == 0 && c2 == 0) a.lse[q_row0 + row] = log_sum(st.x, st.y) * kLn2;
           } else {
             *reinterpret_cast<float2*>(slot + row * D + ch) = v;
-            if (cc == 0 && c2 == 0)
-              *reinterpret_cast<float2*>(slot + C::ROWS * D + row * 2) = make_float2(M, l);
+            if (cc == 0 && c2 == 0) *reinterpret_cast<float2*>(slot + C::ROWS * D + row * 2) = st;
           }
         }
       }
       __syncthreads();
     }
+    rot += nblk;
     if (*abort_flag) break;
-    seg_u = mine_end;
   }
   // every copy must land before the CTA may exit
   if (loader) {
@@ -665,79 +704,142 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
   }
 }
 
-// Joins the partials of the segments that the runs of several CTAs cut, in the order of the CTAs, and
-// writes the rows of empty sequences.  One block per (sequence, key/value head, row group).
+// Where a segment's partials are: those of CTAs g0 .. g1 (g0 == g1: finished by that CTA)
+template <int D, int ROWS>
+struct Partials {
+  const float* part;
+  int g0, g1;
+  __device__ __forceinline__ const float* of(int g) const {
+    return part + ((size_t)g * 2 + (g == g0 ? 1 : 0)) * partial_floats(ROWS, D);
+  }
+};
+
+constexpr int kFinishThreads = 256;
+constexpr int kMaxRuns = 512;  // CTAs of the decode kernel, at most (one per SM)
+
+// What is left when the runs are done.  Blocks [0, segments): the segments that several CTAs' runs cut
+// are joined from their partials, in the order of the CTAs, and the rows of empty sequences are
+// written.  Further blocks, when weights are asked for, kFinishThreads slots of a head each: weights_out =
+// weights_in + sum over the head's rows of 2^(S - L log2e).
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(128) decode_kv4_merge(const DecodeKv4Args a, const float* __restrict__ part,
-                                                       int row_groups, int ctas) {
+__global__ void __launch_bounds__(kFinishThreads)
+    decode_kv4_finish(const DecodeKv4Args a, const float* __restrict__ part, const float* __restrict__ scores,
+                      int row_groups, int ctas) {
   constexpr int ROWS = 8 * NT;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int hr_count = a.hkv * row_groups;
-  const int b = blockIdx.x / hr_count, hr = blockIdx.x - b * hr_count;
-  const int hk = hr / row_groups, rg = hr - hk * row_groups;
+  const int segments = a.b * hr_count;
   const int R = (a.h / a.hkv) * a.nq;
-  const int rows = min(ROWS, R - rg * ROWS);
-  const int64_t row0 = ((int64_t)b * a.hkv + hk) * R + rg * ROWS;
-  if (hr == 0 && threadIdx.x == 0 && clamp_len(a.lens[b], a.capacity) != a.lens[b])
-    report_error(a.err, DERR_BAD_ARG, kSiteKv4Len);
-  const int nb = blocks_of(clamp_len(a.lens[b], a.capacity));
-  if (nb == 0) {
-    for (int i = threadIdx.x; i < rows * D / 2; i += blockDim.x) reinterpret_cast<uint32_t*>(a.o)[row0 * D / 2 + i] = 0u;
-    for (int i = threadIdx.x; i < rows; i += blockDim.x) a.lse[row0 + i] = -INFINITY;
+  const WorkList wl{a.lens, a.b, hr_count, a.capacity};
+  const int64_t total = wl.total(a.b);
+  const int G = runs_of(total, ctas);
+  __shared__ float fac[ROWS][kMaxRuns];
+  __shared__ float2 stat[ROWS];
+  auto partials = [&](int64_t before, int nb, int hr) {
+    const int64_t first = before + (int64_t)hr * WorkList::positions(nb) + kSegCost;
+    return Partials<D, ROWS>{part, run_of(total, first, G), run_of(total, first + nb - 1, G)};
+  };
+  if ((int)blockIdx.x < segments) {
+    const int b = blockIdx.x / hr_count, hr = blockIdx.x - b * hr_count;
+    const int hk = hr / row_groups, rg = hr - hk * row_groups;
+    const int rows = min(ROWS, R - rg * ROWS);
+    const int64_t row0 = ((int64_t)b * a.hkv + hk) * R + rg * ROWS;
+    if (hr == 0 && threadIdx.x == 0 && clamp_len(a.lens[b], a.capacity) != a.lens[b])
+      report_error(a.err, DERR_BAD_ARG, kSiteKv4Len);
+    const int nb = wl.blocks(b);
+    if (nb == 0) {
+      for (int i = threadIdx.x; i < rows * D / 2; i += kFinishThreads)
+        reinterpret_cast<uint32_t*>(a.o)[row0 * D / 2 + i] = 0u;
+      for (int i = threadIdx.x; i < rows; i += kFinishThreads) a.lse[row0 + i] = -INFINITY;
+      return;
+    }
+    const Partials<D, ROWS> P = partials(wl.total(b), nb, hr);
+    if (P.g0 == P.g1) return;
+    const int n = P.g1 - P.g0 + 1;
+    // each row's reference and sum, and each partial's weight: one warp a row
+    for (int row = threadIdx.x >> 5; row < rows; row += kFinishThreads / 32) {
+      const int lane = threadIdx.x & 31;
+      float M = -INFINITY;
+      for (int j = lane; j < n; j += 32) M = fmaxf(M, P.of(P.g0 + j)[ROWS * D + row * 2]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      float l = 0.f;
+      for (int j = lane; j < n; j += 32) {
+        const float2 v = *reinterpret_cast<const float2*>(P.of(P.g0 + j) + ROWS * D + row * 2);
+        const float f = v.x == -INFINITY ? 1.f : ex2(v.x - M);  // (no maximum: nothing seen, or only NaN)
+        fac[row][j] = f;
+        l = fmaf(v.y, f, l);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) {
+        stat[row] = make_float2(M, l);
+        a.lse[row0 + row] = log_sum(M, l) * kLn2;
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kFinishThreads) {
+      const int row = i / (D / 4), c = i - row * (D / 4);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float f = fac[row][j];
+        const float4 x = *reinterpret_cast<const float4*>(P.of(P.g0 + j) + row * D + c * 4);
+        o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
+      }
+      const float l = stat[row].y, inv = l > 0.f ? 1.f / l : 0.f;
+      reinterpret_cast<uint2*>(a.o)[((row0 + row) * D + c * 4) / 4] =
+          make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+    }
     return;
   }
-  const WorkList wl{a.lens, a.b, hr_count, a.capacity};
-  const int64_t total = wl.total();
-  const int G = runs_of(total, ctas);
-  int64_t before = 0;
-  for (int i = threadIdx.x & 31; i < b; i += 32) before += blocks_of(clamp_len(a.lens[i], a.capacity));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  const int64_t s0 = before * hr_count + (int64_t)hr * nb, s1 = s0 + nb;
-  // CTA whose run holds list position u: the largest g with total * g / G <= u
-  const int g0 = (int)(((s0 + 1) * G - 1) / total), g1 = (int)((s1 * G - 1) / total);
-  if (g0 == g1) return;  // finished by that CTA
-  const size_t stride = 2 * partial_floats(ROWS, D);
-  const float* first = part + g0 * stride + partial_floats(ROWS, D);
-  const float* rest = part + (size_t)(g0 + 1) * stride;
-  const int n = g1 - g0;
-  for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
-    const int row = i / (D / 4), c = i - row * (D / 4);
-    auto mlp = [&](int j) {
-      return *reinterpret_cast<const float2*>((j ? rest + (j - 1) * stride : first) + ROWS * D + row * 2);
-    };
-    float M = -INFINITY;
-    for (int j = 0; j <= n; ++j) M = fmaxf(M, mlp(j).x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j <= n; ++j) {
-      const float2 v = mlp(j);
-      const float f = v.x == -INFINITY ? 1.f : ex2(v.x - M);  // (no maximum: nothing seen, or only NaN)
-      l += v.y * f;
-      const float4 x = *reinterpret_cast<const float4*>((j ? rest + (j - 1) * stride : first) + row * D + c * 4);
-      o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    reinterpret_cast<uint2*>(a.o)[((row0 + row) * D + c * 4) / 4] =
-        make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
-    if (c == 0) a.lse[row0 + row] = l > 0.f ? (M - kPShift + log2f(l)) * kLn2 : (isnan(l) ? l : -INFINITY);
-  }
-}
-
-// weights_out = weights_in + sum over the head's rows of 2^(S - L log2e), for the sequence's slots
-__global__ void __launch_bounds__(256) decode_kv4_weights(const DecodeKv4Args a, const float* __restrict__ scores) {
-  const int tiles = (a.capacity + 255) / 256;
-  const int bh = blockIdx.x / tiles, b = bh / a.hkv;
-  const int slot = (blockIdx.x - bh * tiles) * 256 + threadIdx.x;
-  if (slot >= clamp_len(a.lens[b], a.capacity)) return;
-  const int R = (a.h / a.hkv) * a.nq;
-  const float* s = scores + (int64_t)bh * R * a.capacity + slot;
+  // ---- weights
+  const int tiles = (a.capacity + kFinishThreads - 1) / kFinishThreads;
+  const int wb = (int)blockIdx.x - segments;
+  const int bh = wb / tiles, b = bh / a.hkv, hk = bh - b * a.hkv;
+  const int slot0 = (wb - bh * tiles) * kFinishThreads, slot = slot0 + threadIdx.x;
+  const int len = clamp_len(a.lens[b], a.capacity);
+  if (slot0 >= len) return;
+  const int nb = blocks_of(len);
+  const int64_t before = wl.total(b);
+  const int64_t at = (int64_t)bh * a.capacity + slot;
   float w = 0.f;
-  for (int r = 0; r < R; ++r) {
-    const float L = a.lse[(int64_t)bh * R + r];
-    if (L != -INFINITY) w += ex2(s[(int64_t)r * a.capacity] - L * kLog2e);
+  const float w_in = a.w_in && slot < len ? a.w_in[at] : 0.f;
+  const float* s = scores + (int64_t)bh * R * a.capacity + slot;
+  for (int rg = 0; rg < row_groups; ++rg) {
+    // the group's log-sum-exps, from the partials where several CTAs have them (O's block writes L only now)
+    const Partials<D, ROWS> P = partials(before, nb, hk * row_groups + rg);
+    const int rows = min(ROWS, R - rg * ROWS);
+    __syncthreads();
+    for (int row = threadIdx.x >> 5; row < rows; row += kFinishThreads / 32) {
+      const int lane = threadIdx.x & 31;
+      float L;
+      if (P.g0 == P.g1) {
+        L = a.lse[(int64_t)bh * R + rg * ROWS + row] * kLog2e;
+      } else {
+        float M = -INFINITY, l = 0.f;
+        for (int j = P.g0 + lane; j <= P.g1; j += 32) M = fmaxf(M, P.of(j)[ROWS * D + row * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int j = P.g0 + lane; j <= P.g1; j += 32) {
+          const float2 v = *reinterpret_cast<const float2*>(P.of(j) + ROWS * D + row * 2);
+          l = fmaf(v.y, v.x == -INFINITY ? 1.f : ex2(v.x - M), l);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        L = log_sum(M, l);
+      }
+      if (lane == 0) stat[row].x = L;
+    }
+    __syncthreads();
+    if (slot < len)
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) {
+        const float L = stat[r].x;
+        if (L != -INFINITY) w += ex2(s[(int64_t)(rg * ROWS + r) * a.capacity] - L);
+      }
   }
-  const int64_t i = (int64_t)bh * a.capacity + slot;
-  a.w_out[i] = (a.w_in ? a.w_in[i] : 0.f) + w;
+  if (slot < len) a.w_out[at] = w_in + w;
 }
 
 // Groups of 8 query rows that a CTA takes together: two when there are more than 8 rows, so that the cache is
@@ -747,7 +849,7 @@ int row_tiles(int h, int hkv, int nq, int d) { return ((h / hkv) * nq > 8 && d <
 // CTAs of the decode kernel: one per SM, no more than there can be blocks
 int grid_size(int b, int hkv, int row_groups, int capacity) {
   const int64_t most = (int64_t)b * hkv * row_groups * (capacity / kKv4Block);
-  return (int)std::min<int64_t>(most, device_sm_count());
+  return (int)std::min<int64_t>(most, std::min(device_sm_count(), kMaxRuns));
 }
 
 template <int D, bool BF16, int NT>
@@ -763,13 +865,19 @@ cudaError_t launch_nt(const DecodeKv4Args& a) {
   if (e != cudaSuccess) return e;
   kern<<<G, C::THREADS, C::SMEM, a.stream>>>(a, part, scores, row_groups);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  decode_kv4_merge<D, BF16, NT><<<a.b * a.hkv * row_groups, 128, 0, a.stream>>>(a, part, row_groups, G);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.w_out) {
-    decode_kv4_weights<<<(unsigned)((a.capacity + 255) / 256) * a.b * a.hkv, 256, 0, a.stream>>>(a, scores);
-    e = cudaGetLastError();
-  }
-  return e;
+  // launched while the runs are still going (it waits for them before it reads anything)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.b * a.hkv * row_groups));
+  if (a.w_out) cfg.gridDim.x += (unsigned)((a.capacity + kFinishThreads - 1) / kFinishThreads) * a.b * a.hkv;
+  cfg.blockDim = dim3(kFinishThreads);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_kv4_finish<D, BF16, NT>, a, (const float*)part, (const float*)scores,
+                            row_groups, G);
 }
 
 template <int D>
