@@ -48,6 +48,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 8.f;  // P is kept as 2^(S - m + 8)
+constexpr float kRaise = 4.f;   // the reference m is raised when it is this far (log2) below the maximum
+constexpr float kNoScore = 1e30f;  // off before the first score: 2^(-inf + 1e30) is still 0
 constexpr uint32_t kSiteKv4Full = 930, kSiteKv4Drain = 931, kSiteKv4Empty = 932, kSiteKv4Len = 933;
 
 template <int D, int NT>
@@ -87,6 +89,16 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
       "%10, %10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// (a.x b.x + c.x, a.y b.y + c.y)
+__device__ __forceinline__ float2 ffma2v(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -306,10 +318,11 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
   for (int s = 0; s < C::STAGES; ++s) load_next();
 
   float o_acc[D / 16][NT][4];  // tile 4 gr + i: channels 64 gr + 8 g + 2 i (+ 1), rows 2t (+ 1)
-  float m_run[NT][2], l_run[NT][2], corr[C::GROUPS][NT][2];
+  // pairs: rows 2t, 2t + 1.  P = 2^(S + off), off = 8 - m - E for the m and E in use
+  float2 off[NT], l_run[NT], corr[C::GROUPS][NT];
   int e_run;  // exponent of the largest V step so far
   uint32_t qf[D / 16][NT][2];
-  float qsum[C::GROUPS][NT][2], cf[NT][2];
+  float2 qsum[C::GROUPS][NT], cf[NT];
   const CodeConsts kc;
   const int kap = (g >> 1) + (g & 1) * 4;  // token of operand row g: rows 2t, 2t + 1 are tokens t, t + 4
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
@@ -351,8 +364,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
       const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
       const float up = __uint_as_float((uint32_t)(141 - ex) << 23);
       const float factor = __uint_as_float((uint32_t)(113 + ex) << 23) * scale_log2;
-      cf[nt][0] = __shfl_sync(0xffffffffu, factor, (2 * t) * 4);
-      cf[nt][1] = __shfl_sync(0xffffffffu, factor, (2 * t + 1) * 4);
+      cf[nt] = make_float2(__shfl_sync(0xffffffffu, factor, (2 * t) * 4),
+                           __shfl_sync(0xffffffffu, factor, (2 * t + 1) * 4));
 #pragma unroll
       for (int gr = 0; gr < C::GROUPS; ++gr) {
         float sum = 0.f;
@@ -374,8 +387,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         // sum over the group's channels (the four t) of row g, then for this lane's rows 2t, 2t + 1
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qsum[gr][nt][0] = __shfl_sync(0xffffffffu, sum, (2 * t) * 4);
-        qsum[gr][nt][1] = __shfl_sync(0xffffffffu, sum, (2 * t + 1) * 4);
+        qsum[gr][nt] = make_float2(__shfl_sync(0xffffffffu, sum, (2 * t) * 4),
+                                   __shfl_sync(0xffffffffu, sum, (2 * t + 1) * 4));
       }
     }
     int last[NT][2];  // one past the newest slot that rows 2t, 2t + 1 see
@@ -385,12 +398,15 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
       for (int e = 0; e < 2; ++e) {
         const int row = row0 + nt * 8 + 2 * t + e;
         last[nt][e] = a.causal ? sp.len - a.nq + row % a.nq + 1 : sp.len;
-        m_run[nt][e] = -INFINITY;
-        l_run[nt][e] = 0.f;
-#pragma unroll
-        for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt][e] = 0.f;
       }
     e_run = -15;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      off[nt] = make_float2(kNoScore, kNoScore);
+      l_run[nt] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt] = make_float2(0.f, 0.f);
+    }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -426,15 +442,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         const int e_blk = (int)(__reduce_max_sync(0xffffffffu, top) >> 10) - 15;
         if (e_blk > e_run) {
           const float down = __uint_as_float((uint32_t)(127 + e_run - e_blk) << 23);
+          const float drop = (float)(e_run - e_blk);
           e_run = e_blk;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
+            off[nt] = fadd2(off[nt], make_float2(drop, drop));
+            l_run[nt] = fmul2(l_run[nt], make_float2(down, down));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              l_run[nt][e] *= down;
-#pragma unroll
-              for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt][e] *= down;
-            }
+            for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt] = fmul2(corr[gr][nt], make_float2(down, down));
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
       for (int step = 0; step < C::TOK / 32; ++step) {
         const int tok0 = half * C::TOK + step * 32;  // first of this step's 32 tokens in the block
         // ---- S^T of 2 x 16 tokens
-        float sc[2][NT][4];
+        float2 sc[2][NT][2];  // [token tile][row tile][token of this lane, the one 8 behind], rows 2t, 2t + 1
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           const int ta = tok0 + mt * 16 + kap;  // this lane's tokens: ta and ta + 8
@@ -478,71 +493,71 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                sc[mt][nt][e] = fmaf(e < 2 ? p0.x : p1.x, acc[nt][e],
-                                     gr == 0 ? (e < 2 ? p0.y : p1.y) * qsum[0][nt][e & 1]
-                                             : fmaf(e < 2 ? p0.y : p1.y, qsum[gr][nt][e & 1], sc[mt][nt][e]));
+              for (int e = 0; e < 2; ++e) {
+                const float st = e ? p1.x : p0.x, md = e ? p1.y : p0.y;
+                const float2 mid = gr == 0 ? fmul2(qsum[0][nt], make_float2(md, md)) : ffma2(qsum[gr][nt], md, sc[mt][nt][e]);
+                sc[mt][nt][e] = ffma2(make_float2(acc[nt][2 * e], acc[nt][2 * e + 1]), st, mid);
+              }
           }
         }
-        // ---- log2 units, mask, running maximum, exponentials
+        // ---- mask, running maximum (log2 units), exponentials
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= cf[nt][e & 1];
           if (edge) {
             asm volatile("");  // a branch, not eight selections for every block
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (blk * kKv4Block + tok0 + mt * 16 + kap + (e >> 1) * 8 >= last[nt][e & 1])
-                  sc[mt][nt][e] = -INFINITY;
+              for (int e = 0; e < 2; ++e) {
+                const int slot = blk * kKv4Block + tok0 + mt * 16 + kap + e * 8;
+                if (slot >= last[nt][0]) sc[mt][nt][e].x = -INFINITY;
+                if (slot >= last[nt][1]) sc[mt][nt][e].y = -INFINITY;
+              }
           }
           if constexpr (SCORES) {
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int row = nt * 8 + 2 * t + (e & 1);
-                const int slot = blk * kKv4Block + tok0 + mt * 16 + kap + (e >> 1) * 8;
-                if (row0 + row < R) scores[(q_row0 + row) * a.capacity + slot] = sc[mt][nt][e];
+              for (int e = 0; e < 2; ++e) {
+                const int row = nt * 8 + 2 * t;
+                float* dst = scores + (q_row0 + row) * a.capacity + blk * kKv4Block + tok0 + mt * 16 + kap + e * 8;
+                if (row0 + row < R) dst[0] = sc[mt][nt][e].x * cf[nt].x;
+                if (row0 + row + 1 < R) dst[a.capacity] = sc[mt][nt][e].y * cf[nt].y;
               }
           }
-          float mx[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            mx[e] = fmaxf(max3(sc[0][nt][e], sc[0][nt][e + 2], sc[1][nt][e]), sc[1][nt][e + 2]);
+          float2 mx = make_float2(fmaxf(max3(sc[0][nt][0].x, sc[0][nt][1].x, sc[1][nt][0].x), sc[1][nt][1].x),
+                                  fmaxf(max3(sc[0][nt][0].y, sc[0][nt][1].y, sc[1][nt][0].y), sc[1][nt][1].y));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+            mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+            mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
           }
-          if (__any_sync(0xffffffffu, mx[0] > m_run[nt][0] || mx[1] > m_run[nt][1])) {
+          // the reference follows the maximum only when it has fallen kRaise behind it (P <= 2^(8 + kRaise - E))
+          const float2 z = ffma2v(mx, cf[nt], off[nt]);
+          const float top = kPShift - (float)e_run;
+          if (__any_sync(0xffffffffu, fmaxf(z.x, z.y) > top + kRaise)) {
+            mx = fmul2(mx, cf[nt]);
+            const float2 next = make_float2(fminf(off[nt].x, top - mx.x), fminf(off[nt].y, top - mx.y));
+            const float2 alpha = make_float2(ex2(next.x - off[nt].x), ex2(next.y - off[nt].y));
+            off[nt] = next;
+            l_run[nt] = fmul2(l_run[nt], alpha);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float mn = fmaxf(m_run[nt][e], mx[e]);
-              const float alpha = mn == -INFINITY ? 1.f : ex2(m_run[nt][e] - mn);
-              m_run[nt][e] = mn;
-              l_run[nt][e] *= alpha;
+            for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt] = fmul2(corr[gr][nt], alpha);
 #pragma unroll
-              for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt][e] *= alpha;
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                o_acc[i][nt][e] *= alpha;
-                o_acc[i][nt][e + 2] *= alpha;
-              }
+            for (int i = 0; i < D / 16; ++i) {
+              o_acc[i][nt][0] *= alpha.x;
+              o_acc[i][nt][1] *= alpha.y;
+              o_acc[i][nt][2] *= alpha.x;
+              o_acc[i][nt][3] *= alpha.y;
             }
           }
-          const float off[2] = {m_run[nt][0] == -INFINITY ? 0.f : kPShift - (float)e_run - m_run[nt][0],
-                                m_run[nt][1] == -INFINITY ? 0.f : kPShift - (float)e_run - m_run[nt][1]};
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              sc[mt][nt][e] = ex2(sc[mt][nt][e] + off[e & 1]);
-              l_run[nt][e & 1] += sc[mt][nt][e];
+            for (int e = 0; e < 2; ++e) {
+              const float2 x = ffma2v(sc[mt][nt][e], cf[nt], off[nt]);
+              sc[mt][nt][e] = make_float2(ex2(x.x), ex2(x.y));
+              l_run[nt] = fadd2(l_run[nt], sc[mt][nt][e]);
             }
         }
         // ---- O^T += V^T P^T
@@ -563,16 +578,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float x0 = sc[mt][nt][2 * e], x1 = sc[mt][nt][2 * e + 1];
                 const float st = e ? p1.x : p0.x, md = e ? p1.y : p0.y;
-                corr[gr][nt][0] = fmaf(x0, md, corr[gr][nt][0]);
-                corr[gr][nt][1] = fmaf(x1, md, corr[gr][nt][1]);
-                const float y0 = x0 * st, y1 = x1 * st;
-                const uint32_t h = pack2<false>(y0, y1);
+                corr[gr][nt] = ffma2(sc[mt][nt][e], md, corr[gr][nt]);
+                const float2 y = fmul2(sc[mt][nt][e], make_float2(st, st));
+                const uint32_t h = pack2<false>(y.x, y.y);
                 pf[nt][e] = movmatrix(h);
                 if constexpr (!BF16) {
                   const float2 back = unpack2<false>(h);
-                  pl[nt][e] = movmatrix(pack2<false>(y0 - back.x, y1 - back.y));
+                  pl[nt][e] = movmatrix(pack2<false>(y.x - back.x, y.y - back.y));
                 }
               }
 #pragma unroll
@@ -607,12 +620,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float l = l_run[nt][e];
+        float l = e ? l_run[nt].y : l_run[nt].x;
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
         for (int gr = 0; gr < C::GROUPS; ++gr) {
-          float c = corr[gr][nt][e];
+          float c = e ? corr[gr][nt].y : corr[gr][nt].x;
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
 #pragma unroll
@@ -621,9 +634,10 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
             o_acc[gr * 4 + i][nt][e + 2] += c;
           }
         }
-        m_run[nt][e] += (float)e_run;  // the reference of this warp's exponentials
+        const float r = e ? off[nt].y : off[nt].x;
+        const float ref = r == kNoScore ? -INFINITY : kPShift - r;  // m + E of this warp's exponentials
         if (g == 0)
-          *reinterpret_cast<float2*>(ml + (warp * C::ROWS + nt * 8 + 2 * t + e) * 2) = make_float2(m_run[nt][e], l);
+          *reinterpret_cast<float2*>(ml + (warp * C::ROWS + nt * 8 + 2 * t + e) * 2) = make_float2(ref, l);
       }
     // (a warp whose team had none of these blocks has m = -inf, l = 0 and is left out of the sums of O)
     const int nblk = blk1 - blk0;
