@@ -26,7 +26,7 @@ __all__ = [
     "attention_forward", "attention_backward", "attention_decode",
     "attention_forward_fp8", "quantize_fp8", "EXPORTED_SYMBOLS", "NOALLOC_SCRATCH_BYTES",
     "fa_sm_clock_sample", "kv4_cache", "fa_kv4_append", "fa_kv4_read", "kv4_read", "fa_decode_kv4",
-    "fa_decode_kv4_workspace_size", "attention_decode_kv4", "fa_kv4_evict",
+    "fa_decode_kv4_workspace_size", "attention_decode_kv4", "fa_kv4_evict", "fa_fwd_varlen", "attention_forward_varlen",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,7 +42,7 @@ EXPORTED_SYMBOLS = (
     "fa_quantize_fp8", "fa_fwd_fp8", "fa_fwd_fp8_gqa", "fa_fwd_masked", "fa_bwd_masked",
     "fa_selftest_bounded_wait", "fa_fwd_bwd_host", "fa_fwd_bwd_host_workspace_size", "fa_sm_clock_sample",
     "fa_debug_build", "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4",
-    "fa_decode_kv4_workspace_size", "fa_kv4_evict",
+    "fa_decode_kv4_workspace_size", "fa_kv4_evict", "fa_fwd_varlen",
 )
 
 _lib = None
@@ -99,6 +99,7 @@ def load_library(path=None):
         lib.fa_fwd_bwd_host_workspace_size.restype = sz
         lib.fa_fwd_bwd_host.argtypes = [vp] * 10 + [sz, i, i, i, i, i, f, i, i, i, vp]
         i64 = ctypes.c_int64
+        lib.fa_fwd_varlen.argtypes = [vp] * 6 + [i] * 5 + [i64] * 8 + [f, i, i, vp]
         lib.fa_kv4_append.argtypes = [vp] * 6 + [i] * 5 + [i64] * 4 + [i, vp]
         lib.fa_kv4_read.argtypes = [vp] * 5 + [i] * 5 + [i64] * 4 + [i, vp]
         lib.fa_decode_kv4_workspace_size.argtypes = [i] * 7
@@ -122,7 +123,8 @@ def load_library(path=None):
                      "fa_bwd_noalloc", "fa_bwd_preprocess",
                      "fa_bwd_main", "fa_bwd_dq_convert",
                      "fa_check_device_error", "fa_tile_counter", "fa_uses_tensor_cores", "fa_sm_clock_sample",
-                     "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_kv4_evict"):
+                     "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_kv4_evict",
+                     "fa_fwd_varlen"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -438,6 +440,27 @@ def _int32(t, n, what):
         raise ValueError(f"{what} must be an int32 tensor of {n} elements")
 
 
+def fa_fwd_varlen(Q, K, V, O, L, cu_seqlens, scale, causal, stream=None):
+    """Forward over packed sequences: Q, O [T, H, d], K, V [T, Hkv, d] (rows of contiguous d, any
+    strides between them), L [H, T]; sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] (int32)."""
+    T, H, d, q_ts, q_hs = _packed(Q, "Q")
+    Tk, Hkv, dk, k_ts, k_hs = _packed(K, "K")
+    _, _, _, v_ts, v_hs = _packed(V, "V")
+    _, _, _, o_ts, o_hs = _packed(O, "O")
+    _on_device(L, cu_seqlens, strided=(Q, K, V, O))
+    if (Tk, dk) != (T, d) or Hkv < 1 or H % Hkv:
+        raise ValueError("K must be [T, Hkv, d] with H a multiple of Hkv")
+    if V.shape != K.shape or O.shape != Q.shape or not (Q.dtype == K.dtype == V.dtype == O.dtype):
+        raise ValueError("V must have K's shape, O must have Q's, and all four one dtype")
+    _rows(L, H * T)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be an int32 tensor of S + 1 elements")
+    _int32(cu_seqlens, cu_seqlens.numel(), "cu_seqlens")
+    _check(load_library().fa_fwd_varlen(_p(Q), _p(K), _p(V), _p(O), _p(L), _p(cu_seqlens), cu_seqlens.numel() - 1, T, H,
+                                        Hkv, d, q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, float(scale),
+                                        int(bool(causal)), _dt(Q), _stream(stream)))
+
+
 def _kv4_shape(cache):
     """(B, Hkv, capacity, d) of a 4-bit cache tensor (kv4_cache)."""
     if cache.dtype != torch.uint8 or cache.dim() != 4 or cache.shape[3] % 72:
@@ -637,6 +660,17 @@ def attention_decode(q, k, v, scale=None, splits=0, stream=None):
     nbytes = fa_decode_workspace_size(B, H, Hkv, Nq, Nk, d, splits)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     fa_decode(q, k, v, o, lse, scale, splits, ws, stream)
+    return o, lse
+
+
+def attention_forward_varlen(q, k, v, cu_seqlens, causal=False, scale=None, stream=None):
+    """O [T, H, d], L [H, T] = fa_fwd_varlen(...) for packed q [T, H, d], k, v [T, Hkv, d]."""
+    T, H, d, _, _ = _packed(q, "Q")
+    scale = d ** -0.5 if scale is None else scale
+    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    fa_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale, causal, stream)
+    _used_on(stream, o, lse)
     return o, lse
 
 

@@ -569,6 +569,38 @@ fa_status fa_fwd_fp8(const void* Q8, const void* K8, const void* V8, const float
                         stream);
 }
 
+fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* L, const int32_t* cu_seqlens, int S,
+                        int T, int H, int Hkv, int d, int64_t q_token_stride, int64_t q_head_stride,
+                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                        int64_t o_token_stride, int64_t o_head_stride, float scale, int causal, fa_dtype dtype,
+                        void* stream) {
+  if (dtype != FA_BF16 && dtype != FA_FP16)
+    return fail(FA_ERR_UNSUPPORTED, "fa_fwd_varlen takes bf16 or fp16, not dtype %d", (int)dtype);
+  if (S < 0 || T < 0 || H < 0) return fail(FA_ERR_INVALID_ARG, "negative size S=%d T=%d H=%d", S, T, H);
+  if (!fwd_tc_supported((int)dtype, d))
+    return fail(FA_ERR_UNSUPPORTED, "fa_fwd_varlen supports d in {64, 128, 256}, got %d", d);
+  if (S == 0 || T == 0 || H == 0) return FA_OK;
+  fa_status st = check_heads(H, Hkv);
+  if (st != FA_OK) return st;
+  if ((double)H * ((double)T / 128 + S) > 1.0e9 || T > INT32_MAX - 512)
+    return fail(FA_ERR_INVALID_ARG, "problem too large: S=%d T=%d H=%d", S, T, H);
+  if ((st = check_ptrs({Q, K, V, O}, "fa_fwd_varlen")) != FA_OK) return st;
+  if ((st = check_words({L, cu_seqlens}, "fa_fwd_varlen")) != FA_OK) return st;
+  if ((st = check_scale(scale)) != FA_OK) return st;
+  const int64_t strides[] = {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                             v_token_stride, v_head_stride, o_token_stride, o_head_stride};
+  for (int64_t v : strides) {
+    if ((st = check_strides({v}, 2, "fa_fwd_varlen")) != FA_OK) return st;
+    if (v < d) return fail(FA_ERR_INVALID_ARG, "fa_fwd_varlen: a stride of %lld elements < d=%d", (long long)v, d);
+  }
+  DeviceSyms syms;
+  if ((st = device_syms(&syms)) != FA_OK) return st;
+  VarlenFwdArgs a{Q, K, V, O, L, cu_seqlens, S, T, H, H / Hkv, d, q_token_stride, q_head_stride, k_token_stride,
+                  k_head_stride, v_token_stride, v_head_stride, o_token_stride, o_head_stride, scale, causal ? 1 : 0,
+                  (int)dtype, syms.err, syms.counter, static_cast<cudaStream_t>(stream)};
+  return launched(launch_fwd_varlen(a), "fa_fwd_varlen");
+}
+
 static fa_status kv4_rows(bool read, const void* K, const void* V, const int32_t* cu_seqlens, const int32_t* lens,
                           void* cache, float* weights, int B, int T, int Hkv, int capacity, int d,
                           int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,

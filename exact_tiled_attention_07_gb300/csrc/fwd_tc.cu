@@ -154,15 +154,32 @@ struct F8Scales {
   const float* v = nullptr;  // [bh / group][nb]
 };
 
-template <int D, bool BF16, bool MASKED, bool QUEUE, bool F8 = false>
+// Packed variant (VARLEN): sequences of different lengths packed one behind the other, Q, O
+// [n][H][D], K, V [n][Hkv][D] with n rows in all and their own token and head strides, L [H][n].
+// Sequence s is rows [cu[s], cu[s + 1]); a row sees keys of its own sequence only.  The lengths are
+// known on the device only: per head there is one item slot for each NQ x 128 rows of the packing plus one per
+// sequence, and sequence s starts at slot cu[s] / (NQ 128) + s, behind every slot that the sequences before it
+// can need.  The producer turns a slot into (sequence, query rows) by binary search, skips the slots
+// that hold nothing, and publishes the item in shared memory (also when the items come in static order).
+// Key and query tiles start at the sequence's own first row, so only its last tile is ragged: scores of
+// keys behind the end are masked as in the plain kernel, the V rows there (another sequence's) are
+// set to zero in shared memory before P V, since 0 x NaN is NaN, and O rows are stored one by one.
+struct VarlenSpec {
+  const int32_t* cu = nullptr;  // [seqs + 1]
+  int seqs = 0;
+  int64_t o_ts = 0, o_hs = 0;  // O's token and head strides, elements
+};
+
+template <int D, bool BF16, bool MASKED, bool QUEUE, bool F8 = false, bool VARLEN = false>
 __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, void* __restrict__ out, float* __restrict__ lse, int n,
                   int bh_count, int tiles_per_head, float scale_log2, int causal, int group, unsigned long long* err,
                   unsigned long long* counter, int window, const uint8_t* __restrict__ block_mask, int mask_heads,
-                  int heads, int snake, unsigned* __restrict__ sched, int hgroup, F8Scales f8s) {
+                  int heads, int snake, unsigned* __restrict__ sched, int hgroup, F8Scales f8s, VarlenSpec vl) {
   using C = FwdCfg<D, F8>;
   static_assert(!(F8 && MASKED), "the FP8 variant has no masks");
+  static_assert(!VARLEN || (QUEUE && !MASKED && !F8), "the packed variant publishes its items");
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -199,9 +216,38 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
   struct Item {
     int head, kvhead, qrow0;
     int nq[2];  // key tiles of each query tile
+    int base, n, nblk;  // first row of the sequence, its length and its key tiles
   };
+  // key tiles of each query tile of an item whose head, qrow0, n and nblk are set
+  auto count_tiles = [&](Item& w) {
+    w.kvhead = w.head / group;  // grouped-query attention: key/value head shared by `group` query heads
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int first = w.qrow0 + q * BM;
+      if (q >= C::NQ || first >= w.n) {
+        w.nq[q] = 0;
+      } else if (causal) {
+        w.nq[q] = min(w.nblk, (min(first + BM, w.n) - 1) / BN + 1);
+      } else {
+        w.nq[q] = w.nblk;
+      }
+    }
+  };
+  volatile int* vitem = reinterpret_cast<volatile int*>(smem + C::SMEM_STG);  // [2][4] published packed items
   auto item_of = [&](int item) {
     Item w;
+    if constexpr (VARLEN) {  // (item: the slot it was published in)
+      w.head = vitem[item * 4];
+      w.qrow0 = vitem[item * 4 + 1];
+      w.base = vitem[item * 4 + 2];
+      w.n = vitem[item * 4 + 3];
+      w.nblk = (w.n + BN - 1) / BN;
+      count_tiles(w);
+      return w;
+    }
+    w.base = 0;
+    w.n = n;
+    w.nblk = nblocks;
     int tile;
     if (causal) {
       int rank;
@@ -211,19 +257,8 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
       w.head = item / tiles_per_head;
       tile = item - w.head * tiles_per_head;
     }
-    w.kvhead = w.head / group;  // grouped-query attention: key/value head shared by `group` query heads
     w.qrow0 = tile * (C::NQ * BM);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int first = w.qrow0 + q * BM;
-      if (q >= C::NQ || first >= n) {
-        w.nq[q] = 0;
-      } else if (causal) {
-        w.nq[q] = min(nblocks, (min(first + BM, n) - 1) / BN + 1);
-      } else {
-        w.nq[q] = nblocks;
-      }
-    }
+    count_tiles(w);
     return w;
   };
   int* list_hdr = reinterpret_cast<int*>(smem + C::OFF_LIST);  // nq[0], nq[1], visible tiles of q 0, 1
@@ -329,6 +364,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     const int64_t item = (int64_t)r * g + ((snake && (r & 1)) ? (g - 1 - c) : c);
     return item < total_items ? (int)item : -1;
   };
+  Item packed{};  // (packed variant) the item that next_item read
   // this CTA's r-th item for a consumer warp: queue mode reads the producer's slot r % 2 (every
   // consumer warp reads every slot once; `good` turns false, and the item -1, when the bounded
   // wait ran out), otherwise the static order above
@@ -337,12 +373,16 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     const int t = r & 1;
     good = __all_sync(0xffffffffu, mbar_wait(B.item_full + t, (uint32_t)(r >> 1) & 1, ctx, 50)) && good;
     const int item = good ? item_slot[t] : -1;
+    if constexpr (VARLEN) {
+      if (item >= 0) packed = item_of(item);
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(B.item_empty + t);
     return item;
   };
   // the item with, for masked launches, the key-tile counts of its list
   auto item_at = [&](int item) {
+    if constexpr (VARLEN) return packed;
     Item w = item_of(item);
     if constexpr (MASKED) {
       w.nq[0] = list_hdr[0];
@@ -383,12 +423,50 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
       tma_prefetch_desc(&tm_v);
       uint32_t ring_pos = 0;  // ring loads issued so far (all items)
       int q_loads = 0;
+      [[maybe_unused]] unsigned static_turn = 0;
       bool ok = true;
       // the r-th item: queue mode draws a ticket (items are numbered heaviest first) and publishes
       // it, or -1 once the queue is empty, when every reader of the slot's previous item has it
       auto draw = [&](int r) {
         if constexpr (!queue) return nth_item(r);
         if (r >= 2 && !(ok = mbar_wait(B.item_empty + (r & 1), (uint32_t)((r - 2) >> 1) & 1, ctx, 14))) return -1;
+        if constexpr (VARLEN) {
+          // the next slot that holds something
+          for (;;) {
+            int64_t at;
+            if (sched)
+              at = atomicAdd(sched, 1u);
+            else
+              at = (int64_t)(static_turn++) * grid_dim_x() + cta_id_x();
+            if (at >= total_items) break;
+            int head, rank;
+            grouped_work_item((int)at, bh_count, tiles_per_head, hgroup, &head, &rank);
+            const int slot = causal ? tiles_per_head - 1 - rank : rank;
+            // the last sequence that starts at or before the slot (its slots come before the next one's)
+            int lo = 0, hi = vl.seqs;
+            while (hi - lo > 1) {
+              const int mid = (lo + hi) >> 1;
+              if (min(max(vl.cu[mid], 0), n) / (C::NQ * BM) + mid <= slot) lo = mid;
+              else hi = mid;
+            }
+            const int first = vl.cu[lo], end = vl.cu[lo + 1];
+            if (first < 0 || end < first || end > n) report_error(err, DERR_BAD_ARG, 15);
+            const int base = min(max(first, 0), n), len = min(max(end, base), n) - base;
+            const int tile = slot - (base / (C::NQ * BM) + lo);
+            if (tile < 0 || tile >= (len + C::NQ * BM - 1) / (C::NQ * BM)) continue;
+            vitem[(r & 1) * 4] = head;
+            vitem[(r & 1) * 4 + 1] = tile * (C::NQ * BM);
+            vitem[(r & 1) * 4 + 2] = base;
+            vitem[(r & 1) * 4 + 3] = len;
+            packed = item_of(r & 1);
+            item_slot[r & 1] = r & 1;
+            mbar_arrive(B.item_full + (r & 1));
+            return r & 1;
+          }
+          item_slot[r & 1] = -1;
+          mbar_arrive(B.item_full + (r & 1));
+          return -1;
+        }
         const unsigned ticket = atomicAdd(sched, 1u);
         const int item = ticket < (unsigned)total_items ? (int)ticket : -1;
         item_slot[r & 1] = item;
@@ -398,7 +476,8 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
       for (int r = 0, item = draw(0); ok && item >= 0; item = draw(++r)) {
         const Item w = item_at(item);
         const int nmax = max(w.nq[0], w.nq[1]);
-        if (!(ok = debug_check(w.head < bh_count && w.kvhead * group < bh_count && w.qrow0 < n && nmax <= nblocks,
+        if (!(ok = debug_check(w.head < bh_count && w.kvhead * group < bh_count && w.qrow0 < w.n && nmax <= w.nblk &&
+                                   w.base + w.n <= n,
                                ctx, 60)))
           break;
         // Q of this item once the previous item's S = Q K^T are done
@@ -407,13 +486,13 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
         for (int q = 0; q < C::NQ; ++q)
           for (int kb = 0; kb < C::KB; ++kb)
             tma_load_3d(smem + C::OFF_Q + q * C::Q_BYTES + kb * (BM * C::SW), &tm_q, B.q_full, kb * C::BLK_COLS,
-                        w.qrow0 + q * BM, w.head);
+                        w.base + w.qrow0 + q * BM, w.head);
         ++q_loads;
         for (int idx = 0; ok && idx < 2 * nmax; ++idx) {
           bool is_v;
           int j;
           ring_tile(idx, nmax, &is_v, &j);
-          if (!(ok = debug_check(j >= 0 && j < nmax && tile_at(j) >= 0 && tile_at(j) < nblocks, ctx, 61))) break;
+          if (!(ok = debug_check(j >= 0 && j < nmax && tile_at(j) >= 0 && tile_at(j) < w.nblk, ctx, 61))) break;
           const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
           for (int e = 0; e < C::RB; ++e) {
             const uint32_t g = ring_pos;
@@ -423,8 +502,8 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
             uint8_t* dst = smem + C::OFF_RING + slot * C::ENTRY_BYTES;
             constexpr int kbs = C::KB / C::RB;  // column blocks per entry
             for (int kb = 0; kb < kbs; ++kb)
-              tma_load_3d(dst + kb * (BN * C::SW), tm, B.kv_full + slot, (e * kbs + kb) * C::BLK_COLS, tile_at(j) * BN,
-                          w.kvhead);
+              tma_load_3d(dst + kb * (BN * C::SW), tm, B.kv_full + slot, (e * kbs + kb) * C::BLK_COLS,
+                          w.base + tile_at(j) * BN, w.kvhead);
             ++ring_pos;
           }
         }
@@ -553,6 +632,20 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
           __syncwarp();
         }
       };
+      // (packed) the V rows of the item's last key tile that lie behind the sequence: zero
+      auto clear_tail = [&](const Item& w, int j, int vidx) {
+        if constexpr (VARLEN) {
+          const int rem = w.n - j * BN;
+          if (rem >= BN) return;
+          uint8_t* vt = smem + C::OFF_RING + slot_of(vidx) * C::ENTRY_BYTES;
+          for (int i = rem * 8 + lane; i < BN * 8; i += 32)
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+              *reinterpret_cast<uint4*>(vt + kb * (BN * C::SW) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      };
       // the first P V of query tile q in an item overwrites O_q: the softmax must have read it
       auto o_free = [&](int q) { return oq[q] == 0 || wait(B.o_empty + q, (oq[q] - 1) & 1, 26 + q); };
       bool ok = true;
@@ -587,6 +680,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
                 commit(B.s_full + 0);
               }
               if (!(ok = wait_full(vidx))) break;
+              clear_tail(w, j, vidx);
               if (j < nq[0]) {
                 if (!(ok = wait(B.p_full + 0, (tq[0] + j) & 1, 22))) break;
                 if (j == 0 && !(ok = o_free(0))) break;
@@ -617,6 +711,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
             for (int j = 0; ok && j < nmax; ++j) {
               const int vidx = 2 * j + 1, kidx = 2 * j + 2;
               if (!(ok = wait_full(vidx))) break;
+              clear_tail(w, j, vidx);
               if (j < nq[0]) {
                 if (!(ok = wait(B.p_full + 0, (tq[0] + j) & 1, 22))) break;
                 if (j == 0 && !(ok = o_free(0))) break;
@@ -658,6 +753,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
             const int vidx = v_pos(j, nb);
             const int t = tq[0] + j;
             if (!(ok = wait_full(vidx))) break;
+            clear_tail(w, j, vidx);
             if (!(ok = wait(B.p_full + (t & 1), (t >> 1) & 1, 24))) break;
             if (j == 0 && !(ok = o_free(0))) break;
             tc_fence_after();
@@ -766,7 +862,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
         // visible columns [lo, hi) of this row: keys before N, (causal) not after the row,
         // (window) within the window; none when the tile is listed only for the other query tile
         const int jt = tile_at(j);
-        int lo = 0, hi = n - jt * BN;
+        int lo = 0, hi = w.n - jt * BN;
         if (causal) hi = min(hi, row - jt * BN + 1);
         if constexpr (MASKED) {
           if (window > 0) {
@@ -870,7 +966,8 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
       // epilogue: O / l -> global (16-bit), L = (m + log2 l) ln 2
       if (ok && nb > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(B.o_full + q, oq & 1, ctx, 40 + q));
-        if (ok && !MASKED) {
+        // (packed: a whole tile by TMA, the sequence's last rows one by one)
+        if (ok && !MASKED && !(VARLEN && w.qrow0 + (q + 1) * BM > w.n)) {
           // 64 columns at a time: TMEM -> registers (x 1/l) -> this warpgroup's staging box ->
           // one TMA store (rows past N are not written).  The box is taken once the previous
           // store from it has read it; O is released (o_empty) as soon as its last columns are in
@@ -914,20 +1011,24 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
             if (leader) {
               ok = mbar_wait(B.stg_full + q, stg_uses & 1, ctx, 46 + q);
               if (ok) {
-                tma_store_3d(&tm_o, box, pc * 64, w.qrow0 + q * BM, head);
+                tma_store_3d(&tm_o, box, pc * 64, w.base + w.qrow0 + q * BM, head);
                 bulk_commit_group();
               }
             }
             ++stg_uses;
           }
           ++oq;
-          if (row < n) lse[(int64_t)head * n + row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (row < w.n)
+            lse[(int64_t)head * n + w.base + row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
           if (counter && rit == 0) atomicAdd(counter, (unsigned long long)nb);
         } else if (ok) {
-          // masked launches (one item per CTA): rows straight from registers to global memory
+          // masked launches (one item per CTA) and ragged packed tiles: rows straight from registers to
+          // global memory
           tc_fence_after();
           const float inv = l > 0.f ? 1.f / l : 0.f;
           uint8_t* orow = reinterpret_cast<uint8_t*>(out) + (((int64_t)head * n + row) * D) * 2;
+          if constexpr (VARLEN)
+            orow = reinterpret_cast<uint8_t*>(out) + ((w.base + row) * vl.o_ts + head * vl.o_hs) * 2;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t r[32];
@@ -938,7 +1039,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               pk[i] = pack2<BF16>(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
-            if (row < n) {
+            if (row < w.n) {
               uint4* dst = reinterpret_cast<uint4*>(orow + c * 64);
 #pragma unroll
               for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
@@ -948,7 +1049,8 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
           tc_fence_before();
           mbar_arrive(B.o_empty + q);
           ++oq;
-          if (row < n) lse[(int64_t)head * n + row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (row < w.n)
+            lse[(int64_t)head * n + w.base + row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
           if (counter && rit == 0) atomicAdd(counter, (unsigned long long)(MASKED ? list_hdr[2 + q] : nb));
         }
       } else if (MASKED && ok && nb == 0 && row < n) {
@@ -969,7 +1071,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
-  if (queue && threadIdx.x == 0) {  // (queue: a compile-time constant)
+  if (queue && (!VARLEN || sched) && threadIdx.x == 0) {  // (queue: a compile-time constant)
     // this CTA draws no more tickets; the last one to get here empties the queue for the next
     // launch that uses it (every CTA has drawn its last ticket by then)
     __threadfence();
@@ -1044,7 +1146,43 @@ cudaError_t launch_fwd_d(const FwdArgs& a, F8Scales f8 = F8Scales()) {
   if (e == cudaSuccess) {
     kern<<<(unsigned)grid, C::THREADS, smem, a.stream>>>(tq, tk, tv, to, a.o, a.lse, a.n, a.bh, tiles, scale_log2,
                                                          a.causal, a.group, a.err, a.counter, a.window, a.block_mask,
-                                                         a.mask_heads, a.heads, snake, qs.counters, hgroup, f8);
+                                                         a.mask_heads, a.heads, snake, qs.counters, hgroup, f8,
+                                                         VarlenSpec());
+    e = cudaGetLastError();
+  }
+  return queue_slot_done(qs, e, a.stream);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_fwd_varlen_d(const VarlenFwdArgs& a) {
+  using C = FwdCfg<D>;
+  CUtensorMap tq, tk, tv, to;
+  const int hkv = a.h / a.group;
+  if (!make_tmap_16bit_strided(&tq, a.q, BF16, D, a.t, a.h, a.q_ts, a.q_hs, BM) ||
+      !make_tmap_16bit_strided(&tk, a.k, BF16, D, a.t, hkv, a.k_ts, a.k_hs, BN) ||
+      !make_tmap_16bit_strided(&tv, a.v, BF16, D, a.t, hkv, a.v_ts, a.v_hs, BN) ||
+      !make_tmap_16bit_strided(&to, a.o, BF16, D, a.t, a.h, a.o_ts, a.o_hs, BM))
+    return cudaErrorInvalidValue;
+  const int smem = C::SMEM_STG + 32;
+  static_assert(C::SMEM_STG + 32 <= 232448, "shared memory");
+  const int tiles = a.t / (C::NQ * BM) + a.seqs;  // item slots of a head
+  const int64_t items = (int64_t)a.h * tiles;
+  const int64_t grid = std::min<int64_t>(items, device_sm_count());
+  const int hgroup = head_group_for_l2((int64_t)2 * a.t * C::ROW / a.group, kL2HeadBudgetFwd);
+  QueueSlot qs;
+  if (grid < items) qs = queue_slot_take(a.stream);
+  auto kern = fwd_tc_kernel<D, BF16, false, true, false, true>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) {
+    VarlenSpec vl;
+    vl.cu = a.cu;
+    vl.seqs = a.seqs;
+    vl.o_ts = a.o_ts;
+    vl.o_hs = a.o_hs;
+    kern<<<(unsigned)grid, C::THREADS, smem, a.stream>>>(tq, tk, tv, to, a.o, a.lse, a.t, a.h, tiles,
+                                                         a.scale * 1.4426950408889634f, a.causal, a.group, a.err,
+                                                         a.counter, 0, nullptr, 0, a.h, 0, qs.counters, hgroup,
+                                                         F8Scales(), vl);
     e = cudaGetLastError();
   }
   return queue_slot_done(qs, e, a.stream);
@@ -1193,6 +1331,16 @@ cudaError_t launch_fwd_fp8(const Fp8FwdArgs& a) {
 
 bool fwd_tc_supported(int dtype, int d) {
   return (dtype == DT_BF16 || dtype == DT_FP16) && (d == 64 || d == 128 || d == 256);
+}
+
+cudaError_t launch_fwd_varlen(const VarlenFwdArgs& a) {
+  const bool bf = a.dtype == DT_BF16;
+  switch (a.d) {
+    case 64: return bf ? launch_fwd_varlen_d<64, true>(a) : launch_fwd_varlen_d<64, false>(a);
+    case 128: return bf ? launch_fwd_varlen_d<128, true>(a) : launch_fwd_varlen_d<128, false>(a);
+    case 256: return bf ? launch_fwd_varlen_d<256, true>(a) : launch_fwd_varlen_d<256, false>(a);
+    default: return cudaErrorNotSupported;
+  }
 }
 
 cudaError_t launch_fwd_tc(const FwdArgs& a) {

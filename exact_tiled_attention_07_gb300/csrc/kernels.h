@@ -184,6 +184,26 @@ cudaError_t launch_sm_clock_sample(unsigned long long* out, int blocks, cudaStre
 // returns `status`.
 int set_last_error(int status, const char* fmt, ...);
 
+// Forward over packed sequences: Q, O [t][h][d], K, V [t][h / group][d] with the given element strides,
+// L [h][t]; sequence s is rows [cu[s], cu[s + 1]).
+struct VarlenFwdArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  const int32_t* cu;  // [seqs + 1]
+  int seqs, t, h, group, d;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
+  float scale;
+  int causal;
+  int dtype;
+  unsigned long long* err;
+  unsigned long long* counter;
+  cudaStream_t stream;
+};
+cudaError_t launch_fwd_varlen(const VarlenFwdArgs& a);
+
 // 4-bit cache (layout: kv4.cuh) rows: packed K, V rows [t][hkv][d] with the given element strides
 // (rows of sequence b: [cu[b], cu[b + 1])) and the last of the lens[b] cached slots of sequence b.
 struct Kv4RowArgs {

@@ -21,21 +21,28 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// 3-D map over a [heads][rows][cols] row-major array of 16-bit elements (cols
-// contiguous), read in boxes of 64 columns (128 bytes) x box_rows rows with the
-// 128-byte swizzle; rows beyond `rows` read as zero.
-inline bool make_tmap_16bit_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t cols, uint64_t rows,
-                               uint64_t heads, uint32_t box_rows) {
+// 3-D map over 16-bit rows of `cols` contiguous elements, row_stride elements apart, in `heads`
+// matrices head_stride elements apart (strides multiples of 16 bytes); boxes and fill as below.
+inline bool make_tmap_16bit_strided(CUtensorMap* map, const void* base, bool bf16, uint64_t cols, uint64_t rows,
+                                    uint64_t heads, uint64_t row_stride, uint64_t head_stride, uint32_t box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {cols, rows, heads};
-  cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
+  cuuint64_t strides[2] = {row_stride * 2, head_stride * 2};
   cuuint32_t box[3] = {64, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// 3-D map over a [heads][rows][cols] row-major array of 16-bit elements (cols
+// contiguous), read in boxes of 64 columns (128 bytes) x box_rows rows with the
+// 128-byte swizzle; rows beyond `rows` read as zero.
+inline bool make_tmap_16bit_3d(CUtensorMap* map, const void* base, bool bf16, uint64_t cols, uint64_t rows,
+                               uint64_t heads, uint32_t box_rows) {
+  return make_tmap_16bit_strided(map, base, bf16, cols, rows, heads, cols, cols * rows, box_rows);
 }
 
 // 3-D map over a [heads][rows][cols] row-major array of bytes (FP8 codes), boxes of 128 columns

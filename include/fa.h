@@ -286,6 +286,27 @@ FA_API fa_status fa_fwd_fp8_gqa(const void* Q8, const void* K8, const void* V8, 
                                 int Hkv, int N, int d, float scale, int causal, fa_dtype out_dtype, void* stream);
 
 /*
+ * Forward pass over packed sequences of different lengths (whole prompts; fa_fwd_gqa without padding).
+ *   Q, O      [T][H][d], K, V [T][Hkv][d] dtype (bf16 or fp16), the last dimension contiguous, with token and
+ *             head strides in elements that are multiples of 16 bytes and at least d: Q, K and V may be
+ *             slices of one fused projection
+ *   L         out: [H][T] fp32, as fa_fwd
+ *   cu_seqlens  device int32 [S + 1], non-decreasing, in [0, T]: sequence s is rows [cu_seqlens[s], cu_seqlens[s + 1])
+ *             and may be empty. A row sees keys of its own sequence only, with causal != 0 those up to its own
+ *             position. Rows of O and L in no sequence are left as they were. Offsets that decrease or leave
+ *             [0, T] are clamped and recorded as a device error.
+ *   d         64, 128 or 256. H a positive multiple of Hkv; query head h reads key/value head h / (H / Hkv).
+ * What the rows of one sequence hold (NaN, infinity) does not reach another one. The lengths are read on
+ * the device: one captured graph serves any lengths with the same T and S. Launches one kernel; results are
+ * the same bits for the same arguments.
+ */
+FA_API fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* L,
+                               const int32_t* cu_seqlens, int S, int T, int H, int Hkv, int d, int64_t q_token_stride,
+                               int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                               int64_t v_token_stride, int64_t v_head_stride, int64_t o_token_stride,
+                               int64_t o_head_stride, float scale, int causal, fa_dtype dtype, void* stream);
+
+/*
  * A key/value cache held in 4 bits an element (as the FP8 quantiser's block scales, "Lecture 8"
  * §8.1, with one step and one middle per 64 channels of a row; the cache and its decode of §8.2).
  *   cache     [B][Hkv][capacity / 64] blocks of 72 d bytes, 16-byte aligned; capacity (slots of a

@@ -74,6 +74,7 @@ def test_refusals_before_the_library():
     w = torch.zeros(2, 2, 128)
     for call in (lambda: fa.fa_kv4_append(rows, rows, cu, lens, cache), lambda: fa.fa_kv4_read(cache, cu, lens, rows, rows),
                  lambda: fa.fa_decode_kv4(q, cache, lens, q, L, 0.1),
+                 lambda: fa.fa_fwd_varlen(rows, rows, rows, rows, torch.zeros(2, 5), cu, 0.1, True),
                  lambda: fa.fa_kv4_evict(cache, w, lens, 8, 2, cache, w, lens, torch.zeros(32, dtype=torch.int32))):
         with pytest.raises(ValueError, match="CUDA tensors"):
             call()
