@@ -617,7 +617,7 @@ static fa_status kv4_rows(bool read, const void* K, const void* V, const int32_t
   if (weights && (st = check_words({weights}, name)) != FA_OK) return st;
   const int eb = dtype == FA_FP32 ? 4 : 2;
   if ((st = check_strides({k_token_stride, k_head_stride, v_token_stride, v_head_stride}, eb, name)) != FA_OK) return st;
-  if ((int64_t)T * Hkv * (d / 8) > (int64_t)INT32_MAX * 256)
+  if (T > INT32_MAX - 64 || (int64_t)Hkv * (d / 8) > 65535 * 32)
     return fail(FA_ERR_INVALID_ARG, "%s: T=%d rows of %d heads are too many for one call", name, T, Hkv);
   DeviceSyms syms;
   if ((st = device_syms(&syms)) != FA_OK) return st;
@@ -709,7 +709,7 @@ fa_status fa_kv4_evict(const void* cache, const float* weights, const int32_t* l
   if ((st = check_words({weights, lens, out_weights, out_lens, kept}, "fa_kv4_evict")) != FA_OK) return st;
   if (cache == out_cache || weights == out_weights)
     return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: the kept rows go into another cache, not into their own");
-  if ((double)B * Hkv * keep * (d / 16) > 256.0 * INT32_MAX)
+  if ((double)B * Hkv * ((keep + 63) / 64) > (double)INT32_MAX)
     return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: too many rows for one call");
   DeviceSyms syms;
   if ((st = device_syms(&syms)) != FA_OK) return st;

@@ -729,11 +729,12 @@ struct Partials {
 };
 
 constexpr int kFinishThreads = 256;
+constexpr int kWeightSlots = 4 * kFinishThreads;  // slots of a head whose weights a block of the finish adds up
 constexpr int kMaxRuns = 512;  // CTAs of the decode kernel, at most (one per SM)
 
 // What is left when the runs are done.  Blocks [0, segments): the segments that several CTAs' runs cut
 // are joined from their partials, in the order of the CTAs, and the rows of empty sequences are
-// written.  Further blocks, when weights are asked for, kFinishThreads slots of a head each: weights_out =
+// written.  Further blocks, when weights are asked for, kWeightSlots slots of a head each: weights_out =
 // weights_in + sum over the head's rows of 2^(S - L log2e).
 template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(kFinishThreads)
@@ -808,18 +809,23 @@ __global__ void __launch_bounds__(kFinishThreads)
     return;
   }
   // ---- weights
-  const int tiles = (a.capacity + kFinishThreads - 1) / kFinishThreads;
+  const int tiles = (a.capacity + kWeightSlots - 1) / kWeightSlots;
   const int wb = (int)blockIdx.x - segments;
   const int bh = wb / tiles, b = bh / a.hkv, hk = bh - b * a.hkv;
-  const int slot0 = (wb - bh * tiles) * kFinishThreads, slot = slot0 + threadIdx.x;
+  const int slot0 = (wb - bh * tiles) * kWeightSlots + threadIdx.x;  // this thread's slots: slot0 + i * kFinishThreads
   const int len = clamp_len(a.lens[b], a.capacity);
-  if (slot0 >= len) return;
+  if (slot0 - (int)threadIdx.x >= len) return;
   const int nb = blocks_of(len);
   const int64_t before = wl.total(b);
-  const int64_t at = (int64_t)bh * a.capacity + slot;
-  float w = 0.f;
-  const float w_in = a.w_in && slot < len ? a.w_in[at] : 0.f;
-  const float* s = scores + (int64_t)bh * R * a.capacity + slot;
+  constexpr int WT = kWeightSlots / kFinishThreads;
+  const int64_t at = (int64_t)bh * a.capacity + slot0;
+  float w[WT], w_in[WT];
+#pragma unroll
+  for (int i = 0; i < WT; ++i) {
+    w[i] = 0.f;
+    w_in[i] = a.w_in && slot0 + i * kFinishThreads < len ? a.w_in[at + i * kFinishThreads] : 0.f;
+  }
+  const float* s = scores + (int64_t)bh * R * a.capacity + slot0;
   for (int rg = 0; rg < row_groups; ++rg) {
     // the group's log-sum-exps, from the partials where several CTAs have them (O's block writes L only now)
     const Partials<D, ROWS> P = partials(before, nb, hk * row_groups + rg);
@@ -846,14 +852,19 @@ __global__ void __launch_bounds__(kFinishThreads)
       if (lane == 0) stat[row].x = L;
     }
     __syncthreads();
-    if (slot < len)
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r) {
-        const float L = stat[r].x;
-        if (L != -INFINITY) w += ex2(s[(int64_t)(rg * ROWS + r) * a.capacity] - L);
-      }
+#pragma unroll 2
+    for (int r = 0; r < rows; ++r) {
+      const float L = stat[r].x;
+      if (L == -INFINITY) continue;
+#pragma unroll
+      for (int i = 0; i < WT; ++i)
+        if (slot0 + i * kFinishThreads < len)
+          w[i] += ex2(s[(int64_t)(rg * ROWS + r) * a.capacity + i * kFinishThreads] - L);
+    }
   }
-  if (slot < len) a.w_out[at] = w_in + w;
+#pragma unroll
+  for (int i = 0; i < WT; ++i)
+    if (slot0 + i * kFinishThreads < len) a.w_out[at + i * kFinishThreads] = w_in[i] + w[i];
 }
 
 // Groups of 8 query rows that a CTA takes together: two when there are more than 8 rows, so that the cache is
@@ -875,14 +886,15 @@ cudaError_t launch_nt(const DecodeKv4Args& a) {
   float* part = static_cast<float*>(a.ws);
   float* scores = part + (size_t)G * 2 * partial_floats(C::ROWS, D);
   auto kern = a.w_out ? decode_kv4_kernel<D, BF16, NT, true> : decode_kv4_kernel<D, BF16, NT, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<unsigned long long> allowed[2];  // context in which the kernel may have its shared memory
+  cudaError_t e = allow_smem(kern, C::SMEM, &allowed[a.w_out ? 1 : 0]);
   if (e != cudaSuccess) return e;
   kern<<<G, C::THREADS, C::SMEM, a.stream>>>(a, part, scores, row_groups);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the runs are still going (it waits for them before it reads anything)
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.b * a.hkv * row_groups));
-  if (a.w_out) cfg.gridDim.x += (unsigned)((a.capacity + kFinishThreads - 1) / kFinishThreads) * a.b * a.hkv;
+  if (a.w_out) cfg.gridDim.x += (unsigned)((a.capacity + kWeightSlots - 1) / kWeightSlots) * a.b * a.hkv;
   cfg.blockDim = dim3(kFinishThreads);
   cfg.stream = a.stream;
   cudaLaunchAttribute attr{};

@@ -1172,7 +1172,8 @@ cudaError_t launch_fwd_varlen_d(const VarlenFwdArgs& a) {
   QueueSlot qs;
   if (grid < items) qs = queue_slot_take(a.stream);
   auto kern = fwd_tc_kernel<D, BF16, false, true, false, true>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<unsigned long long> allowed;
+  cudaError_t e = allow_smem(kern, smem, &allowed);
   if (e == cudaSuccess) {
     VarlenSpec vl;
     vl.cu = a.cu;

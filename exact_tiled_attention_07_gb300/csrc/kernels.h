@@ -1,6 +1,7 @@
 // Internal launch interface between the C ABI (api.cu) and the kernel files.
 #pragma once
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 namespace fa {
@@ -183,6 +184,17 @@ cudaError_t launch_sm_clock_sample(unsigned long long* out, int blocks, cudaStre
 // Records the calling thread's last error message (read by fa_last_error_message) and
 // returns `status`.
 int set_last_error(int status, const char* fmt, ...);
+
+// Lets a kernel have `bytes` of dynamic shared memory, once per context (the call takes about 1 us of
+// host time); *done holds the id of the context it was made in.
+template <typename K>
+inline cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>* done) {
+  const unsigned long long ctx = current_context_id();
+  if (ctx != 0 && done->load(std::memory_order_relaxed) == ctx) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->store(ctx, std::memory_order_relaxed);
+  return e;
+}
 
 // Forward over packed sequences: Q, O [t][h][d], K, V [t][h / group][d] with the given element strides,
 // L [h][t]; sequence s is rows [cu[s], cu[s + 1]).

@@ -78,122 +78,165 @@ __device__ __forceinline__ bool row_slot(const Kv4RowArgs& a, int r, int b, int6
   return false;
 }
 
-// One thread per 8 channels of a row (one 32-bit word of codes); the 8 threads of a group find its
-// minimum and maximum with three shuffles.  Bound by HBM: 8 elements in, 4.5 bytes out a thread.
-template <typename T>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowArgs a, int words_per_row) {
-  const int64_t per_row = (int64_t)a.hkv * words_per_row;
-  const int64_t total = (int64_t)a.t * per_row;
-  // words_per_row is a multiple of 8 and a group's words are 8 consecutive threads of a warp: all
-  // 8 have the same row, head and fate, so the shuffles stay inside them
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= total) return;
-  const int r = (int)(i / per_row);
-  const int rest = (int)(i - (int64_t)r * per_row);
-  const int h = rest / words_per_row, word = rest - h * words_per_row;
-  const int b = packed_sequence(a.cu, a.b, r);
+// Sequence of packed row r for a whole warp (every lane gets it): the number of sequences that end at
+// or before r, 32 ends at a time; -1 when r belongs to none.  Any contents of cu give a b in range.
+__device__ __forceinline__ int warp_sequence(const int32_t* __restrict__ cu, int B, int r) {
+  const int lane = threadIdx.x & 31;
+  int b = 0;
+  for (int base = 0; base < B; base += 32) {
+    const bool past = base + lane < B && cu[base + lane + 1] <= r;
+    const int n = __popc(__ballot_sync(0xffffffffu, past));
+    b += n;
+    if (n < 32) break;
+  }
+  return b < B && r >= cu[0] ? b : -1;
+}
+
+constexpr int kRowWarps = 8;  // rows of a block: one warp each
+
+// A warp takes CH x 32 words (8 channels each) of a row's key/value heads: a lane loads 16 bytes of
+// 16-bit elements, keys and values, before anything else is known; the 8 lanes of a group find its minimum and
+// maximum with three shuffles and a lane's codes are one 32-bit word.  Bound by HBM: 16 bytes in, 4.5 out
+// for 8 channels.  The quotient is taken as a product with 1 / step, whose distance from the IEEE quotient
+// is below 2^-20 for |quotient| <= 8.5; only where it lies within 2^-18 of a half (where that could change the
+// rounding) is the division done.
+template <typename T, int CH>
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4RowArgs a, int word_shift) {
+  const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= a.t) return;
+  const int words = a.hkv << word_shift;  // of a row
+  const int w0 = blockIdx.y * (CH * 32) + lane;
+  float x[CH][2][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int w = w0 + c * 32;
+    if (w >= words) continue;
+    const int h = w >> word_shift, word = w - (h << word_shift);
+    Elem<T>::load8(static_cast<const T*>(a.k) + r * a.k_ts + h * a.k_hs + word * 8, x[c][0]);
+    Elem<T>::load8(static_cast<const T*>(a.v) + r * a.v_ts + h * a.v_hs + word * 8, x[c][1]);
+  }
+  const int b = warp_sequence(a.cu, a.b, r);
   if (b < 0) return;
   int64_t slot;
   if (!row_slot(a, r, b, &slot, kSiteAppend)) return;
-  const int d = a.d;
-  uint8_t* block = a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(d);
-  const int in = (int)(slot % kKv4Block);
-  const unsigned lanes = 0xFFu << (threadIdx.x & 24);
+  const int d = a.d, in = (int)(slot % kKv4Block);
+  const unsigned lanes = 0xFFu << (lane & 24);
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const T* src = which ? static_cast<const T*>(a.v) + r * a.v_ts + h * a.v_hs
-                         : static_cast<const T*>(a.k) + r * a.k_ts + h * a.k_hs;
-    float x[8];
-    Elem<T>::load8(src + word * 8, x);
-    float lo = x[0], hi = x[0];
-    bool bad = false;
+  for (int c = 0; c < CH; ++c) {
+    const int w = w0 + c * 32;
+    if (w >= words) continue;  // (words is a multiple of 8: a group's lanes go together)
+    const int h = w >> word_shift, word = w - (h << word_shift);
+    uint8_t* block = a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(d);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      bad |= !(fabsf(x[j]) <= kKv4Limit);
-      lo = fminf(lo, x[j]);
-      hi = fmaxf(hi, x[j]);
-    }
+    for (int which = 0; which < 2; ++which) {
+      const float(&y)[8] = x[c][which];
+      float lo = y[0], hi = y[0];
+      bool bad = false;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(lanes, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o));
-    }
-    bad = __any_sync(lanes, bad);
-    const __half step = __float2half_ru(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-    const float s = __half2float(step);
-    const __half middle = __float2half_rn(__fadd_rn(lo, 8.f * s));
-    const float m = __half2float(middle);
-    uint32_t codes = 0;
+      for (int j = 0; j < 8; ++j) {
+        bad |= !(fabsf(y[j]) <= kKv4Limit);
+        lo = fminf(lo, y[j]);
+        hi = fmaxf(hi, y[j]);
+      }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float c = 0.f;
-      if (!bad && s > 0.f) c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[j], m), s)), -8.f), 7.f);
-      codes |= (uint32_t)((int)c + 8) << (4 * j);
+      for (int o = 4; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(lanes, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o));
+      }
+      bad = __any_sync(lanes, bad);
+      const __half step = __float2half_ru(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+      const float s = __half2float(step);
+      const __half middle = __float2half_rn(__fadd_rn(lo, 8.f * s));
+      const float m = __half2float(middle);
+      uint32_t codes = 0x88888888u;
+      if (!bad && s > 0.f) {
+        const float inv = __frcp_rn(s);
+        codes = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float diff = __fsub_rn(y[j], m);
+          float q = diff * inv;
+          if (fabsf(q - rintf(q)) > 0.5f - 0x1p-18f) q = __fdiv_rn(diff, s);
+          codes |= (uint32_t)((int)fminf(fmaxf(rintf(q), -8.f), 7.f) + 8) << (4 * j);
+        }
+      }
+      *reinterpret_cast<uint32_t*>(block + kv4_codes_at(d, which) + in * kv4_code_bytes(d) + word * 4) = codes;
+      if ((word & 7) == 0) {
+        const uint32_t par = bad ? kKv4NanParam
+                                 : (uint32_t)__half_as_ushort(step) | ((uint32_t)__half_as_ushort(middle) << 16);
+        *reinterpret_cast<uint32_t*>(block + kv4_params_at(d, which) + (in * kv4_param_words(d) + (word >> 3)) * 4) = par;
+      }
     }
-    *reinterpret_cast<uint32_t*>(block + kv4_codes_at(d, which) + in * kv4_code_bytes(d) + word * 4) = codes;
-    if ((word & 7) == 0) {
-      const uint32_t par = bad ? kKv4NanParam
-                               : (uint32_t)__half_as_ushort(step) | ((uint32_t)__half_as_ushort(middle) << 16);
-      *reinterpret_cast<uint32_t*>(block + kv4_params_at(d, which) + (in * kv4_param_words(d) + (word >> 3)) * 4) = par;
-    }
+    if (a.weights && word == 0) a.weights[((int64_t)b * a.hkv + h) * a.capacity + slot] = 0.f;
   }
-  if (a.weights && word == 0) a.weights[((int64_t)b * a.hkv + h) * a.capacity + slot] = 0.f;
 }
 
-// The inverse: one thread per 8 channels of a row, middle + step (code - 8) in fp32, rounded once.
-template <typename T>
-__global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4RowArgs a, int words_per_row) {
-  const int64_t per_row = (int64_t)a.hkv * words_per_row;
-  const int64_t total = (int64_t)a.t * per_row;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= total) return;
-  const int r = (int)(i / per_row);
-  const int rest = (int)(i - (int64_t)r * per_row);
-  const int h = rest / words_per_row, word = rest - h * words_per_row;
-  const int b = packed_sequence(a.cu, a.b, r);
+// The inverse, with the same split: middle + step (code - 8) in fp32, rounded once.
+template <typename T, int CH>
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const Kv4RowArgs a, int word_shift) {
+  const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= a.t) return;
+  const int words = a.hkv << word_shift;
+  const int w0 = blockIdx.y * (CH * 32) + lane;
+  const int b = warp_sequence(a.cu, a.b, r);
   if (b < 0) return;
   int64_t slot;
   if (!row_slot(a, r, b, &slot, kSiteRead)) return;
-  const int d = a.d;
-  const uint8_t* block =
-      a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(d);
-  const int in = (int)(slot % kKv4Block);
+  const int d = a.d, in = (int)(slot % kKv4Block);
+  uint32_t codes[CH][2], par[CH][2];
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const uint32_t codes =
-        *reinterpret_cast<const uint32_t*>(block + kv4_codes_at(d, which) + in * kv4_code_bytes(d) + word * 4);
-    const uint32_t par = *reinterpret_cast<const uint32_t*>(block + kv4_params_at(d, which) +
-                                                            (in * kv4_param_words(d) + (word >> 3)) * 4);
-    const float s = __half2float(__ushort_as_half((unsigned short)(par & 0xFFFF)));
-    const float m = __half2float(__ushort_as_half((unsigned short)(par >> 16)));
-    float x[8];
+  for (int c = 0; c < CH; ++c) {
+    const int w = w0 + c * 32;
+    if (w >= words) continue;
+    const int h = w >> word_shift, word = w - (h << word_shift);
+    const uint8_t* block =
+        a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(d);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = fmaf(s, (float)((int)((codes >> (4 * j)) & 15u) - 8), m);
-    T* dst = which ? static_cast<T*>(const_cast<void*>(a.v)) + r * a.v_ts + h * a.v_hs
-                   : static_cast<T*>(const_cast<void*>(a.k)) + r * a.k_ts + h * a.k_hs;
-    Elem<T>::store8(dst + word * 8, x);
+    for (int which = 0; which < 2; ++which) {
+      codes[c][which] =
+          *reinterpret_cast<const uint32_t*>(block + kv4_codes_at(d, which) + in * kv4_code_bytes(d) + word * 4);
+      par[c][which] = *reinterpret_cast<const uint32_t*>(block + kv4_params_at(d, which) +
+                                                         (in * kv4_param_words(d) + (word >> 3)) * 4);
+    }
   }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int w = w0 + c * 32;
+    if (w >= words) continue;
+    const int h = w >> word_shift, word = w - (h << word_shift);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const float2 p = unpack2<false>(par[c][which]);
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = fmaf(p.x, (float)((int)((codes[c][which] >> (4 * j)) & 15u) - 8), p.y);
+      T* dst = which ? static_cast<T*>(const_cast<void*>(a.v)) + r * a.v_ts + h * a.v_hs
+                     : static_cast<T*>(const_cast<void*>(a.k)) + r * a.k_ts + h * a.k_hs;
+      Elem<T>::store8(dst + word * 8, x);
+    }
+  }
+}
+
+// Two chunks of 32 words a warp (one where a row has no more) keep 64 bytes a lane in flight.
+template <bool READ, typename T>
+cudaError_t launch_rows_t(const Kv4RowArgs& a) {
+  const int shift = a.d == 64 ? 3 : (a.d == 128 ? 4 : 5);
+  const int words = a.hkv << shift;
+  const int ch = words > 32 ? 2 : 1;
+  const dim3 grid((unsigned)((a.t + kRowWarps - 1) / kRowWarps), (unsigned)((words + 32 * ch - 1) / (32 * ch)));
+  auto kern = READ ? (ch == 2 ? kv4_read_kernel<T, 2> : kv4_read_kernel<T, 1>)
+                   : (ch == 2 ? kv4_append_kernel<T, 2> : kv4_append_kernel<T, 1>);
+  kern<<<grid, kRowWarps * 32, 0, a.stream>>>(a, shift);
+  return cudaGetLastError();
 }
 
 template <bool READ>
 cudaError_t launch_rows(const Kv4RowArgs& a) {
-  const int words = a.d / 8;
-  const int64_t threads = (int64_t)a.t * a.hkv * words;
-  const unsigned grid = (unsigned)((threads + 255) / 256);
   switch (a.dtype) {
-    case DT_BF16:
-      if (READ) kv4_read_kernel<__nv_bfloat16><<<grid, 256, 0, a.stream>>>(a, words);
-      else kv4_append_kernel<__nv_bfloat16><<<grid, 256, 0, a.stream>>>(a, words);
-      break;
-    case DT_FP16:
-      if (READ) kv4_read_kernel<__half><<<grid, 256, 0, a.stream>>>(a, words);
-      else kv4_append_kernel<__half><<<grid, 256, 0, a.stream>>>(a, words);
-      break;
-    default:
-      if (READ) kv4_read_kernel<float><<<grid, 256, 0, a.stream>>>(a, words);
-      else kv4_append_kernel<float><<<grid, 256, 0, a.stream>>>(a, words);
+    case DT_BF16: return launch_rows_t<READ, __nv_bfloat16>(a);
+    case DT_FP16: return launch_rows_t<READ, __half>(a);
+    default: return launch_rows_t<READ, float>(a);
   }
-  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------- eviction
@@ -203,10 +246,10 @@ cudaError_t launch_rows(const Kv4RowArgs& a) {
 // slots keep their order, so the last slots stay the newest.
 //
 // kv4_select_kernel (one block per head): weights as 32-bit keys that order like the numbers
-// (NaN above everything, -0 as 0); the k-th largest key is found digit by digit (8 bits, four
-// histogram passes over the keys); then one ordered pass writes the kept slots: those above the
-// threshold key, the first ones equal to it, and the newest.
-// kv4_gather_kernel: moves rows, 16 bytes a thread.
+// (NaN above everything, -0 as 0); the k-th largest key is found digit by digit (11, 11 and 10 bits:
+// three histogram passes over the keys, which stay in L2 or L1); then each warp walks its share of the slots
+// twice, counting and writing those above the threshold key, the first ones equal to it, and the newest.
+// kv4_gather_kernel: one block per 64 kept slots of a head, a block of the new cache, 16 bytes a thread.
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (isnan(w)) return 0xFFFFFFFFu;
@@ -223,124 +266,167 @@ __device__ __forceinline__ int evict_len(const Kv4EvictArgs& a, int b) {
   return n;
 }
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32, kSelBins = 2048;
+
+// Adds this warp's digits to the histogram; lanes that agree throughout (equal weights) add once.
+__device__ __forceinline__ void count_digit(unsigned* hist, bool there, uint32_t digit) {
+  const unsigned all = __ballot_sync(0xffffffffu, there);
+  if (!all) return;
+  int same;
+  __match_all_sync(0xffffffffu, there ? digit : 0xFFFFFFFFu, &same);
+  if (same) {
+    if ((threadIdx.x & 31) == 0) atomicAdd(&hist[digit], 32u);
+  } else if (there) {
+    atomicAdd(&hist[digit], 1u);
+  }
+}
 
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictArgs a) {
   const int bh = blockIdx.x, b = bh / a.hkv;
   const int n = evict_len(a, b);
-  const int kept_n = min(n, a.keep);
   int32_t* kept = a.kept + (int64_t)bh * a.keep;
-  const int tid = threadIdx.x;
-  for (int i = kept_n + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = min(n, a.keep) + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
   if (n <= a.keep) {
     for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
     return;
   }
-  const float* w = a.weights + (int64_t)bh * a.capacity;
-  const int m = n - a.recent;  // candidates: slots [0, m)
+  const float* __restrict__ w = a.weights + (int64_t)bh * a.capacity;
+  const int m = n - a.recent;       // candidates: slots [0, m)
   const int k = a.keep - a.recent;  // of which k stay, 0 <= k < m
-  __shared__ unsigned hist[256];
-  __shared__ unsigned warp_sum[2][32];
+  __shared__ unsigned hist[kSelBins];
+  __shared__ unsigned warp_sum[kSelWarps], warp_eq[kSelWarps];
   __shared__ unsigned sel_digit, sel_left;
   uint32_t prefix = 0, mask = 0;
   unsigned left = (unsigned)k;  // still to take among the keys that match prefix
   if (k > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = tid; i < m; i += kSelThreads) {
-        const uint32_t key = weight_key(w[i]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+      constexpr int U = 8;  // loads in flight
+      for (int base = warp * 32; base < m; base += kSelThreads * U) {
+        uint32_t key[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = base + u * kSelThreads + lane;
+          key[u] = i < m ? weight_key(w[i]) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = base + u * kSelThreads + lane;
+          count_digit(hist, i < m && (key[u] & mask) == prefix, (key[u] >> shift) & digits);
+        }
       }
       __syncthreads();
-      if (tid == 0) {
-        unsigned rest = left;
-        int digit = 255;
-        for (; digit > 0; --digit) {
-          if (hist[digit] >= rest) break;
-          rest -= hist[digit];
-        }
-        sel_digit = (unsigned)digit;
-        sel_left = rest;
+      // the digit at which the counts from the top reach `left`: thread t holds bins 2047 - 2t and 2046 - 2t
+      const int top = kSelBins - 1 - 2 * tid;
+      const unsigned c0 = hist[top], c1 = hist[top - 1];
+      unsigned incl = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      unsigned before = incl - c0 - c1;
+      for (int j = 0; j < warp; ++j) before += warp_sum[j];
+      if (before < left && before + c0 + c1 >= left) {
+        const bool first = before + c0 >= left;
+        sel_digit = (unsigned)(first ? top : top - 1);
+        sel_left = left - before - (first ? 0u : c0);
       }
       __syncthreads();
       prefix |= sel_digit << shift;
-      mask |= 0xFFu << shift;
+      mask |= digits << shift;
       left = sel_left;
-      __syncthreads();
     }
   }
-  // keys above `prefix` stay, and the first `left` of those equal to it
-  unsigned out = 0, eq = 0;  // kept so far, equal ones seen so far (slots before this round)
-  for (int base = 0; base < n; base += kSelThreads) {
-    const int i = base + tid;
-    bool above = false, equal = false;
-    if (i < n) {
-      if (i >= m) {
-        above = true;
-      } else if (k > 0) {
-        const uint32_t key = weight_key(w[i]);
-        above = key > prefix;
-        equal = key == prefix;
-      }
+  // slots of key > prefix stay, the first `left` of those equal to it, and the newest; warp j walks the
+  // slots [j * share, (j + 1) * share)
+  const int share = ((n + kSelThreads - 1) / kSelThreads) * 32;
+  const int from = min(n, warp * share), to = min(n, from + share);
+  auto kind = [&](int i, bool* above, bool* equal) {
+    *above = *equal = false;
+    if (i >= to) return;
+    if (i >= m) {
+      *above = true;
+    } else if (k > 0) {
+      const uint32_t key = weight_key(w[i]);
+      *above = key > prefix;
+      *equal = key == prefix;
     }
-    const unsigned be = __ballot_sync(0xffffffffu, equal);
-    const int warp = tid >> 5, lane = tid & 31;
-    if (lane == 0) warp_sum[0][warp] = __popc(be);
-    __syncthreads();
-    unsigned eq_before = eq, eq_total = 0;
-    for (int j = 0; j < 32; ++j) {
-      const unsigned v = warp_sum[0][j];
-      if (j < warp) eq_before += v;
-      eq_total += v;
-    }
-    const bool take = above || (equal && eq_before + __popc(be & ((1u << lane) - 1u)) < left);
-    const unsigned bt = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) warp_sum[1][warp] = __popc(bt);
-    __syncthreads();
-    unsigned at = out, total = 0;
-    for (int j = 0; j < 32; ++j) {
-      const unsigned v = warp_sum[1][j];
-      if (j < warp) at += v;
-      total += v;
-    }
-    if (take) {
-      const unsigned pos = at + __popc(bt & ((1u << lane) - 1u));
-      if (pos < (unsigned)a.keep) kept[pos] = i;
-    }
-    out += total;
-    eq += eq_total;
-    __syncthreads();
+  };
+  unsigned na = 0, ne = 0;
+#pragma unroll 4
+  for (int i = from + lane; i - lane < to; i += 32) {
+    bool above, equal;
+    kind(i, &above, &equal);
+    na += above;
+    ne += equal;
+  }
+  na = __reduce_add_sync(0xffffffffu, na);
+  ne = __reduce_add_sync(0xffffffffu, ne);
+  if (lane == 0) {
+    warp_sum[warp] = na;
+    warp_eq[warp] = ne;
+  }
+  __syncthreads();
+  unsigned above_before = 0, eq_before = 0;
+  for (int j = 0; j < warp; ++j) {
+    above_before += warp_sum[j];
+    eq_before += warp_eq[j];
+  }
+  const unsigned under = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int i = from + lane; i - lane < to; i += 32) {
+    bool above, equal;
+    kind(i, &above, &equal);
+    const unsigned ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
+    const unsigned my_eq = eq_before + __popc(be & under);  // equal ones in front of this slot
+    const unsigned pos = above_before + __popc(ba & under) + min(my_eq, left);
+    if ((above || (equal && my_eq < left)) && pos < (unsigned)a.keep) kept[pos] = i;
+    above_before += __popc(ba);
+    eq_before += __popc(be);
   }
 }
 
-// One thread per 16 bytes of codes of a kept row (K and V), the first threads of a row also its
-// parameters and weight.
-__global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a) {
-  const int d = a.d, per = d / 32;  // 16-byte pieces of a row's codes
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+__global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, int blocks_per_head) {
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.b; b += blockDim.x) a.out_lens[b] = min(min(max(a.lens[b], 0), a.capacity), a.keep);
-  const int64_t row = i / (2 * per);
-  if (row >= (int64_t)a.b * a.hkv * a.keep) return;
-  const int piece = (int)(i - row * (2 * per));
-  const int64_t bh = row / a.keep;
-  const int to = (int)(row - bh * a.keep);
-  const int from = a.kept[row];
-  if (from < 0) return;
-  const uint8_t* sb =
-      a.cache + (bh * (a.capacity / kKv4Block) + from / kKv4Block) * kv4_block_bytes(d);
-  uint8_t* db = a.out_cache + (bh * (a.out_capacity / kKv4Block) + to / kKv4Block) * kv4_block_bytes(d);
-  const int si = from % kKv4Block, di = to % kKv4Block;
-  const int which = piece / per, part = piece - which * per;
-  const int at = kv4_codes_at(d, which) + part * 16;
-  *reinterpret_cast<uint4*>(db + at + di * kv4_code_bytes(d)) =
-      *reinterpret_cast<const uint4*>(sb + at + si * kv4_code_bytes(d));
-  const int pw = kv4_param_words(d);
-  if (part < pw)
-    *reinterpret_cast<uint32_t*>(db + kv4_params_at(d, which) + (di * pw + part) * 4) =
-        *reinterpret_cast<const uint32_t*>(sb + kv4_params_at(d, which) + (si * pw + part) * 4);
-  if (piece == 0) a.out_weights[bh * a.out_capacity + to] = a.weights[bh * a.capacity + from];
+  const int bh = blockIdx.x / blocks_per_head, blk = blockIdx.x - bh * blocks_per_head;
+  const int to0 = blk * kKv4Block;
+  __shared__ int from[kKv4Block];
+  if (threadIdx.x < kKv4Block)
+    from[threadIdx.x] = to0 + (int)threadIdx.x < a.keep ? a.kept[(int64_t)bh * a.keep + to0 + threadIdx.x] : -1;
+  __syncthreads();
+  const int d = a.d, pw = kv4_param_words(d);
+  const int shift = d == 64 ? 1 : (d == 128 ? 2 : 3);  // log2 of the 16-byte pieces of a row's codes
+  const uint8_t* src = a.cache + (int64_t)bh * (a.capacity / kKv4Block) * kv4_block_bytes(d);
+  uint8_t* dst = a.out_cache + ((int64_t)bh * (a.out_capacity / kKv4Block) + blk) * kv4_block_bytes(d);
+  // codes of K, then of V: in the order of the new block
+#pragma unroll 2
+  for (int i = threadIdx.x; i < 2 * (kKv4Block << shift); i += blockDim.x) {
+    const int which = i >> (6 + shift), row = (i >> shift) & (kKv4Block - 1), part = i & ((1 << shift) - 1);
+    const int f = from[row];
+    if (f < 0) continue;
+    const uint8_t* sb = src + (int64_t)(f / kKv4Block) * kv4_block_bytes(d) + kv4_codes_at(d, which) +
+                        (f % kKv4Block) * kv4_code_bytes(d);
+    *reinterpret_cast<uint4*>(dst + i * 16) = *reinterpret_cast<const uint4*>(sb + part * 16);
+  }
+  for (int i = threadIdx.x; i < 2 * kKv4Block * pw; i += blockDim.x) {
+    const int which = i / (kKv4Block * pw), rest = i - which * (kKv4Block * pw), row = rest / pw;
+    const int f = from[row];
+    if (f < 0) continue;
+    const uint8_t* sb = src + (int64_t)(f / kKv4Block) * kv4_block_bytes(d) + kv4_params_at(d, which) +
+                        ((f % kKv4Block) * pw + rest % pw) * 4;
+    *reinterpret_cast<uint32_t*>(dst + kv4_params_at(d, 0) + i * 4) = *reinterpret_cast<const uint32_t*>(sb);
+  }
+  if (threadIdx.x < kKv4Block && from[threadIdx.x] >= 0)
+    a.out_weights[(int64_t)bh * a.out_capacity + to0 + threadIdx.x] =
+        a.weights[(int64_t)bh * a.capacity + from[threadIdx.x]];
 }
 
 }  // namespace
@@ -352,8 +438,8 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
   kv4_select_kernel<<<a.b * a.hkv, kSelThreads, 0, a.stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t threads = (int64_t)a.b * a.hkv * a.keep * 2 * (a.d / 32);
-  kv4_gather_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, a.stream>>>(a);
+  const int per_head = (a.keep + kKv4Block - 1) / kKv4Block;
+  kv4_gather_kernel<<<(unsigned)per_head * a.b * a.hkv, 256, 0, a.stream>>>(a, per_head);
   return cudaGetLastError();
 }
 

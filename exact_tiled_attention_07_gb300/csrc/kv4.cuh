@@ -26,18 +26,4 @@ __host__ __device__ constexpr int kv4_param_words(int d) { return d / 64; }     
 __host__ __device__ constexpr int kv4_codes_at(int d, int which) { return which * 32 * d; }
 __host__ __device__ constexpr int kv4_params_at(int d, int which) { return 64 * d + which * 4 * d; }
 
-// Sequence that packed row r belongs to: the b in [0, B) with cu[b] <= r < cu[b + 1] for a
-// non-decreasing cu (some b in range for any other contents); -1 when r lies before cu[0] or at
-// or behind cu[B].
-__device__ __forceinline__ int packed_sequence(const int32_t* __restrict__ cu, int B, int r) {
-  if (r < cu[0] || r >= cu[B]) return -1;
-  int lo = 0, hi = B;  // cu[lo] <= r < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= r) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 }  // namespace fa
