@@ -146,7 +146,7 @@ __device__ __forceinline__ int blocks_of(int n) { return (n + kKv4Block - 1) / k
 // The list: sequences, then their heads x row groups (segments), then the segment's nb blocks, each a
 // position, behind kSegCost positions that stand for what a segment costs whatever its length (its queries, joining
 // the warps, its output: about the time of that many blocks).
-constexpr int kSegCost = 8;
+constexpr int kSegCost = 12;
 
 struct Cursor {
   int64_t first;  // list position of sequence b's first segment

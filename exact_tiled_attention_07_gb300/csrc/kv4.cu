@@ -9,6 +9,7 @@
 //   code   = clamp(rint((x - middle) / step), -8, 7) + 8     (8 when step is 0)
 // so |middle + step (code - 8) - x| <= max(step / 2, 2^-11 |middle|) up to fp32 rounding.  The
 // quotient and the two sums are IEEE operations: the codes are the same wherever they are taken.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -22,19 +23,9 @@ namespace {
 constexpr uint32_t kSiteAppend = 920, kSiteRead = 921, kSiteEvict = 922;
 
 template <typename T>
-struct Elem;  // eight consecutive elements of a row as fp32, and back (rounded to nearest)
+struct Elem;  // eight consecutive elements of a row from fp32 (rounded to nearest)
 template <>
 struct Elem<__nv_bfloat16> {
-  static __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<true>(w[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
   static __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack2<true>(x[0], x[1]), pack2<true>(x[2], x[3]), pack2<true>(x[4], x[5]),
                                               pack2<true>(x[6], x[7]));
@@ -42,16 +33,6 @@ struct Elem<__nv_bfloat16> {
 };
 template <>
 struct Elem<__half> {
-  static __device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<false>(w[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
   static __device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack2<false>(x[0], x[1]), pack2<false>(x[2], x[3]),
                                               pack2<false>(x[4], x[5]), pack2<false>(x[6], x[7]));
@@ -59,15 +40,90 @@ struct Elem<__half> {
 };
 template <>
 struct Elem<float> {
-  static __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
   static __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
+
+// Smallest and largest of a group's 64 elements, eight in this lane (raw: as loaded) and the rest in the
+// other seven lanes of `lanes`; NaN when one of them is.  16-bit elements stay packed: the minimum and
+// the negated maximum share a register through the shuffles.
+template <typename T2, typename T>
+__device__ __forceinline__ float2 packed_range(const uint32_t (&w)[4], unsigned lanes) {
+  const T2* v = reinterpret_cast<const T2*>(w);
+  const T2 mn = __hmin2_nan(__hmin2_nan(v[0], v[1]), __hmin2_nan(v[2], v[3]));
+  const T2 mx = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+  T2 r;
+  r.x = __hmin_nan(mn.x, mn.y);
+  r.y = __hneg(__hmax_nan(mx.x, mx.y));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    const uint32_t u = __shfl_xor_sync(lanes, *reinterpret_cast<const uint32_t*>(&r), o);
+    r = __hmin2_nan(r, *reinterpret_cast<const T2*>(&u));
+  }
+  return make_float2((float)r.x, -(float)r.y);
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <typename T>
+struct Raw;  // eight elements as loaded
+template <>
+struct Raw<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ float2 range(unsigned lanes) const { return packed_range<__nv_bfloat162, __nv_bfloat16>(w, lanes); }
+  __device__ __forceinline__ float2 pair(int i) const { return unpack2<true>(w[i]); }
+};
+template <>
+struct Raw<__half> {
+  uint32_t w[4];
+  __device__ __forceinline__ float2 range(unsigned lanes) const { return packed_range<__half2, __half>(w, lanes); }
+  __device__ __forceinline__ float2 pair(int i) const { return unpack2<false>(w[i]); }
+};
+template <>
+struct Raw<float> {
+  uint32_t w[8];
+  __device__ __forceinline__ float2 pair(int i) const {
+    return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  __device__ __forceinline__ float2 range(unsigned lanes) const {
+    float lo = __uint_as_float(w[0]), nhi = -lo;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      lo = min_nan(lo, __uint_as_float(w[i]));
+      nhi = min_nan(nhi, -__uint_as_float(w[i]));
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(lanes, lo, o));
+      nhi = min_nan(nhi, __shfl_xor_sync(lanes, nhi, o));
+    }
+    return make_float2(lo, -nhi);
+  }
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+    r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
+  }
+  return r;
+}
+
+// x / 15 correctly rounded: a quotient from the rounded reciprocal is within an ulp, and its exact
+// remainder times that reciprocal corrects it (Markstein's theorem)
+__device__ __forceinline__ float fifteenth(float x) {
+  constexpr float r = 1.f / 15.f;
+  const float q = x * r;
+  return fmaf(fmaf(-15.f, q, x), r, q);
+}
 
 // Slot that packed row r of sequence b takes: the sequence's rows are the last ones of its
 // lens[b] cached slots.  False (with the device error recorded) when that is not inside the cache.
@@ -96,24 +152,26 @@ constexpr int kRowWarps = 8;  // rows of a block: one warp each
 
 // A warp takes CH x 32 words (8 channels each) of a row's key/value heads: a lane loads 16 bytes of
 // 16-bit elements, keys and values, before anything else is known; the 8 lanes of a group find its minimum and
-// maximum with three shuffles and a lane's codes are one 32-bit word.  Bound by HBM: 16 bytes in, 4.5 out
-// for 8 channels.  The quotient is taken as a product with 1 / step, whose distance from the IEEE quotient
-// is below 2^-20 for |quotient| <= 8.5; only where it lies within 2^-18 of a half (where that could change the
-// rounding) is the division done.
+// maximum together and a lane's codes are one 32-bit word.  Bytes: 16 in, 4.5 out for 8 channels.  The quotient is
+// taken as a product with an approximate 1 / step (2^-23), which is within 2^-19 of the IEEE quotient
+// for |quotient| <= 8.5; only where it lies within 2^-17 of a half (where that could change the rounding) is
+// the division done.  Rounding to an integer is an addition of 1.5 2^23, which leaves it in the low bits;
+// rint and the conversion to int instead (16 a clock on an SM) cost 109 us against %APPEND% for 34,001 rows of 8 heads
+// of 128 bf16 channels.
 template <typename T, int CH>
 __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4RowArgs a, int word_shift) {
   const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= a.t) return;
   const int words = a.hkv << word_shift;  // of a row
   const int w0 = blockIdx.y * (CH * 32) + lane;
-  float x[CH][2][8];
+  Raw<T> x[CH][2];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int w = w0 + c * 32;
     if (w >= words) continue;
     const int h = w >> word_shift, word = w - (h << word_shift);
-    Elem<T>::load8(static_cast<const T*>(a.k) + r * a.k_ts + h * a.k_hs + word * 8, x[c][0]);
-    Elem<T>::load8(static_cast<const T*>(a.v) + r * a.v_ts + h * a.v_hs + word * 8, x[c][1]);
+    x[c][0] = load_raw(static_cast<const T*>(a.k) + r * a.k_ts + h * a.k_hs + word * 8);
+    x[c][1] = load_raw(static_cast<const T*>(a.v) + r * a.v_ts + h * a.v_hs + word * 8);
   }
   const int b = warp_sequence(a.cu, a.b, r);
   if (b < 0) return;
@@ -129,35 +187,40 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4Row
     uint8_t* block = a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(d);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const float(&y)[8] = x[c][which];
-      float lo = y[0], hi = y[0];
-      bool bad = false;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        bad |= !(fabsf(y[j]) <= kKv4Limit);
-        lo = fminf(lo, y[j]);
-        hi = fmaxf(hi, y[j]);
-      }
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(lanes, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o));
-      }
-      bad = __any_sync(lanes, bad);
-      const __half step = __float2half_ru(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+      const float2 range = x[c][which].range(lanes);  // (lo, hi), both NaN when an element is
+      const bool bad = !(range.x >= -kKv4Limit && range.y <= kKv4Limit);
+      const __half step = __float2half_ru(fifteenth(__fsub_rn(range.y, range.x)));
       const float s = __half2float(step);
-      const __half middle = __float2half_rn(__fadd_rn(lo, 8.f * s));
+      const __half middle = __float2half_rn(__fadd_rn(range.x, 8.f * s));
       const float m = __half2float(middle);
       uint32_t codes = 0x88888888u;
       if (!bad && s > 0.f) {
-        const float inv = __frcp_rn(s);
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        constexpr float kRound = 12582912.f;  // 1.5 2^23
+        float2 q[4];
+        float worst = 0.f;  // largest distance from the nearest integer
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          q[j] = fmul2(fsub2(x[c][which].pair(j), make_float2(m, m)), make_float2(inv, inv));
+          const float2 n = fsub2(fadd2(q[j], make_float2(kRound, kRound)), make_float2(kRound, kRound));
+          const float2 e = fsub2(q[j], n);
+          worst = fmaxf(worst, fmaxf(fabsf(e.x), fabsf(e.y)));
+        }
+        if (worst > 0.5f - 0x1p-17f) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = x[c][which].pair(j);
+            q[j] = make_float2(__fdiv_rn(__fsub_rn(y.x, m), s), __fdiv_rn(__fsub_rn(y.y, m), s));
+          }
+        }
         codes = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float diff = __fsub_rn(y[j], m);
-          float q = diff * inv;
-          if (fabsf(q - rintf(q)) > 0.5f - 0x1p-18f) q = __fdiv_rn(diff, s);
-          codes |= (uint32_t)((int)fminf(fmaxf(rintf(q), -8.f), 7.f) + 8) << (4 * j);
+        for (int j = 0; j < 4; ++j) {
+          const float2 u = fadd2(make_float2(fminf(fmaxf(q[j].x, -8.f), 7.f), fminf(fmaxf(q[j].y, -8.f), 7.f)),
+                                 make_float2(kRound + 8.f, kRound + 8.f));
+          codes |= (__float_as_uint(u.x) & 15u) << (8 * j);
+          codes |= (__float_as_uint(u.y) & 15u) << (8 * j + 4);
         }
       }
       *reinterpret_cast<uint32_t*>(block + kv4_codes_at(d, which) + in * kv4_code_bytes(d) + word * 4) = codes;
@@ -245,10 +308,14 @@ cudaError_t launch_rows(const Kv4RowArgs& a) {
 // slots) and, of the others, those of the largest weight, ties going to the lowest slot.  Kept
 // slots keep their order, so the last slots stay the newest.
 //
-// kv4_select_kernel (one block per head): weights as 32-bit keys that order like the numbers
-// (NaN above everything, -0 as 0); the k-th largest key is found digit by digit (11, 11 and 10 bits:
-// three histogram passes over the keys, which stay in L2 or L1); then each warp walks its share of the slots
-// twice, counting and writing those above the threshold key, the first ones equal to it, and the newest.
+// kv4_select_kernel (one block per head, or a cluster of 2 to 8 with a run of the slots each): weights
+// as 32-bit keys that order like the numbers (NaN above everything, -0 as 0); the k-th largest key is found
+// digit by digit (10, 11 and 11 bits: three histogram passes over the keys, which stay in L2 or L1;
+// the blocks of a cluster add up each other's histograms through distributed shared memory, so all find the
+// same digit); then each warp walks its share of the slots twice, counting and writing those above
+// the threshold key, the first ones equal to it, and the newest.  Bound by the shared-memory atomics of
+// the first pass, whose digit (sign, exponent, one bit) takes few values: 16 copies of that histogram, one
+// per pair of lanes.
 // kv4_gather_kernel: one block per 64 kept slots of a head, a block of the new cache, 16 bytes a thread.
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -267,62 +334,95 @@ __device__ __forceinline__ int evict_len(const Kv4EvictArgs& a, int b) {
 }
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32, kSelBins = 2048;
+constexpr int kSelKeys = 16;  // keys of a thread in registers
+constexpr int kSelCopies = 16, kSelFirstBins = 1024;
+constexpr int kSelSmem = (kSelCopies * kSelFirstBins + 2 * kSelBins) * 4;
 
-// Adds this warp's digits to the histogram; lanes that agree throughout (equal weights) add once.
-__device__ __forceinline__ void count_digit(unsigned* hist, bool there, uint32_t digit) {
-  const unsigned all = __ballot_sync(0xffffffffu, there);
-  if (!all) return;
-  int same;
-  __match_all_sync(0xffffffffu, there ? digit : 0xFFFFFFFFu, &same);
-  if (same) {
-    if ((threadIdx.x & 31) == 0) atomicAdd(&hist[digit], 32u);
-  } else if (there) {
-    atomicAdd(&hist[digit], 1u);
-  }
-}
-
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictArgs a) {
-  const int bh = blockIdx.x, b = bh / a.hkv;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
+  auto sync_all = [&]() {
+    if constexpr (CLUSTER) cluster.sync();
+    else __syncthreads();
+  };
+  auto remote = [&](unsigned* p, int j) -> const unsigned* {
+    if constexpr (CLUSTER) return cluster.map_shared_rank(p, j);
+    else return p;
+  };
+  const int bh = blockIdx.x / ctas, b = bh / a.hkv;
   const int n = evict_len(a, b);
   int32_t* kept = a.kept + (int64_t)bh * a.keep;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = min(n, a.keep) + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
-  if (n <= a.keep) {
-    for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
+  for (int i = min(n, a.keep) + rank * kSelThreads + tid; i < a.keep; i += ctas * kSelThreads) kept[i] = -1;
+  if (n <= a.keep) {  // (the whole cluster)
+    for (int i = rank * kSelThreads + tid; i < n; i += ctas * kSelThreads) kept[i] = i;
     return;
   }
   const float* __restrict__ w = a.weights + (int64_t)bh * a.capacity;
   const int m = n - a.recent;       // candidates: slots [0, m)
   const int k = a.keep - a.recent;  // of which k stay, 0 <= k < m
-  __shared__ unsigned hist[kSelBins];
-  __shared__ unsigned warp_sum[kSelWarps], warp_eq[kSelWarps];
+  // this block's slots [lo, hi), whole warps' worth of them
+  const int share = (n + ctas * 32 - 1) / (ctas * 32) * 32;
+  const int lo = min(n, rank * share), hi = min(n, lo + share);
+  // warp j has slots [lo + j * part, lo + (j + 1) * part), lane by lane: key[u] is slot from + u * 32 + lane of the
+  // panel that is loaded.  One panel, as for up to 16384 slots a block, stays in registers throughout.
+  const int part = ((share + kSelThreads - 1) / kSelThreads) * 32;
+  const int from = min(hi, lo + warp * part), to = min(hi, from + part);
+  const int panels = (part + kSelKeys * 32 - 1) / (kSelKeys * 32);
+  uint32_t key[kSelKeys];
+  auto load_panel = [&](int p) {
+#pragma unroll
+    for (int u = 0; u < kSelKeys; ++u) {
+      const int i = from + (p * kSelKeys + u) * 32 + lane;
+      key[u] = i < min(to, m) ? weight_key(w[i]) : 0u;
+    }
+  };
+  if (panels == 1 && k > 0) load_panel(0);
+  // two histograms in turn: the other blocks may still read the last pass's while this one's is filled
+  extern __shared__ unsigned copies[];  // [kSelFirstBins][kSelCopies], then the two histograms
+  unsigned* hist = copies + kSelCopies * kSelFirstBins;
+  __shared__ unsigned warp_sum[kSelWarps], warp_eq[kSelWarps], totals[2];
   __shared__ unsigned sel_digit, sel_left;
   uint32_t prefix = 0, mask = 0;
   unsigned left = (unsigned)k;  // still to take among the keys that match prefix
   if (k > 0) {
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const uint32_t digits = pass == 2 ? 1023u : 2047u;
-      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+      const int shift = pass == 0 ? 22 : (pass == 1 ? 11 : 0);
+      const uint32_t digits = pass == 0 ? 1023u : 2047u;
+      unsigned* mine = hist + (pass & 1) * kSelBins;
+      for (int i = tid; i < kSelBins; i += kSelThreads) mine[i] = 0;
+      if (pass == 0)
+        for (int i = tid; i < kSelCopies * kSelFirstBins; i += kSelThreads) copies[i] = 0;
       __syncthreads();
-      constexpr int U = 8;  // loads in flight
-      for (int base = warp * 32; base < m; base += kSelThreads * U) {
-        uint32_t key[U];
+      for (int p = 0; p < panels; ++p) {
+        if (panels > 1) load_panel(p);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = base + u * kSelThreads + lane;
-          key[u] = i < m ? weight_key(w[i]) : 0u;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = base + u * kSelThreads + lane;
-          count_digit(hist, i < m && (key[u] & mask) == prefix, (key[u] >> shift) & digits);
+        for (int u = 0; u < kSelKeys; ++u) {
+          if (from + (p * kSelKeys + u) * 32 + lane >= min(to, m)) break;
+          if (pass == 0)
+            atomicAdd(&copies[(key[u] >> shift) * kSelCopies + (lane & (kSelCopies - 1))], 1u);
+          else if ((key[u] & mask) == prefix)
+            atomicAdd(&mine[(key[u] >> shift) & digits], 1u);
         }
       }
       __syncthreads();
+      if (pass == 0) {
+        unsigned c = 0;
+#pragma unroll
+        for (int j = 0; j < kSelCopies; ++j) c += copies[tid * kSelCopies + ((j + tid) & (kSelCopies - 1))];
+        mine[tid] = c;  // (the bins above kSelFirstBins stay empty)
+      }
+      sync_all();
       // the digit at which the counts from the top reach `left`: thread t holds bins 2047 - 2t and 2046 - 2t
       const int top = kSelBins - 1 - 2 * tid;
-      const unsigned c0 = hist[top], c1 = hist[top - 1];
+      unsigned c0 = 0, c1 = 0;
+      for (int j = 0; j < ctas; ++j) {
+        const uint2 v = *reinterpret_cast<const uint2*>(remote(mine, j) + top - 1);
+        c1 += v.x;
+        c0 += v.y;
+      }
       unsigned incl = c0 + c1;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -344,55 +444,64 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
       left = sel_left;
     }
   }
-  // slots of key > prefix stay, the first `left` of those equal to it, and the newest; warp j walks the
-  // slots [j * share, (j + 1) * share)
-  const int share = ((n + kSelThreads - 1) / kSelThreads) * 32;
-  const int from = min(n, warp * share), to = min(n, from + share);
-  auto kind = [&](int i, bool* above, bool* equal) {
-    *above = *equal = false;
-    if (i >= to) return;
-    if (i >= m) {
-      *above = true;
-    } else if (k > 0) {
-      const uint32_t key = weight_key(w[i]);
-      *above = key > prefix;
-      *equal = key == prefix;
-    }
+  // slots of key > prefix stay, the first `left` of those equal to it, and the newest
+  auto kind = [&](int i, uint32_t ky, bool* above, bool* equal) {
+    *above = i < to && (i >= m || (k > 0 && ky > prefix));
+    *equal = i < min(to, m) && k > 0 && ky == prefix;
   };
   unsigned na = 0, ne = 0;
-#pragma unroll 4
-  for (int i = from + lane; i - lane < to; i += 32) {
-    bool above, equal;
-    kind(i, &above, &equal);
-    na += above;
-    ne += equal;
+  for (int p = 0; p < panels; ++p) {
+    if (panels > 1 && k > 0) load_panel(p);
+#pragma unroll
+    for (int u = 0; u < kSelKeys; ++u) {
+      bool above, equal;
+      kind(from + (p * kSelKeys + u) * 32 + lane, key[u], &above, &equal);
+      na += above;
+      ne += equal;
+    }
   }
   na = __reduce_add_sync(0xffffffffu, na);
   ne = __reduce_add_sync(0xffffffffu, ne);
+  __syncthreads();  // (warp_sum is read above)
   if (lane == 0) {
     warp_sum[warp] = na;
     warp_eq[warp] = ne;
   }
   __syncthreads();
-  unsigned above_before = 0, eq_before = 0;
-  for (int j = 0; j < warp; ++j) {
-    above_before += warp_sum[j];
-    eq_before += warp_eq[j];
+  unsigned above_before = 0, eq_before = 0, above_all = 0, eq_all = 0;
+  for (int j = 0; j < kSelWarps; ++j) {
+    if (j == warp) above_before = above_all, eq_before = eq_all;
+    above_all += warp_sum[j];
+    eq_all += warp_eq[j];
+  }
+  if (tid == 0) totals[0] = above_all, totals[1] = eq_all;
+  sync_all();
+  for (int j = 0; j < rank; ++j) {
+    const unsigned* t = remote(totals, j);
+    above_before += t[0];
+    eq_before += t[1];
   }
   const unsigned under = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int i = from + lane; i - lane < to; i += 32) {
-    bool above, equal;
-    kind(i, &above, &equal);
-    const unsigned ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
-    const unsigned my_eq = eq_before + __popc(be & under);  // equal ones in front of this slot
-    const unsigned pos = above_before + __popc(ba & under) + min(my_eq, left);
-    if ((above || (equal && my_eq < left)) && pos < (unsigned)a.keep) kept[pos] = i;
-    above_before += __popc(ba);
-    eq_before += __popc(be);
+  for (int p = 0; p < panels; ++p) {
+    if (panels > 1 && k > 0) load_panel(p);
+#pragma unroll
+    for (int u = 0; u < kSelKeys; ++u) {
+      const int i = from + (p * kSelKeys + u) * 32 + lane;
+      if (i - lane >= to) break;
+      bool above, equal;
+      kind(i, key[u], &above, &equal);
+      const unsigned ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
+      const unsigned my_eq = eq_before + __popc(be & under);  // equal ones in front of this slot
+      const unsigned pos = above_before + __popc(ba & under) + min(my_eq, left);
+      if ((above || (equal && my_eq < left)) && pos < (unsigned)a.keep) kept[pos] = i;
+      above_before += __popc(ba);
+      eq_before += __popc(be);
+    }
   }
+  if constexpr (CLUSTER) cluster.sync();  // no block leaves while another may read its shared memory
 }
 
+template <int D>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, int blocks_per_head) {
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.b; b += blockDim.x) a.out_lens[b] = min(min(max(a.lens[b], 0), a.capacity), a.keep);
@@ -402,31 +511,44 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, i
   if (threadIdx.x < kKv4Block)
     from[threadIdx.x] = to0 + (int)threadIdx.x < a.keep ? a.kept[(int64_t)bh * a.keep + to0 + threadIdx.x] : -1;
   __syncthreads();
-  const int d = a.d, pw = kv4_param_words(d);
-  const int shift = d == 64 ? 1 : (d == 128 ? 2 : 3);  // log2 of the 16-byte pieces of a row's codes
-  const uint8_t* src = a.cache + (int64_t)bh * (a.capacity / kKv4Block) * kv4_block_bytes(d);
-  uint8_t* dst = a.out_cache + ((int64_t)bh * (a.out_capacity / kKv4Block) + blk) * kv4_block_bytes(d);
-  // codes of K, then of V: in the order of the new block
-#pragma unroll 2
-  for (int i = threadIdx.x; i < 2 * (kKv4Block << shift); i += blockDim.x) {
-    const int which = i >> (6 + shift), row = (i >> shift) & (kKv4Block - 1), part = i & ((1 << shift) - 1);
-    const int f = from[row];
-    if (f < 0) continue;
-    const uint8_t* sb = src + (int64_t)(f / kKv4Block) * kv4_block_bytes(d) + kv4_codes_at(d, which) +
-                        (f % kKv4Block) * kv4_code_bytes(d);
-    *reinterpret_cast<uint4*>(dst + i * 16) = *reinterpret_cast<const uint4*>(sb + part * 16);
+  constexpr int BYTES = kv4_block_bytes(D), PW = kv4_param_words(D);
+  constexpr int PER = D / 32;                   // 16-byte pieces of a row's codes
+  constexpr int N = 2 * kKv4Block * PER / 256;  // pieces of a thread: K codes, then V codes, in the new block's order
+  constexpr int NP = (2 * kKv4Block * PW + 255) / 256;
+  const uint8_t* src = a.cache + (int64_t)bh * (a.capacity / kKv4Block) * BYTES;
+  uint8_t* dst = a.out_cache + ((int64_t)bh * (a.out_capacity / kKv4Block) + blk) * BYTES;
+  auto row_of = [&](int f, int at, int row_bytes) {
+    return src + (int64_t)(f / kKv4Block) * BYTES + at + (f % kKv4Block) * row_bytes;
+  };
+  uint4 codes[N];
+  uint32_t par[NP];
+  float w = 0.f;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int i = u * 256 + threadIdx.x, which = i / (kKv4Block * PER), row = (i / PER) % kKv4Block;
+    if (from[row] >= 0)
+      codes[u] = *reinterpret_cast<const uint4*>(row_of(from[row], kv4_codes_at(D, which), kv4_code_bytes(D)) + i % PER * 16);
   }
-  for (int i = threadIdx.x; i < 2 * kKv4Block * pw; i += blockDim.x) {
-    const int which = i / (kKv4Block * pw), rest = i - which * (kKv4Block * pw), row = rest / pw;
-    const int f = from[row];
-    if (f < 0) continue;
-    const uint8_t* sb = src + (int64_t)(f / kKv4Block) * kv4_block_bytes(d) + kv4_params_at(d, which) +
-                        ((f % kKv4Block) * pw + rest % pw) * 4;
-    *reinterpret_cast<uint32_t*>(dst + kv4_params_at(d, 0) + i * 4) = *reinterpret_cast<const uint32_t*>(sb);
+#pragma unroll
+  for (int u = 0; u < NP; ++u) {
+    const int i = u * 256 + threadIdx.x, which = i / (kKv4Block * PW), row = (i / PW) % kKv4Block;
+    if (i < 2 * kKv4Block * PW && from[row] >= 0)
+      par[u] = *reinterpret_cast<const uint32_t*>(row_of(from[row], kv4_params_at(D, which), PW * 4) + i % PW * 4);
   }
-  if (threadIdx.x < kKv4Block && from[threadIdx.x] >= 0)
-    a.out_weights[(int64_t)bh * a.out_capacity + to0 + threadIdx.x] =
-        a.weights[(int64_t)bh * a.capacity + from[threadIdx.x]];
+  const bool weighted = threadIdx.x < kKv4Block && from[threadIdx.x % kKv4Block] >= 0;
+  if (weighted) w = a.weights[(int64_t)bh * a.capacity + from[threadIdx.x]];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int i = u * 256 + threadIdx.x;
+    if (from[(i / PER) % kKv4Block] >= 0) *reinterpret_cast<uint4*>(dst + i * 16) = codes[u];
+  }
+#pragma unroll
+  for (int u = 0; u < NP; ++u) {
+    const int i = u * 256 + threadIdx.x;
+    if (i < 2 * kKv4Block * PW && from[(i / PW) % kKv4Block] >= 0)
+      *reinterpret_cast<uint32_t*>(dst + kv4_params_at(D, 0) + i * 4) = par[u];
+  }
+  if (weighted) a.out_weights[(int64_t)bh * a.out_capacity + to0 + threadIdx.x] = w;
 }
 
 }  // namespace
@@ -435,11 +557,39 @@ cudaError_t launch_kv4_append(const Kv4RowArgs& a) { return launch_rows<false>(a
 cudaError_t launch_kv4_read(const Kv4RowArgs& a) { return launch_rows<true>(a); }
 
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
-  kv4_select_kernel<<<a.b * a.hkv, kSelThreads, 0, a.stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // blocks per head: as many as there are SMs for (a block's registers fill one), while each has some
+  // thousand slots
+  int ctas = 1;
+  while (ctas < 8 && (int64_t)a.b * a.hkv * ctas * 2 <= device_sm_count() && a.capacity / (ctas * 2) >= 2048) ctas *= 2;
+  static std::atomic<unsigned long long> allowed[2];
+  cudaError_t e = ctas > 1 ? allow_smem(kv4_select_kernel<true>, kSelSmem, &allowed[1])
+                           : allow_smem(kv4_select_kernel<false>, kSelSmem, &allowed[0]);
+  if (e != cudaSuccess) return e;
+  if (ctas == 1) {
+    kv4_select_kernel<false><<<a.b * a.hkv, kSelThreads, kSelSmem, a.stream>>>(a);
+    e = cudaGetLastError();
+  } else {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.b * a.hkv * ctas));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = kSelSmem;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kv4_select_kernel<true>, a);
+  }
   if (e != cudaSuccess) return e;
   const int per_head = (a.keep + kKv4Block - 1) / kKv4Block;
-  kv4_gather_kernel<<<(unsigned)per_head * a.b * a.hkv, 256, 0, a.stream>>>(a, per_head);
+  const unsigned grid = (unsigned)per_head * a.b * a.hkv;
+  switch (a.d) {
+    case 64: kv4_gather_kernel<64><<<grid, 256, 0, a.stream>>>(a, per_head); break;
+    case 128: kv4_gather_kernel<128><<<grid, 256, 0, a.stream>>>(a, per_head); break;
+    default: kv4_gather_kernel<256><<<grid, 256, 0, a.stream>>>(a, per_head);
+  }
   return cudaGetLastError();
 }
 
