@@ -237,6 +237,12 @@ __device__ __forceinline__ void run_blocks(int64_t seg, int nb, int64_t u0, int6
 // in this CTA's run and goes on), [ROWS][D] unnormalised O and [ROWS][2] (m, l).
 __host__ __device__ __forceinline__ size_t partial_floats(int rows, int d) { return (size_t)rows * (d + 2); }
 
+// i modulo N for -N < i < N
+template <int N>
+__device__ __forceinline__ int turn(int i) {
+  return i < 0 ? i + N : i;
+}
+
 // Log-sum-exp in log2 units of a row's (reference, sum): -inf where it saw nothing, NaN where it saw one
 __device__ __forceinline__ float log_sum(float m, float l) {
   return l > 0.f ? m - kPShift + log2f(l) : (isnan(l) ? l : -INFINITY);
@@ -296,8 +302,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
         int first, end;
         run_blocks(p.seg, p.nb, u0, u1, &first, &end);
         load_u = p.seg + WorkList::positions(p.nb);
-        const int mine = first + ((team - load_rot) & (C::TEAMS - 1));
-        load_rot += end - first;
+        const int mine = first + turn<C::TEAMS>(team - load_rot);
+        load_rot = (load_rot + end - first) % C::TEAMS;
         if (mine < end) {
           const int hk = p.hr / row_groups;
           load_src = a.cache + (((int64_t)p.b * a.hkv + hk) * (a.capacity / kKv4Block) + mine) * C::BLOCK;
@@ -414,7 +420,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o_acc[i][nt][e] = 0.f;
 
-    for (int blk = blk0 + ((team - rot) & (C::TEAMS - 1)); ok && blk < blk1; blk += C::TEAMS) {
+    for (int blk = blk0 + turn<C::TEAMS>(team - rot); ok && blk < blk1; blk += C::TEAMS) {
       const int s = uses % C::STAGES;
       ok = __all_sync(0xffffffffu, mbar_wait(full + s, (uint32_t)(uses / C::STAGES) & 1, ctx, kSiteKv4Full));
       if (!ok) break;
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
       }
     // (a warp whose team had none of these blocks has m = -inf, l = 0 and is left out of the sums of O)
     const int nblk = blk1 - blk0;
-    auto active = [&](int w) { return ((w / C::TEAM - rot) & (C::TEAMS - 1)) < nblk; };
+    auto active = [&](int w) { return turn<C::TEAMS>(w / C::TEAM - rot) < nblk; };
     __syncthreads();
     float* fac = obuf + C::NW * C::ROWS * C::OSTRIDE;  // [NW][ROWS] weight of each warp's sums, then [ROWS][2] (m, l)
     float* mlt = fac + C::NW * C::ROWS;
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
       }
       __syncthreads();
     }
-    rot += nblk;
+    rot = (rot + nblk) % C::TEAMS;
     if (*abort_flag) break;
   }
   // every copy must land before the CTA may exit
