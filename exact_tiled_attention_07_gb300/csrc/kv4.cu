@@ -47,10 +47,10 @@ struct Elem<float> {
 };
 
 // Smallest and largest of a group's 64 elements, eight in this lane (raw: as loaded) and the rest in the
-// other seven lanes of `lanes`; NaN when one of them is.  16-bit elements stay packed: the minimum and
+// other seven lanes of the group; NaN when one of them is.  16-bit elements stay packed: the minimum and
 // the negated maximum share a register through the shuffles.
-template <typename T2, typename T>
-__device__ __forceinline__ float2 packed_range(const uint32_t (&w)[4], unsigned lanes) {
+template <typename T2>
+__device__ __forceinline__ float2 packed_range(const uint32_t (&w)[4]) {
   const T2* v = reinterpret_cast<const T2*>(w);
   const T2 mn = __hmin2_nan(__hmin2_nan(v[0], v[1]), __hmin2_nan(v[2], v[3]));
   const T2 mx = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
@@ -59,12 +59,17 @@ __device__ __forceinline__ float2 packed_range(const uint32_t (&w)[4], unsigned 
   r.y = __hneg(__hmax_nan(mx.x, mx.y));
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) {
-    const uint32_t u = __shfl_xor_sync(lanes, *reinterpret_cast<const uint32_t*>(&r), o);
+    const uint32_t u = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&r), o);
     r = __hmin2_nan(r, *reinterpret_cast<const T2*>(&u));
   }
   return make_float2((float)r.x, -(float)r.y);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -76,13 +81,13 @@ struct Raw;  // eight elements as loaded
 template <>
 struct Raw<__nv_bfloat16> {
   uint32_t w[4];
-  __device__ __forceinline__ float2 range(unsigned lanes) const { return packed_range<__nv_bfloat162, __nv_bfloat16>(w, lanes); }
+  __device__ __forceinline__ float2 range() const { return packed_range<__nv_bfloat162>(w); }
   __device__ __forceinline__ float2 pair(int i) const { return unpack2<true>(w[i]); }
 };
 template <>
 struct Raw<__half> {
   uint32_t w[4];
-  __device__ __forceinline__ float2 range(unsigned lanes) const { return packed_range<__half2, __half>(w, lanes); }
+  __device__ __forceinline__ float2 range() const { return packed_range<__half2>(w); }
   __device__ __forceinline__ float2 pair(int i) const { return unpack2<false>(w[i]); }
 };
 template <>
@@ -91,7 +96,7 @@ struct Raw<float> {
   __device__ __forceinline__ float2 pair(int i) const {
     return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
   }
-  __device__ __forceinline__ float2 range(unsigned lanes) const {
+  __device__ __forceinline__ float2 range() const {
     float lo = __uint_as_float(w[0]), nhi = -lo;
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
@@ -100,8 +105,8 @@ struct Raw<float> {
     }
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(lanes, lo, o));
-      nhi = min_nan(nhi, __shfl_xor_sync(lanes, nhi, o));
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      nhi = min_nan(nhi, __shfl_xor_sync(0xffffffffu, nhi, o));
     }
     return make_float2(lo, -nhi);
   }
@@ -154,22 +159,22 @@ constexpr int kRowWarps = 8;  // rows of a block: one warp each
 // 16-bit elements, keys and values, before anything else is known; the 8 lanes of a group find its minimum and
 // maximum together and a lane's codes are one 32-bit word.  Bytes: 16 in, 4.5 out for 8 channels.  The quotient is
 // taken as a product with an approximate 1 / step (2^-23), which is within 2^-19 of the IEEE quotient
-// for |quotient| <= 8.5; only where it lies within 2^-17 of a half (where that could change the rounding) is
-// the division done.  Rounding to an integer is an addition of 1.5 2^23, which leaves it in the low bits;
-// rint and the conversion to int instead (16 a clock on an SM) cost 109 us against %APPEND% for 34,001 rows of 8 heads
-// of 128 bf16 channels.
-template <typename T, int CH>
-__global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4RowArgs a, int word_shift) {
+// for |quotient| <= 8.5; only where one lies within 2^-17 of a half (where that could change the rounding) or
+// beyond the codes is the division done.  Rounding to an integer is an addition of 1.5 2^23 and its
+// subtraction, and four codes are put together by multiply-adds: conversions to int (16 a clock on an SM)
+// and shifts and masks (64) instead cost 109 and 58 us, against %APPEND% us, for 34,001 rows of 8 heads of 128 bf16 channels.
+template <typename T, int D, int CH>
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4RowArgs a) {
+  constexpr int kWords = D / 8;  // of a row of one head
   const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= a.t) return;
-  const int words = a.hkv << word_shift;  // of a row
+  const int words = a.hkv * kWords;
   const int w0 = blockIdx.y * (CH * 32) + lane;
   Raw<T> x[CH][2];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int w = w0 + c * 32;
-    if (w >= words) continue;
-    const int h = w >> word_shift, word = w - (h << word_shift);
+    const int w = min(w0 + c * 32, words - 1);  // (lanes behind the row go along, so that the shuffles are whole)
+    const int h = w / kWords, word = w % kWords;
     x[c][0] = load_raw(static_cast<const T*>(a.k) + r * a.k_ts + h * a.k_hs + word * 8);
     x[c][1] = load_raw(static_cast<const T*>(a.v) + r * a.v_ts + h * a.v_hs + word * 8);
   }
@@ -177,17 +182,16 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4Row
   if (b < 0) return;
   int64_t slot;
   if (!row_slot(a, r, b, &slot, kSiteAppend)) return;
-  const int d = a.d, in = (int)(slot % kKv4Block);
-  const unsigned lanes = 0xFFu << (lane & 24);
+  const int in = (int)(slot % kKv4Block);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int w = w0 + c * 32;
-    if (w >= words) continue;  // (words is a multiple of 8: a group's lanes go together)
-    const int h = w >> word_shift, word = w - (h << word_shift);
-    uint8_t* block = a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(d);
+    const bool there = w0 + c * 32 < words;  // (words is a multiple of 8: a group's lanes go together)
+    const int w = min(w0 + c * 32, words - 1);
+    const int h = w / kWords, word = w % kWords;
+    uint8_t* block = a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(D);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const float2 range = x[c][which].range(lanes);  // (lo, hi), both NaN when an element is
+      const float2 range = x[c][which].range();  // (lo, hi), both NaN when an element is
       const bool bad = !(range.x >= -kKv4Limit && range.y <= kKv4Limit);
       const __half step = __float2half_ru(fifteenth(__fsub_rn(range.y, range.x)));
       const float s = __half2float(step);
@@ -198,75 +202,77 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4Row
         float inv;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
         constexpr float kRound = 12582912.f;  // 1.5 2^23
-        float2 q[4];
+        float2 n[4];
         float worst = 0.f;  // largest distance from the nearest integer
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          q[j] = fmul2(fsub2(x[c][which].pair(j), make_float2(m, m)), make_float2(inv, inv));
-          const float2 n = fsub2(fadd2(q[j], make_float2(kRound, kRound)), make_float2(kRound, kRound));
-          const float2 e = fsub2(q[j], n);
-          worst = fmaxf(worst, fmaxf(fabsf(e.x), fabsf(e.y)));
+          const float2 q = fmul2(fsub2(x[c][which].pair(j), make_float2(m, m)), make_float2(inv, inv));
+          n[j] = fsub2(fadd2(q, make_float2(kRound, kRound)), make_float2(kRound, kRound));
+          const float2 e = fsub2(q, n[j]);
+          worst = max3(worst, fabsf(e.x), fabsf(e.y));
         }
-        if (worst > 0.5f - 0x1p-17f) {
+        // (the quotients lie between those of lo and hi: where these round to -8 and 7 at the most, none is clamped)
+        const bool clamped = !((range.x - m) * inv > -8.49f && (range.y - m) * inv < 7.49f);
+        if (worst > 0.5f - 0x1p-17f || clamped) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = x[c][which].pair(j);
-            q[j] = make_float2(__fdiv_rn(__fsub_rn(y.x, m), s), __fdiv_rn(__fsub_rn(y.y, m), s));
+          for (int j = 0; j < 8; ++j) {
+            const float2 y = x[c][which].pair(j / 2);
+            const float diff = __fsub_rn(j & 1 ? y.y : y.x, m);
+            float& r = j & 1 ? n[j / 2].y : n[j / 2].x;
+            if (clamped || fabsf(diff * inv - r) > 0.5f - 0x1p-17f) r = fminf(fmaxf(rintf(__fdiv_rn(diff, s)), -8.f), 7.f);
           }
         }
-        codes = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 u = fadd2(make_float2(fminf(fmaxf(q[j].x, -8.f), 7.f), fminf(fmaxf(q[j].y, -8.f), 7.f)),
-                                 make_float2(kRound + 8.f, kRound + 8.f));
-          codes |= (__float_as_uint(u.x) & 15u) << (8 * j);
-          codes |= (__float_as_uint(u.y) & 15u) << (8 * j + 4);
-        }
+        // four codes to a sum of codes times powers of 16, exact, which the offset brings to the low 16 bits
+        const float a0 = fmaf(fmaf(n[1].y, 16.f, n[1].x), 256.f, fmaf(n[0].y, 16.f, n[0].x)) + (kRound + 34952.f);
+        const float a1 = fmaf(fmaf(n[3].y, 16.f, n[3].x), 256.f, fmaf(n[2].y, 16.f, n[2].x)) + (kRound + 34952.f);
+        codes = __byte_perm(__float_as_uint(a0), __float_as_uint(a1), 0x5410);
       }
-      *reinterpret_cast<uint32_t*>(block + kv4_codes_at(d, which) + in * kv4_code_bytes(d) + word * 4) = codes;
+      if (!there) continue;
+      *reinterpret_cast<uint32_t*>(block + kv4_codes_at(D, which) + in * kv4_code_bytes(D) + word * 4) = codes;
       if ((word & 7) == 0) {
         const uint32_t par = bad ? kKv4NanParam
                                  : (uint32_t)__half_as_ushort(step) | ((uint32_t)__half_as_ushort(middle) << 16);
-        *reinterpret_cast<uint32_t*>(block + kv4_params_at(d, which) + (in * kv4_param_words(d) + (word >> 3)) * 4) = par;
+        *reinterpret_cast<uint32_t*>(block + kv4_params_at(D, which) + (in * kv4_param_words(D) + (word >> 3)) * 4) = par;
       }
     }
-    if (a.weights && word == 0) a.weights[((int64_t)b * a.hkv + h) * a.capacity + slot] = 0.f;
+    if (a.weights && there && word == 0) a.weights[((int64_t)b * a.hkv + h) * a.capacity + slot] = 0.f;
   }
 }
 
 // The inverse, with the same split: middle + step (code - 8) in fp32, rounded once.
-template <typename T, int CH>
-__global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const Kv4RowArgs a, int word_shift) {
+template <typename T, int D, int CH>
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const Kv4RowArgs a) {
+  constexpr int kWords = D / 8;
   const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= a.t) return;
-  const int words = a.hkv << word_shift;
+  const int words = a.hkv * kWords;
   const int w0 = blockIdx.y * (CH * 32) + lane;
   const int b = warp_sequence(a.cu, a.b, r);
   if (b < 0) return;
   int64_t slot;
   if (!row_slot(a, r, b, &slot, kSiteRead)) return;
-  const int d = a.d, in = (int)(slot % kKv4Block);
+  const int in = (int)(slot % kKv4Block);
   uint32_t codes[CH][2], par[CH][2];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int w = w0 + c * 32;
     if (w >= words) continue;
-    const int h = w >> word_shift, word = w - (h << word_shift);
+    const int h = w / kWords, word = w % kWords;
     const uint8_t* block =
-        a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(d);
+        a.cache + (((int64_t)b * a.hkv + h) * (a.capacity / kKv4Block) + slot / kKv4Block) * kv4_block_bytes(D);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       codes[c][which] =
-          *reinterpret_cast<const uint32_t*>(block + kv4_codes_at(d, which) + in * kv4_code_bytes(d) + word * 4);
-      par[c][which] = *reinterpret_cast<const uint32_t*>(block + kv4_params_at(d, which) +
-                                                         (in * kv4_param_words(d) + (word >> 3)) * 4);
+          *reinterpret_cast<const uint32_t*>(block + kv4_codes_at(D, which) + in * kv4_code_bytes(D) + word * 4);
+      par[c][which] = *reinterpret_cast<const uint32_t*>(block + kv4_params_at(D, which) +
+                                                         (in * kv4_param_words(D) + (word >> 3)) * 4);
     }
   }
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int w = w0 + c * 32;
     if (w >= words) continue;
-    const int h = w >> word_shift, word = w - (h << word_shift);
+    const int h = w / kWords, word = w % kWords;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const float2 p = unpack2<false>(par[c][which]);
@@ -281,16 +287,21 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const Kv4RowAr
 }
 
 // Two chunks of 32 words a warp (one where a row has no more) keep 64 bytes a lane in flight.
-template <bool READ, typename T>
-cudaError_t launch_rows_t(const Kv4RowArgs& a) {
-  const int shift = a.d == 64 ? 3 : (a.d == 128 ? 4 : 5);
-  const int words = a.hkv << shift;
+template <bool READ, typename T, int D>
+cudaError_t launch_rows_d(const Kv4RowArgs& a) {
+  const int words = a.hkv * (D / 8);
   const int ch = words > 32 ? 2 : 1;
   const dim3 grid((unsigned)((a.t + kRowWarps - 1) / kRowWarps), (unsigned)((words + 32 * ch - 1) / (32 * ch)));
-  auto kern = READ ? (ch == 2 ? kv4_read_kernel<T, 2> : kv4_read_kernel<T, 1>)
-                   : (ch == 2 ? kv4_append_kernel<T, 2> : kv4_append_kernel<T, 1>);
-  kern<<<grid, kRowWarps * 32, 0, a.stream>>>(a, shift);
+  auto kern = READ ? (ch == 2 ? kv4_read_kernel<T, D, 2> : kv4_read_kernel<T, D, 1>)
+                   : (ch == 2 ? kv4_append_kernel<T, D, 2> : kv4_append_kernel<T, D, 1>);
+  kern<<<grid, kRowWarps * 32, 0, a.stream>>>(a);
   return cudaGetLastError();
+}
+
+template <bool READ, typename T>
+cudaError_t launch_rows_t(const Kv4RowArgs& a) {
+  return a.d == 64 ? launch_rows_d<READ, T, 64>(a)
+                   : (a.d == 128 ? launch_rows_d<READ, T, 128>(a) : launch_rows_d<READ, T, 256>(a));
 }
 
 template <bool READ>
