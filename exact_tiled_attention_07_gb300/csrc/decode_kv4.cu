@@ -747,7 +747,6 @@ __global__ void __launch_bounds__(kFinishThreads)
     decode_kv4_finish(const DecodeKv4Args a, const float* __restrict__ part, const float* __restrict__ scores,
                       int row_groups, int ctas) {
   constexpr int ROWS = 8 * NT;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int hr_count = a.hkv * row_groups;
   const int segments = a.b * hr_count;
   const int R = (a.h / a.hkv) * a.nq;
@@ -760,6 +759,8 @@ __global__ void __launch_bounds__(kFinishThreads)
     const int64_t first = before + (int64_t)hr * WorkList::positions(nb) + kSegCost;
     return Partials<D, ROWS>{part, run_of(total, first, G), run_of(total, first + nb - 1, G)};
   };
+  // The lengths are older than the runs (the decode kernel itself started only when all before it was
+  // done), so only what follows has to wait for them.
   if ((int)blockIdx.x < segments) {
     const int b = blockIdx.x / hr_count, hr = blockIdx.x - b * hr_count;
     const int hk = hr / row_groups, rg = hr - hk * row_groups;
@@ -768,13 +769,15 @@ __global__ void __launch_bounds__(kFinishThreads)
     if (hr == 0 && threadIdx.x == 0 && clamp_len(a.lens[b], a.capacity) != a.lens[b])
       report_error(a.err, DERR_BAD_ARG, kSiteKv4Len);
     const int nb = wl.blocks(b);
+    const int64_t before = wl.total(b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (nb == 0) {
       for (int i = threadIdx.x; i < rows * D / 2; i += kFinishThreads)
         reinterpret_cast<uint32_t*>(a.o)[row0 * D / 2 + i] = 0u;
       for (int i = threadIdx.x; i < rows; i += kFinishThreads) a.lse[row0 + i] = -INFINITY;
       return;
     }
-    const Partials<D, ROWS> P = partials(wl.total(b), nb, hr);
+    const Partials<D, ROWS> P = partials(before, nb, hr);
     if (P.g0 == P.g1) return;
     const int n = P.g1 - P.g0 + 1;
     // each row's reference and sum, and each partial's weight: one warp a row
@@ -823,6 +826,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (slot0 - (int)threadIdx.x >= len) return;
   const int nb = blocks_of(len);
   const int64_t before = wl.total(b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int WT = kWeightSlots / kFinishThreads;
   const int64_t at = (int64_t)bh * a.capacity + slot0;
   float w[WT], w_in[WT];
