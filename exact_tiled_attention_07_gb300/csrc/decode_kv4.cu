@@ -57,21 +57,26 @@ struct Kv4Cfg {
   static constexpr int ROWS = 8 * NT;     // query rows of a CTA
   static constexpr int GROUPS = D / 64;   // parameter groups of a row
   static constexpr int BLOCK = kv4_block_bytes(D);
-  // 16 warps where 128 registers a thread hold a row tile's accumulators, else 8
-  static constexpr int NW = NT == 1 && D <= 128 ? 16 : 8;
-  static constexpr int TEAM = D == 256 || (D == 128 && NW == 16) ? 2 : 1;  // warps that share a block
+  // CTAs of an SM: two where 128 registers a thread hold a row tile's accumulators, so that one's start and end of a
+  // segment run under the other's loop
+  static constexpr int CTAS = NT == 1 && D <= 128 ? 2 : 1;
+  static constexpr int NW = 8;  // warps
+  static constexpr int TEAM = D == 256 || (D == 128 && CTAS == 2) ? 2 : 1;  // warps that share a block
   static constexpr int TEAMS = NW / TEAM;
   static constexpr int TOK = 64 / TEAM;   // tokens of a block for one warp
-  static constexpr int STAGES = D == 64 && NW == 8 ? 4 : 2;
+  static constexpr int STAGES = D == 64 && CTAS == 1 ? 4 : 2;
   static constexpr int THREADS = NW * 32;
-  static constexpr int OSTRIDE = 64 + 4;  // floats of a row in the exchange buffer
+  // channels that the warps exchange at a time (a whole row where two CTAs have the shared memory for it)
+  static constexpr int OCH = NT == 1 && D <= 128 ? D : 64;
+  static constexpr int OSTRIDE = OCH + 4;  // floats of a row in the exchange buffer
   static constexpr int OFF_RING = 0;
   static constexpr int OFF_O = TEAMS * STAGES * BLOCK;                // [NW][ROWS][OSTRIDE] fp32
   static constexpr int OFF_ML = OFF_O + (NW * ROWS * OSTRIDE + NW * ROWS + ROWS * 2) * 4;  // [NW][ROWS][2] fp32
   static constexpr int OFF_BAR = OFF_ML + NW * ROWS * 2 * 4;
   static constexpr int NBAR = 2 * TEAMS * STAGES;  // full, then empty
-  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
-  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr int OFF_LIST = OFF_BAR + NBAR * 8 + 16;  // [TEAMS] ListPlace
+  static constexpr int SMEM = OFF_LIST + TEAMS * 40;
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024 && SMEM <= 232448, "shared memory");
   static_assert(BLOCK % 16 == 0 && OFF_O % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 };
 
@@ -146,7 +151,7 @@ __device__ __forceinline__ int blocks_of(int n) { return (n + kKv4Block - 1) / k
 // The list: sequences, then their heads x row groups (segments), then the segment's nb blocks, each a
 // position, behind kSegCost positions that stand for what a segment costs whatever its length (its queries, joining
 // the warps, its output: about the time of that many blocks).
-constexpr int kSegCost = 12;
+constexpr int kSegCost = 10;
 
 struct Cursor {
   int64_t first;  // list position of sequence b's first segment
@@ -233,6 +238,15 @@ __device__ __forceinline__ void run_blocks(int64_t seg, int nb, int64_t u0, int6
   *end = (int)max((int64_t)*first, min((int64_t)nb, u1 - at));
 }
 
+// Where a loading thread is in the list: kept in shared memory, as it is needed once a segment and would cost
+// registers in the loop over the blocks.
+struct ListPlace {
+  Cursor c;
+  int64_t u;  // list position of the segment to load from next
+  int rot;    // blocks of the run before it, modulo the teams
+};
+static_assert(sizeof(ListPlace) == 40, "size");
+
 // Partials of the merge: per CTA two slots (0: a segment that began in an earlier CTA's run, 1: one that began
 // in this CTA's run and goes on), [ROWS][D] unnormalised O and [ROWS][2] (m, l).
 __host__ __device__ __forceinline__ size_t partial_floats(int rows, int d) { return (size_t)rows * (d + 2); }
@@ -249,7 +263,7 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 }
 
 template <int D, bool BF16, int NT, bool SCORES>
-__global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
+__global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
     decode_kv4_kernel(const DecodeKv4Args a, float* __restrict__ part, float* __restrict__ scores, int row_groups) {
   using C = Kv4Cfg<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -280,13 +294,12 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
   // Blocks go to the teams in turn: of a segment's blocks [first, end) in this run, team (rot + i) % TEAMS takes
   // first + i, where rot counts the run's blocks before.  A team's i-th block of the run is in slot i % STAGES.
   uint8_t* ring = smem + C::OFF_RING + team * C::STAGES * C::BLOCK;
-  Cursor ahead = wl.find(u0);
-  Cursor here = ahead;
+  Cursor here = wl.find(u0);
+  ListPlace* lists = reinterpret_cast<ListPlace*>(smem + C::OFF_LIST);
   int loads = 0, uses = 0;
   const bool loader = half == 0 && lane == 0;
   bool ok = true;
-  int64_t load_u = u0;  // list position of the segment to load from next
-  int load_rot = 0;
+  if (loader) lists[team] = ListPlace{here, u0, 0};
   bool load_ok = true;  // (when a wait of the loader runs out, the teams' waits for their blocks run out too)
   const uint8_t* load_src = nullptr;  // the block loaded last, and how many blocks of its segment's part follow it
   int load_left = 0;
@@ -297,13 +310,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
       load_left -= C::TEAMS;
     } else {
       load_left = -1;
-      while (load_left < 0 && load_u < u1) {
-        const Place p = wl.at(ahead, load_u);
+      ListPlace& at = lists[team];
+      while (load_left < 0 && at.u < u1) {
+        const Place p = wl.at(at.c, at.u);
         int first, end;
         run_blocks(p.seg, p.nb, u0, u1, &first, &end);
-        load_u = p.seg + WorkList::positions(p.nb);
-        const int mine = first + turn<C::TEAMS>(team - load_rot);
-        load_rot = (load_rot + end - first) % C::TEAMS;
+        at.u = p.seg + WorkList::positions(p.nb);
+        const int mine = first + turn<C::TEAMS>(team - at.rot);
+        at.rot = (at.rot + end - first) % C::TEAMS;
         if (mine < end) {
           const int hk = p.hr / row_groups;
           load_src = a.cache + (((int64_t)p.b * a.hkv + hk) * (a.capacity / kKv4Block) + mine) * C::BLOCK;
@@ -671,22 +685,22 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
     const bool whole = nblk == sp.nb;
     float* slot = part + ((size_t)blockIdx.x * 2 + (blk0 == 0 ? 1 : 0)) * partial_floats(C::ROWS, D);
 #pragma unroll 1
-    for (int cc = 0; cc < D / 64; ++cc) {
+    for (int cc = 0; cc < D / C::OCH; ++cc) {
       if (active(warp)) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          if (i / 4 != cc) continue;
+          if (i / (C::OCH / 16) != cc) continue;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              *reinterpret_cast<float2*>(obuf + (warp * C::ROWS + nt * 8 + 2 * t + e) * C::OSTRIDE + g * 8 +
-                                         (i % 4) * 2) = make_float2(o_acc[i][nt][e], o_acc[i][nt][2 + e]);
+              *reinterpret_cast<float2*>(obuf + (warp * C::ROWS + nt * 8 + 2 * t + e) * C::OSTRIDE +
+                                         (i / 4 * 64) % C::OCH + g * 8 + (i % 4) * 2) = make_float2(o_acc[i][nt][e], o_acc[i][nt][2 + e]);
         }
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < C::ROWS * 32; i += C::THREADS) {
-        const int row = i / 32, c2 = i % 32;  // channel pair
+      for (int i = threadIdx.x; i < C::ROWS * (C::OCH / 2); i += C::THREADS) {
+        const int row = i / (C::OCH / 2), c2 = i % (C::OCH / 2);  // channel pair
         float2 v = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < C::NW; ++w)
@@ -696,7 +710,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, 1)
             v.x = fmaf(x.x, f, v.x);
             v.y = fmaf(x.y, f, v.y);
           }
-        const int ch = cc * 64 + c2 * 2;
+        const int ch = cc * C::OCH + c2 * 2;
         if (row0 + row < R) {
           const float2 st = *reinterpret_cast<const float2*>(mlt + row * 2);
           if (whole) {
@@ -736,7 +750,7 @@ struct Partials {
 
 constexpr int kFinishThreads = 256;
 constexpr int kWeightSlots = 4 * kFinishThreads;  // slots of a head whose weights a block of the finish adds up
-constexpr int kMaxRuns = 512;  // CTAs of the decode kernel, at most (one per SM)
+constexpr int kMaxRuns = 512;  // CTAs of the decode kernel, at most
 
 // What is left when the runs are done.  Blocks [0, segments): the segments that several CTAs' runs cut
 // are joined from their partials, in the order of the CTAs, and the rows of empty sequences are
@@ -881,10 +895,13 @@ __global__ void __launch_bounds__(kFinishThreads)
 // read once for 16; d = 256 has no registers for two (768 bytes of spills).
 int row_tiles(int h, int hkv, int nq, int d) { return ((h / hkv) * nq > 8 && d < 256) ? 2 : 1; }
 
-// CTAs of the decode kernel: one per SM, no more than there can be blocks
-int grid_size(int b, int hkv, int row_groups, int capacity) {
+// CTAs of the decode kernel: as many as run at once, no more than there can be blocks
+int grid_size(int b, int hkv, int row_groups, int capacity, int ctas) {
   const int64_t most = (int64_t)b * hkv * row_groups * (capacity / kKv4Block);
-  return (int)std::min<int64_t>(most, std::min(device_sm_count(), kMaxRuns));
+  return (int)std::min<int64_t>(most, std::min(ctas * device_sm_count(), kMaxRuns));
+}
+int ctas_per_sm(int d, int row_tiles) {
+  return row_tiles == 2 ? Kv4Cfg<128, 2>::CTAS : (d == 256 ? Kv4Cfg<256, 1>::CTAS : Kv4Cfg<128, 1>::CTAS);
 }
 
 template <int D, bool BF16, int NT>
@@ -892,7 +909,7 @@ cudaError_t launch_nt(const DecodeKv4Args& a) {
   using C = Kv4Cfg<D, NT>;
   const int R = (a.h / a.hkv) * a.nq;
   const int row_groups = (R + C::ROWS - 1) / C::ROWS;
-  const int G = grid_size(a.b, a.hkv, row_groups, a.capacity);
+  const int G = grid_size(a.b, a.hkv, row_groups, a.capacity, C::CTAS);
   float* part = static_cast<float*>(a.ws);
   float* scores = part + (size_t)G * 2 * partial_floats(C::ROWS, D);
   auto kern = a.w_out ? decode_kv4_kernel<D, BF16, NT, true> : decode_kv4_kernel<D, BF16, NT, false>;
@@ -927,10 +944,10 @@ cudaError_t launch_d(const DecodeKv4Args& a) {
 }  // namespace
 
 size_t decode_kv4_workspace_bytes(int b, int h, int hkv, int nq, int capacity, int d, bool weights) {
-  const int rows = 8 * row_tiles(h, hkv, nq, d);
+  const int nt = row_tiles(h, hkv, nq, d), rows = 8 * nt;
   const int R = (h / hkv) * nq;
   const int row_groups = (R + rows - 1) / rows;
-  size_t n = (size_t)grid_size(b, hkv, row_groups, capacity) * 2 * partial_floats(rows, d);
+  size_t n = (size_t)grid_size(b, hkv, row_groups, capacity, ctas_per_sm(d, nt)) * 2 * partial_floats(rows, d);
   if (weights) n += (size_t)b * hkv * R * capacity;
   return n * sizeof(float);
 }
