@@ -617,6 +617,9 @@ static fa_status kv4_rows(bool read, const void* K, const void* V, const int32_t
   if (weights && (st = check_words({weights}, name)) != FA_OK) return st;
   const int eb = dtype == FA_FP32 ? 4 : 2;
   if ((st = check_strides({k_token_stride, k_head_stride, v_token_stride, v_head_stride}, eb, name)) != FA_OK) return st;
+  if (read)  // rows that lie over one another cannot all be written
+    for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
+      if (s < d) return fail(FA_ERR_INVALID_ARG, "%s: an output stride of %lld elements < d=%d", name, (long long)s, d);
   if (T > INT32_MAX - 64 || (int64_t)Hkv * (d / 8) > 65535 * 32)
     return fail(FA_ERR_INVALID_ARG, "%s: T=%d rows of %d heads are too many for one call", name, T, Hkv);
   DeviceSyms syms;
@@ -654,7 +657,7 @@ static fa_status check_decode_kv4(int B, int H, int Hkv, int Nq, int capacity, i
   // rows of one key/value head, and its blocks times groups of eight of them, are counted in 32 bits
   const int64_t rows = (int64_t)(H / Hkv) * Nq;
   if (rows > INT32_MAX / 64 || (double)B * Hkv * ((rows + 7) / 8) > 1.0e9 ||
-      (double)Hkv * ((rows + 7) / 8) * (capacity / 64) > 2.0e9 || (double)B * Hkv * (capacity / 64) > 2.0e9 ||
+      (double)Hkv * ((rows + 7) / 8) * (capacity / 64 + 64) > 2.0e9 || (double)B * Hkv * (capacity / 64) > 2.0e9 ||
       (double)B * Hkv * rows * capacity > 2.0e18)
     return fail(FA_ERR_INVALID_ARG, "problem too large");
   return FA_OK;

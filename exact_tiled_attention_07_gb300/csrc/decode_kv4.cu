@@ -10,13 +10,19 @@
 // value in front of it, in fp32, so keys and values are not rounded.
 //
 // Bound: HBM (9/16 byte a channel of a key or value), then the instructions that turn codes into
-// numbers.  So codes go from shared memory straight into the registers of mma.sync (m16n8k16, fp16,
-// fp32 sums) operands: tcgen05 would want them as 8- or 16-bit tiles in shared or tensor memory, two to
-// four times the bytes written and read again, for a tile of 128 rows where a head has 8.  A nibble
-// or-ed into fp16 1024 counts 1 or 16, in place or after a shift by 8, and one addition or
-// fused multiply-add brings the pair to code - 8 (exact): 9 instructions for 8 codes.  (E4M3
-// holds the bytes 0000cccc as they are, but its mma.sync runs as conversions and fp16 products here:
-// 523 instructions for 16 tokens of 128 channels against 441 for a version with 13 per 8 codes.)
+// numbers (343 for 16 tokens of 128 channels, of which 139 on the integer pipe, half the rate of the others).
+// So codes go from shared memory straight into the registers of mma.sync (m16n8k16, fp16, fp32 sums)
+// operands.  A nibble or-ed into fp16 1024 counts 1 or 16, in place or after a shift by 8, and
+// one addition or fused multiply-add brings the pair to code - 8 (exact): 9 instructions for 8 codes.
+// Measured, 32 x 8 heads of 32,768 slots, d = 128, four rows a head (1.21 GB): 240 us, 5.04 TB/s, 0.74 of the
+// measured copy rate; 203 us with the arithmetic left out.  Other forms of it:
+//   * one CTA of 8, 12 or 16 warps an SM: 248 to 256 us;
+//   * constants of the nibble extraction as immediates (each mask-and-or two instructions): 313 us;
+//   * keys as E4M3 bytes 0000cccc, which hold c 2^-9 exactly, by mma.sync: 351 us (it runs as conversions
+//     and fp16 products, 523 instructions);
+//   * the same bytes by tcgen05, codes unpacked into shared memory, probabilities in three E4M3 pieces: right to
+//     the same tolerances, 398 us; a tile's unpacking, product, softmax and product wait for one another,
+//     and the bytes written and read again (110 KB for 128 tokens) come near what shared memory moves in that time.
 //
 //   S^T = K Q^T: K is the A operand (16 tokens x 16 channels).  Channels may come in any order in a
 //     dot product, so Q is laid out to match; it is scaled by a power of two that puts the row's
@@ -25,15 +31,17 @@
 //     tokens, so the words of two tokens are interleaved by halves first.  P step_V is rounded to
 //     fp16 (2^-11); for fp16 queries the rounding error is a second operand, so that only O's own
 //     rounding is left.  P^T comes out of the S^T accumulators by movmatrix.
-//     Range: P step_V is kept below 2^9 by a running exponent E of the steps met so far, which is part of the
-//     reference of the exponentials just as the running maximum is: P = 2^(S - m - E + 8).
+//     Range: P step_V is kept below 2^13 by a running exponent E of the steps met so far, which is part of the
+//     reference of the exponentials just as the running maximum is: P = 2^(S - m - E + 8), where m may lag
+//     behind the maximum by 4.
 //
 // Work split: the 64-slot blocks of all (sequence, key/value head, group of 8 NT query rows) form one list;
 // each CTA takes an equal run of it, whatever the lengths of the sequences, found on the device
 // from lens.  A head that lies inside one CTA's run is finished there; one that is cut leaves a
 // partial (unnormalised O, m, l) per CTA in the workspace, at most two per CTA, and
 // decode_kv4_finish joins them in the CTAs' order.  Inside a CTA each team of warps takes every TEAMS-th
-// block through a ring of its own, filled by one bulk copy per block.
+// block through a ring of its own, filled by one bulk copy per block.  (Equal pieces of every sequence instead,
+// sized by the longest: 76 us against 42 for a batch of lengths 1 to 32,768.)
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <cstdint>
@@ -57,7 +65,7 @@ struct Kv4Cfg {
   static constexpr int ROWS = 8 * NT;     // query rows of a CTA
   static constexpr int GROUPS = D / 64;   // parameter groups of a row
   static constexpr int BLOCK = kv4_block_bytes(D);
-  // CTAs of an SM: two where 128 registers a thread hold a row tile's accumulators, so that one's start and end of a
+  // (8 warps with the 255 registers they need otherwise.)  CTAs of an SM: two where 128 registers a thread hold a row tile's accumulators, so that one's start and end of a
   // segment run under the other's loop
   static constexpr int CTAS = NT == 1 && D <= 128 ? 2 : 1;
   static constexpr int NW = 8;  // warps
@@ -150,7 +158,8 @@ __device__ __forceinline__ int blocks_of(int n) { return (n + kKv4Block - 1) / k
 
 // The list: sequences, then their heads x row groups (segments), then the segment's nb blocks, each a
 // position, behind kSegCost positions that stand for what a segment costs whatever its length (its queries, joining
-// the warps, its output: about the time of that many blocks).
+// the warps, its output: about the time of that many blocks; 10 and 16 measure alike, 6 is 5 to 10 % slower where
+// sequences are short).
 constexpr int kSegCost = 10;
 
 struct Cursor {

@@ -156,13 +156,16 @@ __device__ __forceinline__ int warp_sequence(const int32_t* __restrict__ cu, int
 constexpr int kRowWarps = 8;  // rows of a block: one warp each
 
 // A warp takes CH x 32 words (8 channels each) of a row's key/value heads: a lane loads 16 bytes of
-// 16-bit elements, keys and values, before anything else is known; the 8 lanes of a group find its minimum and
-// maximum together and a lane's codes are one 32-bit word.  Bytes: 16 in, 4.5 out for 8 channels.  The quotient is
-// taken as a product with an approximate 1 / step (2^-23), which is within 2^-19 of the IEEE quotient
-// for |quotient| <= 8.5; only where one lies within 2^-17 of a half (where that could change the rounding) or
-// beyond the codes is the division done.  Rounding to an integer is an addition of 1.5 2^23 and its
-// subtraction, and four codes are put together by multiply-adds: conversions to int (16 a clock on an SM)
-// and shifts and masks (64) instead cost 109 and 58 us, against %APPEND% us, for 34,001 rows of 8 heads of 128 bf16 channels.
+// 16-bit elements, keys and values, before anything else is known; the 8 lanes of a group find its minimum
+// and maximum together and a lane's codes are one 32-bit word.  The quotient is taken as a product with an
+// approximate 1 / step (2^-23), which is within 2^-19 of the IEEE quotient for |quotient| <= 8.5;
+// where one lies within 2^-17 of a half (exact halves are one in 1,200 of bf16 data) or beyond the codes, the
+// division is done for it.  Rounding to an integer is an addition of 1.5 2^23 and its subtraction,
+// and four codes are put together by multiply-adds.
+// Bound: instructions (160 for 32 words; HBM wants 26 us for 34,001 rows of 8 heads of 128 bf16
+// channels, 139 MB in and 39 MB out).  Measured there: 51 us (3.5 TB/s); 109 with conversions to int (16 a clock
+// on an SM) and a division each, 58 with shifts and masks for the packing.  One chunk a warp instead of two 96
+// against 85 us with the read behind it, four 87.
 template <typename T, int D, int CH>
 __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4RowArgs a) {
   constexpr int kWords = D / 8;  // of a row of one head
@@ -239,7 +242,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4Row
   }
 }
 
-// The inverse, with the same split: middle + step (code - 8) in fp32, rounded once.
+// The inverse, with the same split: middle + step (code - 8) in fp32, rounded once.  Bound: HBM; 32 us for the rows
+// above (5.6 TB/s, 0.83 of the measured copy rate).
 template <typename T, int D, int CH>
 __global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const Kv4RowArgs a) {
   constexpr int kWords = D / 8;
@@ -327,7 +331,11 @@ cudaError_t launch_rows(const Kv4RowArgs& a) {
 // the threshold key, the first ones equal to it, and the newest.  Bound by the shared-memory atomics of
 // the first pass, whose digit (sign, exponent, one bit) takes few values: 16 copies of that histogram, one
 // per pair of lanes.
-// kv4_gather_kernel: one block per 64 kept slots of a head, a block of the new cache, 16 bytes a thread.
+// Measured for 8 x 8 heads of 32,768 slots, 8,192 to stay: 28 us (two blocks a head); 44 with one block a head
+// and the keys read again in every pass, 47 with four blocks, of which only half are resident.
+// kv4_gather_kernel: one block per 64 kept slots of a head, a block of the new cache, all of a thread's loads
+// before its stores.  Bound: HBM (151 MB moved for those heads, and half as much again in sectors of which
+// only a row's parameters are used): 28 us, 5.4 TB/s.
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (isnan(w)) return 0xFFFFFFFFu;

@@ -324,7 +324,8 @@ FA_API fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void
  *             no length: the caller owns lens, counts it up and may change it between calls on the
  *             stream. (The lengths are read on the device, so one captured graph serves any lengths.)
  *   rows      K, V of several sequences packed one behind the other, [T][Hkv][d] with the last
- *             dimension contiguous and any token and head strides that are multiples of 16 bytes;
+ *             dimension contiguous and any token and head strides that are multiples of 16 bytes (at
+ *             least d where rows are written);
  *             cu_seqlens, device int32 [B + 1], non-decreasing: rows [cu_seqlens[b], cu_seqlens[b + 1]) belong
  *             to sequence b. Rows outside [cu_seqlens[0], cu_seqlens[B]) are neither read nor written.
  * fa_kv4_append writes a sequence's rows into its newest slots: n_b rows go to slots lens[b] - n_b ..

@@ -151,6 +151,10 @@ def test_refusals(fa):
         fa.fa_kv4_evict(cache, w, lens, 32, 33, out, w2, n2, kept)
     with pytest.raises(fa.FAError, match="another cache"):
         fa.fa_kv4_evict(cache, w, lens, 32, 3, cache, w, n2, kept)
+    k = torch.zeros(3, 1, d, dtype=torch.bfloat16, device="cuda").expand(3, 2, d)
+    fa.fa_kv4_append(k, k, i32([0, 1, 3]), lens, cache)  # one head for all: fine to read, not to write
+    with pytest.raises(fa.FAError, match="output stride"):
+        fa.fa_kv4_read(cache, i32([0, 1, 3]), lens, k, k)
     with pytest.raises(fa.FAError, match="16 bytes"):
         odd = torch.zeros(3, 2, 132, dtype=torch.bfloat16, device="cuda")[..., :128]
         fa.fa_kv4_append(odd, odd, i32([0, 1, 3]), lens, cache)
