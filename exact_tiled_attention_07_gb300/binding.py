@@ -519,20 +519,27 @@ def fa_decode_kv4(Q, cache, lens, O, L, scale, causal=False, weights_in=None, we
                   stream=None):
     """Decode: Q, O [B, H, Nq, d] over a 4-bit cache with lens [B] slots in use; L [B, H, Nq].
     weights_out [B, Hkv, capacity] = weights_in + the attention each slot got (slots in use)."""
+    shape = _kv4_decode_shape(Q, cache, lens, weights_in, weights_out)
+    _on_device(O, L, Q, workspace)
+    _same(Q, O)
+    _rows(L, O.numel() // O.shape[3])
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().fa_decode_kv4(_p(Q), _p(cache), _p(lens), _p(O), _p(L), _p(weights_in), _p(weights_out),
+                                        *shape, float(scale), int(bool(causal)), _dt(Q), _p(workspace), nbytes,
+                                        _stream(stream)))
+
+
+def _kv4_decode_shape(Q, cache, lens, weights_in, weights_out):
+    """(B, H, Hkv, Nq, capacity, d) of a decode over a 4-bit cache, after checking what it reads."""
     B, H, Nq, d = _shape4(Q)
     Bc, Hkv, capacity, dc = _kv4_shape(cache)
-    _on_device(Q, cache, lens, O, L, weights_in, weights_out, workspace)
+    _on_device(Q, cache, lens, weights_in, weights_out)
     if (Bc, dc) != (B, d):
         raise ValueError("the cache must have Q's batch and head dimension")
-    _same(Q, O)
-    _rows(L, B * H * Nq)
     _int32(lens, B, "lens")
     _kv4_weights(weights_in, B, Hkv, capacity, "weights_in")
     _kv4_weights(weights_out, B, Hkv, capacity, "weights_out")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load_library().fa_decode_kv4(_p(Q), _p(cache), _p(lens), _p(O), _p(L), _p(weights_in), _p(weights_out), B, H,
-                                        Hkv, Nq, capacity, d, float(scale), int(bool(causal)), _dt(Q), _p(workspace),
-                                        nbytes, _stream(stream)))
+    return B, H, Hkv, Nq, capacity, d
 
 
 def fa_kv4_evict(cache, weights, lens, keep, recent, out_cache, out_weights, out_lens, kept, stream=None):
@@ -700,14 +707,15 @@ def kv4_read(cache, cu_seqlens, lens, total, dtype=torch.bfloat16, stream=None):
 def attention_decode_kv4(q, cache, lens, causal=False, scale=None, weights_in=None, weights_out=None, stream=None):
     """O, L = fa_decode_kv4(...) for q [B, H, Nq, d] over a 4-bit cache; outputs and workspace
     allocated with torch."""
-    B, H, Nq, d = _shape4(q)
-    _, Hkv, capacity, _ = _kv4_shape(cache)
-    scale = d ** -0.5 if scale is None else scale
+    shape = B, H, Hkv, Nq, capacity, d = _kv4_decode_shape(q, cache, lens, weights_in, weights_out)
+    lib = load_library()
     o = torch.empty_like(q)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    nbytes = fa_decode_kv4_workspace_size(B, H, Hkv, Nq, capacity, d, weights_out is not None)
+    nbytes = lib.fa_decode_kv4_workspace_size(*shape, int(weights_out is not None))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    fa_decode_kv4(q, cache, lens, o, lse, scale, causal, weights_in, weights_out, ws, stream)
+    _check(lib.fa_decode_kv4(_p(q), _p(cache), _p(lens), _p(o), _p(lse), _p(weights_in), _p(weights_out), *shape,
+                             d ** -0.5 if scale is None else float(scale), int(bool(causal)), _dt(q), _p(ws), nbytes,
+                             _stream(stream)))
     _used_on(stream, o, lse, ws)
     return o, lse
 

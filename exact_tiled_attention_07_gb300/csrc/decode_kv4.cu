@@ -16,7 +16,7 @@
 // one addition or fused multiply-add brings the pair to code - 8 (exact): 9 instructions for 8 codes.
 // Measured, 32 x 8 heads of 32,768 slots, d = 128, four rows a head (1.21 GB): 240 us, 5.04 TB/s, 0.74 of the
 // measured copy rate; 203 us with the arithmetic left out.  Other forms of it:
-//   * one CTA of 8, 12 or 16 warps an SM: 248 to 256 us;
+//   * one CTA of 8, 12 or 16 warps an SM instead of four of 4: 248 to 256 us;
 //   * constants of the nibble extraction as immediates (each mask-and-or two instructions): 313 us;
 //   * keys as E4M3 bytes 0000cccc, which hold c 2^-9 exactly, by mma.sync: 351 us (it runs as conversions
 //     and fp16 products, 523 instructions);
@@ -65,14 +65,15 @@ struct Kv4Cfg {
   static constexpr int ROWS = 8 * NT;     // query rows of a CTA
   static constexpr int GROUPS = D / 64;   // parameter groups of a row
   static constexpr int BLOCK = kv4_block_bytes(D);
-  // (8 warps with the 255 registers they need otherwise.)  CTAs of an SM: two where 128 registers a thread hold a row tile's accumulators, so that one's start and end of a
-  // segment run under the other's loop
-  static constexpr int CTAS = NT == 1 && D <= 128 ? 2 : 1;
-  static constexpr int NW = 8;  // warps
-  static constexpr int TEAM = D == 256 || (D == 128 && CTAS == 2) ? 2 : 1;  // warps that share a block
+  // CTAs of 4 warps, four an SM where 128 registers a thread hold a row tile's accumulators, else two: one's start
+  // and end of a segment run under the others' loops.  128 x 8 heads of 100 slots, d = 128: 21 us; two CTAs of
+  // 8 warps 26, one of 16 warps 38; heads of 32,768 slots measure the same with four and two, 4 % more with one.
+  static constexpr int CTAS = NT == 1 && D <= 128 ? 4 : 2;
+  static constexpr int NW = 4;  // warps
+  static constexpr int TEAM = D == 256 || (D == 128 && NT == 1) ? 2 : 1;  // warps that share a block
   static constexpr int TEAMS = NW / TEAM;
   static constexpr int TOK = 64 / TEAM;   // tokens of a block for one warp
-  static constexpr int STAGES = D == 64 && CTAS == 1 ? 4 : 2;
+  static constexpr int STAGES = 2;
   static constexpr int THREADS = NW * 32;
   // channels that the warps exchange at a time (a whole row where two CTAs have the shared memory for it)
   static constexpr int OCH = NT == 1 && D <= 128 ? D : 64;
@@ -158,9 +159,8 @@ __device__ __forceinline__ int blocks_of(int n) { return (n + kKv4Block - 1) / k
 
 // The list: sequences, then their heads x row groups (segments), then the segment's nb blocks, each a
 // position, behind kSegCost positions that stand for what a segment costs whatever its length (its queries, joining
-// the warps, its output: about the time of that many blocks; 10 and 16 measure alike, 6 is 5 to 10 % slower where
-// sequences are short).
-constexpr int kSegCost = 10;
+// the warps, its output: about the time of that many blocks).
+constexpr int kSegCost = 6;
 
 struct Cursor {
   int64_t first;  // list position of sequence b's first segment
@@ -759,7 +759,7 @@ struct Partials {
 
 constexpr int kFinishThreads = 256;
 constexpr int kWeightSlots = 4 * kFinishThreads;  // slots of a head whose weights a block of the finish adds up
-constexpr int kMaxRuns = 512;  // CTAs of the decode kernel, at most
+constexpr int kMaxRuns = 640;  // CTAs of the decode kernel, at most
 
 // What is left when the runs are done.  Blocks [0, segments): the segments that several CTAs' runs cut
 // are joined from their partials, in the order of the CTAs, and the rows of empty sequences are
@@ -909,10 +909,6 @@ int grid_size(int b, int hkv, int row_groups, int capacity, int ctas) {
   const int64_t most = (int64_t)b * hkv * row_groups * (capacity / kKv4Block);
   return (int)std::min<int64_t>(most, std::min(ctas * device_sm_count(), kMaxRuns));
 }
-int ctas_per_sm(int d, int row_tiles) {
-  return row_tiles == 2 ? Kv4Cfg<128, 2>::CTAS : (d == 256 ? Kv4Cfg<256, 1>::CTAS : Kv4Cfg<128, 1>::CTAS);
-}
-
 template <int D, bool BF16, int NT>
 cudaError_t launch_nt(const DecodeKv4Args& a) {
   using C = Kv4Cfg<D, NT>;
@@ -954,9 +950,10 @@ cudaError_t launch_d(const DecodeKv4Args& a) {
 
 size_t decode_kv4_workspace_bytes(int b, int h, int hkv, int nq, int capacity, int d, bool weights) {
   const int nt = row_tiles(h, hkv, nq, d), rows = 8 * nt;
+  const int ctas = nt == 1 ? (d == 256 ? Kv4Cfg<256, 1>::CTAS : Kv4Cfg<128, 1>::CTAS) : Kv4Cfg<128, 2>::CTAS;
   const int R = (h / hkv) * nq;
   const int row_groups = (R + rows - 1) / rows;
-  size_t n = (size_t)grid_size(b, hkv, row_groups, capacity, ctas_per_sm(d, nt)) * 2 * partial_floats(rows, d);
+  size_t n = (size_t)grid_size(b, hkv, row_groups, capacity, ctas) * 2 * partial_floats(rows, d);
   if (weights) n += (size_t)b * hkv * R * capacity;
   return n * sizeof(float);
 }

@@ -360,6 +360,7 @@ constexpr int kSelSmem = (kSelCopies * kSelFirstBins + 2 * kSelBins) * 4;
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictArgs a) {
   namespace cg = cooperative_groups;
+  asm volatile("griddepcontrol.launch_dependents;");
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
   auto sync_all = [&]() {
@@ -522,6 +523,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
 
 template <int D>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, int blocks_per_head) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched while the selection is still going)
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.b; b += blockDim.x) a.out_lens[b] = min(min(max(a.lens[b], 0), a.capacity), a.keep);
   const int bh = blockIdx.x / blocks_per_head, blk = blockIdx.x - bh * blocks_per_head;
@@ -603,13 +605,17 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
   }
   if (e != cudaSuccess) return e;
   const int per_head = (a.keep + kKv4Block - 1) / kKv4Block;
-  const unsigned grid = (unsigned)per_head * a.b * a.hkv;
-  switch (a.d) {
-    case 64: kv4_gather_kernel<64><<<grid, 256, 0, a.stream>>>(a, per_head); break;
-    case 128: kv4_gather_kernel<128><<<grid, 256, 0, a.stream>>>(a, per_head); break;
-    default: kv4_gather_kernel<256><<<grid, 256, 0, a.stream>>>(a, per_head);
-  }
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)per_head * a.b * a.hkv);
+  cfg.blockDim = dim3(256);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, a.d == 64 ? kv4_gather_kernel<64> : (a.d == 128 ? kv4_gather_kernel<128> : kv4_gather_kernel<256>),
+                            a, per_head);
 }
 
 }  // namespace fa
