@@ -127,31 +127,14 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   return r;
 }
 
-// Constants of code_pairs, read through volatile moves so that they stay in registers: as immediates each
-// mask-and-or becomes two instructions (an instruction has room for one immediate).
-struct CodeConsts {
-  uint32_t magic, bias, sixteenth, bias16;
-  __device__ __forceinline__ CodeConsts() {
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));      // 1024
-    asm volatile("mov.b32 %0, 0xE408E408;" : "=r"(bias));       // -1032
-    asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(sixteenth));  // 1/16
-    asm volatile("mov.b32 %0, 0xD480D480;" : "=r"(bias16));     // -72
-  }
-};
-
-// The four nibbles of each half of x as four pairs of fp16, code - 8 (exact): 1024 + c - 1032, and
-// (1024 + 16 c) / 16 - 72
-__device__ __forceinline__ void code_pairs(uint32_t x, const CodeConsts& k, uint32_t (&out)[4]) {
+// The four nibbles of each half of x as four pairs of fp16: codes times 2^-24 (even) and 2^-20 (odd), as
+// the subnormal numbers that their bits are where they stand
+__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&out)[4]) {
   const uint32_t y = x >> 8;
-  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(out[0]) : "r"(x), "r"(k.magic));
-  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(out[1]) : "r"(x), "r"(k.magic));
-  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(out[2]) : "r"(y), "r"(k.magic));
-  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(out[3]) : "r"(y), "r"(k.magic));
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(out[i]) : "r"(k.bias));
-    asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(out[i + 1]) : "r"(k.sixteenth), "r"(k.bias16));
-  }
+  out[0] = x & 0x000F000Fu;
+  out[1] = x & 0x00F000F0u;
+  out[2] = y & 0x000F000Fu;
+  out[3] = y & 0x00F000F0u;
 }
 
 __device__ __forceinline__ int clamp_len(int n, int capacity) { return min(max(n, 0), capacity); }
@@ -352,7 +335,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
   int e_run;  // exponent of the largest V step so far
   uint32_t qf[D / 16][NT][2];
   float2 qsum[C::GROUPS][NT], cf[NT];
-  const CodeConsts kc;
   const int kap = (g >> 1) + (g & 1) * 4;  // token of operand row g: rows 2t, 2t + 1 are tokens t, t + 4
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* obuf = reinterpret_cast<float*>(smem + C::OFF_O);
@@ -392,7 +374,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
       // scaled by 2^(14 - ex), the row's largest element lies in [2^14, 2^15)
       const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
       const float up = __uint_as_float((uint32_t)(141 - ex) << 23);
-      const float factor = __uint_as_float((uint32_t)(113 + ex) << 23) * scale_log2;
+      const float factor = __uint_as_float((uint32_t)(113 + ex) << 23) * (scale_log2 * 0x1p24f);  // (codes count 2^-24)
       cf[nt] = make_float2(__shfl_sync(0xffffffffu, factor, (2 * t) * 4),
                            __shfl_sync(0xffffffffu, factor, (2 * t + 1) * 4));
 #pragma unroll
@@ -408,14 +390,16 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
             f[i] = fmul2(f[i], make_float2(up, up));
             sum += f[i].x + f[i].y;
           }
-          qf[ks * 2][nt][0] = pack2<false>(f[0].x, f[2].x);      // channels 0, 4 of the eight
-          qf[ks * 2][nt][1] = pack2<false>(f[0].y, f[2].y);      // 1, 5
-          qf[ks * 2 + 1][nt][0] = pack2<false>(f[1].x, f[3].x);  // 2, 6
-          qf[ks * 2 + 1][nt][1] = pack2<false>(f[1].y, f[3].y);  // 3, 7
+          // (odd codes count 16 times as much)
+          qf[ks * 2][nt][0] = pack2<false>(f[0].x, f[2].x);                          // channels 0, 4 of the eight
+          qf[ks * 2][nt][1] = pack2<false>(f[0].y * 0.0625f, f[2].y * 0.0625f);      // 1, 5
+          qf[ks * 2 + 1][nt][0] = pack2<false>(f[1].x, f[3].x);                      // 2, 6
+          qf[ks * 2 + 1][nt][1] = pack2<false>(f[1].y * 0.0625f, f[3].y * 0.0625f);  // 3, 7
         }
         // sum over the group's channels (the four t) of row g, then for this lane's rows 2t, 2t + 1
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= 0x1p-24f;
         qsum[gr][nt] = make_float2(__shfl_sync(0xffffffffu, sum, (2 * t) * 4),
                                    __shfl_sync(0xffffffffu, sum, (2 * t + 1) * 4));
       }
@@ -503,8 +487,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t xa[4], xb[4];
-              code_pairs(j ? wa.y : wa.x, kc, xa);
-              code_pairs(j ? wb.y : wb.x, kc, xb);
+              code_pairs(j ? wa.y : wa.x, xa);
+              code_pairs(j ? wb.y : wb.x, xb);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const uint32_t af[4] = {xa[2 * k], xb[2 * k], xa[2 * k + 1], xb[2 * k + 1]};
@@ -523,7 +507,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float st = e ? p1.x : p0.x, md = e ? p1.y : p0.y;
+                const float st = e ? p1.x : p0.x, md = fmaf(-8.f, st, e ? p1.y : p0.y);
                 const float2 mid = gr == 0 ? fmul2(qsum[0][nt], make_float2(md, md)) : ffma2(qsum[gr][nt], md, sc[mt][nt][e]);
                 sc[mt][nt][e] = ffma2(make_float2(acc[nt][2 * e], acc[nt][2 * e + 1]), st, mid);
               }
@@ -611,9 +595,11 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
                 corr[gr][nt] = ffma2(sc[mt][nt][e], md, corr[gr][nt]);
                 const float2 y = fmul2(sc[mt][nt][e], make_float2(st, st));
                 const uint32_t h = pack2<false>(y.x, y.y);
+                // the codes' offset of 8, times what the codes are multiplied with
+                const float2 back = unpack2<false>(h);
+                corr[gr][nt] = ffma2(BF16 ? back : y, -8.f, corr[gr][nt]);
                 pf[nt][e] = movmatrix(h);
                 if constexpr (!BF16) {
-                  const float2 back = unpack2<false>(h);
                   pl[nt][e] = movmatrix(pack2<false>(y.x - back.x, y.y - back.y));
                 }
               }
@@ -621,8 +607,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
             for (int hi = 0; hi < 2; ++hi) {
               const uint32_t sel = hi ? 0x7632u : 0x5410u;
               uint32_t lo4[4], hi4[4];
-              code_pairs(__byte_perm(c[0], c[1], sel), kc, lo4);
-              code_pairs(__byte_perm(c[2], c[3], sel), kc, hi4);
+              code_pairs(__byte_perm(c[0], c[1], sel), lo4);
+              code_pairs(__byte_perm(c[2], c[3], sel), hi4);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 // operand rows g, g + 8: channels 64 gr + 8 g + 4 hi + 2 k and + 1
@@ -659,8 +645,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
           for (int o = 4; o < 32; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            o_acc[gr * 4 + i][nt][e] += c;
-            o_acc[gr * 4 + i][nt][e + 2] += c;
+            o_acc[gr * 4 + i][nt][e] = fmaf(o_acc[gr * 4 + i][nt][e], 0x1p24f, c);
+            o_acc[gr * 4 + i][nt][e + 2] = fmaf(o_acc[gr * 4 + i][nt][e + 2], 0x1p20f, c);
           }
         }
         const float r = e ? off[nt].y : off[nt].x;
