@@ -2,22 +2,24 @@
 //
 // For the R = (H / Hkv) Nq query rows that read one key/value head, with x_hat the value that a
 // cached code stands for (x_hat = middle + step (code - 8), one step and middle per 64 channels):
-//   S_rj = tau log2e sum_g [ step_K(j, g) (q_r . (code_K(j) - 8))_g + middle_K(j, g) sum_g q_r ]
-//   O_r  = sum_g [ sum_j P_rj step_V(j, g) (code_V(j) - 8) + sum_j P_rj middle_V(j, g) ] / l_r
+//   S_rj = tau log2e sum_g [ step_K(j, g) (q_r . code_K(j))_g + (middle_K - 8 step_K)(j, g) sum_g q_r ]
+//   O_r  = sum_g [ sum_j P_rj step_V(j, g) code_V(j) + sum_j P_rj (middle_V - 8 step_V)(j, g) ] / l_r
 //   P_rj = 2^(S_rj - m_r), l_r = sum_j P_rj, L_r = (m_r + log2 l_r) ln 2
 //   weights_j += sum_r P_rj / l_r      (when asked for)
 // Steps and middles never touch the codes: those of a key enter behind the dot product, those of a
 // value in front of it, in fp32, so keys and values are not rounded.
 //
 // Bound: HBM (9/16 byte a channel of a key or value), then the instructions that turn codes into
-// numbers (343 for 16 tokens of 128 channels, of which 139 on the integer pipe, half the rate of the others).
-// So codes go from shared memory straight into the registers of mma.sync (m16n8k16, fp16, fp32 sums)
-// operands.  A nibble or-ed into fp16 1024 counts 1 or 16, in place or after a shift by 8, and
-// one addition or fused multiply-add brings the pair to code - 8 (exact): 9 instructions for 8 codes.
-// Measured, 32 x 8 heads of 32,768 slots, d = 128, four rows a head (1.21 GB): 240 us, 5.04 TB/s, 0.74 of the
-// measured copy rate; 203 us with the arithmetic left out.  Other forms of it:
-//   * one CTA of 8, 12 or 16 warps an SM instead of four of 4: 248 to 256 us;
-//   * constants of the nibble extraction as immediates (each mask-and-or two instructions): 313 us;
+// numbers (283 for 16 tokens of 128 channels in all, half of them on the integer pipe, which has half the rate of
+// the others).  So codes go from shared memory straight into the registers of mma.sync (m16n8k16,
+// fp16, fp32 sums) operands.  Masked out of its word, a nibble is an fp16 subnormal, c 2^-24 where it stands
+// lowest and c 2^-20 next to that: 4 masks and a shift for 8 codes, nothing to convert; what the codes are
+// multiplied with and the sums carry the powers of two, and the offset of 8 is taken off in fp32.
+// Measured, 32 x 8 heads of 32,768 slots, d = 128, four rows a head (1.21 GB): 205 us, 5.9 TB/s, 0.87 of the
+// measured copy rate; with the arithmetic left out 194.  Other forms of it:
+//   * codes to fp16 numbers by or-ing them into 1024 and taking that and 8 off (9 instructions for 8 codes): 236 us,
+//     313 with the or's constant as an immediate (each mask-and-or two instructions);
+//   * one CTA of 8, 12 or 16 warps an SM instead of four of 4, in that form: 248 to 256 us;
 //   * keys as E4M3 bytes 0000cccc, which hold c 2^-9 exactly, by mma.sync: 351 us (it runs as conversions
 //     and fp16 products, 523 instructions);
 //   * the same bytes by tcgen05, codes unpacked into shared memory, probabilities in three E4M3 pieces: right to
@@ -29,7 +31,8 @@
 //     largest element in [2^14, 2^15), so a bf16 q is exact in fp16 down to 2^-29 of that.
 //   O^T = V^T P^T: V^T is the A operand (16 channels x 16 tokens): a register holds one channel of two
 //     tokens, so the words of two tokens are interleaved by halves first.  P step_V is rounded to
-//     fp16 (2^-11); for fp16 queries the rounding error is a second operand, so that only O's own
+//     fp16 (2^-11), and what the offset of 8 takes off is counted with the rounded one, so the error is that of
+//     code - 8; for fp16 queries the rounding error is a second operand, so that only O's own
 //     rounding is left.  P^T comes out of the S^T accumulators by movmatrix.
 //     Range: P step_V is kept below 2^13 by a running exponent E of the steps met so far, which is part of the
 //     reference of the exponentials just as the running maximum is: P = 2^(S - m - E + 8), where m may lag
@@ -323,7 +326,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
       load_ok = mbar_wait(empty + s, (uint32_t)(loads / C::STAGES - 1) & 1, ctx, kSiteKv4Empty);
     if (load_ok) {
       mbar_arrive_expect_tx(full + s, C::BLOCK);
-      bulk_load(ring + s * C::BLOCK, load_src, C::BLOCK, full + s);
+      // read once, so first to leave L2: 222 -> 214 us for 1.21 GB
+      bulk_load_once(ring + s * C::BLOCK, load_src, C::BLOCK, full + s);
       ++loads;
     }
   };
