@@ -268,9 +268,11 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + team * C::STAGES;
   uint64_t* empty = full + C::TEAMS * C::STAGES;  // (teams of several warps) every warp has read the slot
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + C::NBAR * 8);
+  volatile uint8_t* nan_seen = smem + C::OFF_BAR + C::NBAR * 8 + 4;  // [NW]
   const ErrCtx ctx{a.err, abort_flag};
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    for (int w = 0; w < C::NW; ++w) nan_seen[w] = 0;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     for (int s = 0; s < C::NBAR; ++s) mbar_init(bars + s, s < C::TEAMS * C::STAGES ? 1 : C::TEAM);
     fence_barrier_init();
@@ -440,11 +442,14 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
       // not every slot of this block is inside every row's range
       const bool edge = blk * kKv4Block + kKv4Block > sp.len - (a.causal ? a.nq - 1 : 0);
       if (edge) {
-        // V parameters of slots behind the sequence to zero: v_hat = 0 whatever lies there
+        // V parameters of slots behind the sequence to zero: v_hat = 0 whatever lies there.  NaN in a slot that
+        // some rows do not see (0 x NaN is not 0 to them) too: the other rows get theirs behind the loop.
         for (int i = lane; i < C::TOK * C::GROUPS; i += 32) {
-          const int tok = half * C::TOK + i / C::GROUPS;
-          if (blk * kKv4Block + tok >= sp.len)
-            reinterpret_cast<uint32_t*>(blkp + kv4_params_at(D, 1))[half * C::TOK * C::GROUPS + i] = 0u;
+          const int slot = blk * kKv4Block + half * C::TOK + i / C::GROUPS;
+          uint32_t* par = reinterpret_cast<uint32_t*>(blkp + kv4_params_at(D, 1)) + half * C::TOK * C::GROUPS + i;
+          const bool nan = slot > sp.len - a.nq && (*par & 0x7FFFu) > 0x7C00u;
+          if (nan && slot < sp.len && a.causal) nan_seen[warp] = 1;
+          if (slot >= sp.len || (nan && a.causal)) *par = 0u;
         }
         __syncwarp();
       }
@@ -632,6 +637,24 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
       __syncwarp();
       if (C::TEAM > 1 && lane == 0) mbar_arrive(empty + s);
       load_next();
+    }
+
+    if (nan_seen[warp]) {  // rows that see one of the newest slots that hold NaN
+      const int64_t block0 = ((int64_t)sp.b * a.hkv + hk) * (a.capacity / kKv4Block);
+      for (int slot = max(blk0 * kKv4Block, sp.len - a.nq + 1); slot < min(blk1 * kKv4Block, sp.len); ++slot) {
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(a.cache + (block0 + slot / kKv4Block) * C::BLOCK +
+                                                                kv4_params_at(D, 1)) + slot % kKv4Block * C::GROUPS;
+#pragma unroll
+        for (int gr = 0; gr < C::GROUPS; ++gr)
+          if ((par[gr] & 0x7FFFu) > 0x7C00u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (slot < last[nt][0]) corr[gr][nt].x = __int_as_float(0x7FC00000);
+              if (slot < last[nt][1]) corr[gr][nt].y = __int_as_float(0x7FC00000);
+            }
+      }
+      __syncwarp();
+      nan_seen[warp] = 0;
     }
 
     // ---- join the warps: rows' maxima and sums, then O 64 channels at a time

@@ -296,7 +296,9 @@ FA_API fa_status fa_fwd_fp8_gqa(const void* Q8, const void* K8, const void* V8, 
  *             position. Rows of O and L in no sequence are left as they were. Offsets that decrease or leave
  *             [0, T] are clamped and recorded as a device error.
  *   d         64, 128 or 256. H a positive multiple of Hkv; query head h reads key/value head h / (H / Hkv).
- * What the rows of one sequence hold (NaN, infinity) does not reach another one. The lengths are read on
+ * What the rows of one sequence hold (NaN, infinity) does not reach another one. (Within a causal sequence, as in
+ * fa_fwd, a row's weights for later rows are exact zeros, so a V row that is not finite reaches the rows in front of it
+ * whose 128-row tile of queries meets its 128-row tile of keys.) The lengths are read on
  * the device: one captured graph serves any lengths with the same T and S. Launches one kernel; results are
  * the same bits for the same arguments.
  */
@@ -349,7 +351,7 @@ FA_API fa_status fa_kv4_read(const void* cache, const int32_t* cu_seqlens, const
  *   Q, O      [B][H][Nq][d] dtype (bf16 or fp16), the new query rows; L [B][H][Nq] fp32
  *   lens      as above; a row sees slots [0, lens[b]), or with causal != 0 row i of the Nq sees slots
  *             [0, lens[b] - Nq + i + 1): the Nq rows are then the newest slots' own. A row that sees
- *             nothing gets O = 0, L = -inf. A length outside [0, capacity] is clamped to it and
+ *             nothing gets O = 0, L = -inf; a NaN in a slot does not reach the rows that do not see it. A length outside [0, capacity] is clamped to it and
  *             recorded as a device error.
  *   weights   weights_out non-NULL: weights_out[b][hkv][j] = weights_in[b][hkv][j] + the sum of the probabilities
  *             that slot j got from the H / Hkv x Nq rows of its key/value head, for j < lens[b]; the other
@@ -357,8 +359,8 @@ FA_API fa_status fa_kv4_read(const void* cache, const int32_t* cu_seqlens, const
  *   workspace fa_decode_kv4_workspace_size(...) bytes for the same arguments (weights: whether
  *             weights_out is given); its contents on entry do not matter. Calls that may overlap on the
  *             GPU need workspaces of their own.
- * Keys and their scores are never rounded to 16 bits; values and probabilities enter the second product
- * rounded to fp16 (relative 2^-11). The work is cut into equal runs of blocks on the device, whatever
+ * Keys, values and scores are never rounded to 16 bits; bf16 queries' probabilities times the values' steps enter the
+ * second product rounded to fp16 (relative 2^-11), fp16 queries' with the rounding error as a second operand. The work is cut into equal runs of blocks on the device, whatever
  * the lengths. Results do not depend on timing: two calls with the same arguments give the same bits.
  */
 FA_API size_t fa_decode_kv4_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d, int weights);

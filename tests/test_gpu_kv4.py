@@ -263,6 +263,35 @@ def test_decode_of_nan_rows(fa):
     assert torch.isfinite(o).all() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_decode_nan_in_a_slot_that_a_row_does_not_see(fa, d, dtype):
+    # causal, four new rows: a NaN in the third newest slot reaches the two rows behind it and itself only
+    cap, n, nq = 128, 90, 4
+    for weights in (False, True):
+        cache, _, held_v = make_cache(2, 1, cap, d, 62)
+        cache_max = np.abs(held_v).max()
+        g = torch.Generator().manual_seed(63)
+        q = torch.randn(2, 4, nq, d, generator=g).to(TORCH[dtype]).cuda()
+        args = dict(weights_out=torch.zeros(2, 1, cap, device="cuda")) if weights else {}
+        ref, ref_l = fa.attention_decode_kv4(q, cache, i32([n, n]), causal=True, **args)
+        # a row that does not see it: both results are within O's tolerance of the formula (check_decode; the
+        # scores' part, 2 (d / 16 + 9) 2^-21 |q| . |k| scale for |q| . |k| scale < 64, is below 2^-9)
+        tol = 2 * (cache_max * (2 * 2.0 ** -11 + 2.0 ** -9) + EPS[dtype] * ref[0, :, 0].abs().max().item())
+        for bad_k in (False, True):
+            k = torch.randn(1, 1, d, generator=g).cuda()
+            v = k.clone()
+            (k if bad_k else v)[0, 0, 5] = float("nan")
+            c = cache.clone()
+            fa.fa_kv4_append(k, v, i32([0, 1, 1]), i32([n - 2, 0]), c)  # slot n - 3 of sequence 0
+            o, lse = fa.attention_decode_kv4(q, c, i32([n, n]), causal=True, **args)
+            assert torch.equal(o[1], ref[1]) and torch.equal(lse[1], ref_l[1])
+            assert ((o[0, :, 0].float() - ref[0, :, 0].float()).abs() <= tol).all()  # (false for NaN)
+            assert ((lse[0, :, 0] - ref_l[0, :, 0]).abs() <= 2.0 ** -9).all()
+            assert torch.isnan(o[0, :, 1:, :64]).all()  # the group of 64 channels that holds it
+            assert torch.isnan(lse[0, :, 1:]).all() == bad_k
+
+
 def test_decode_length_outside_the_cache(fa):
     d, cap = 64, 128
     cache, _, _ = make_cache(3, 1, cap, d, 61)
@@ -358,6 +387,24 @@ def test_evict(fa, d, keep, recent):
                 for x, y, z in zip(s, t, f):
                     assert same_bytes(x[b, h][want], y[b, h][:n])
                     assert same_bytes(z[b, h][n:], y[b, h][n:])
+
+
+@pytest.mark.parametrize("B,hkv,cap,keep", [(40, 2, 20032, 3000), (1, 1, 140032, 20000)])
+def test_evict_more_slots_than_a_block_holds(fa, B, hkv, cap, keep):
+    d, recent = 64, 100
+    cache = torch.randint(0, 256, (B, hkv, cap // 64, 72 * d), dtype=torch.uint8, device="cuda")
+    w = torch.randint(0, 5000, (B, hkv, cap), device="cuda").float()  # ties
+    lens = [cap - 7 * b for b in range(B)]
+    out, w2 = fa.kv4_cache(B, hkv, keep, d), torch.zeros(B, hkv, (keep + 63) // 64 * 64, device="cuda")
+    kept = torch.zeros(B, hkv, keep, dtype=torch.int32, device="cuda")
+    n2 = i32([0] * B)
+    fa.fa_kv4_evict(cache, w, i32(lens), keep, recent, out, w2, n2, kept)
+    fa.fa_check_device_error()
+    for b in range(0, B, 13):
+        for h in range(hkv):
+            want = KV.evict(w[b, h].cpu().numpy(), lens[b], keep, recent)
+            assert kept[b, h].tolist() == want.tolist()
+            assert np.array_equal(w2[b, h, :keep].cpu().numpy(), w[b, h].cpu().numpy()[want])
 
 
 def test_evict_long_and_in_place_lengths(fa):
