@@ -773,144 +773,196 @@ struct Partials {
 constexpr int kFinishThreads = 256;
 constexpr int kWeightSlots = 4 * kFinishThreads;  // slots of a head whose weights a block of the finish adds up
 constexpr int kMaxRuns = 640;  // CTAs of the decode kernel, at most
+constexpr int kAhead = 8;      // partials of O that a thread loads before their weights are known
+constexpr int kJoinAtOnce = 64;  // partials whose weights are in shared memory
+// channels of a segment that a block of the finish joins: four for each thread
+template <int D, int NT>
+constexpr int finish_channels() {
+  return NT == 1 ? (D < 128 ? D : 128) : 64;
+}
 
-// What is left when the runs are done.  Blocks [0, segments): the segments that several CTAs' runs cut
-// are joined from their partials, in the order of the CTAs, and the rows of empty sequences are
-// written.  Further blocks, when weights are asked for, kWeightSlots slots of a head each: weights_out =
+// What is left when the runs are done.  Blocks [0, segments x D / finish_channels): the segments that several CTAs'
+// runs cut are joined from their partials, in the order of the CTAs, and the rows of empty sequences are
+// written.  What it costs is a chain of latencies, so all that hangs on the lengths alone is done before
+// the runs are over and the partials are loaded with the numbers that weigh them (8 sequences, d = 256: 26 us a
+// call -> 23; 80 registers, as blocks that need more find room only when two of the runs are over: 26 with 64
+// and their spills).  Further blocks, when weights are asked for, kWeightSlots slots of a head each: weights_out =
 // weights_in + sum over the head's rows of 2^(S - L log2e).
-template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(kFinishThreads)
+template <int D, bool BF16, int NT, bool SCORES>
+__global__ void __launch_bounds__(kFinishThreads, 3)
     decode_kv4_finish(const DecodeKv4Args a, const float* __restrict__ part, const float* __restrict__ scores,
                       int row_groups, int ctas) {
   constexpr int ROWS = 8 * NT;
+  constexpr int CH = finish_channels<D, NT>(), SPLIT = D / CH;
+  static_assert(ROWS * CH / 4 <= kFinishThreads, "four channels of a row for each thread");
   const int hr_count = a.hkv * row_groups;
-  const int segments = a.b * hr_count;
+  const int joins = a.b * hr_count * SPLIT;  // blocks that join
   const int R = (a.h / a.hkv) * a.nq;
   const WorkList wl{a.lens, a.b, hr_count, a.capacity};
   const int64_t total = wl.total(a.b);
   const int G = runs_of(total, ctas);
-  __shared__ float fac[ROWS][kMaxRuns];
+  __shared__ float fac[ROWS][kJoinAtOnce];
   __shared__ float2 stat[ROWS];
   auto partials = [&](int64_t before, int nb, int hr) {
     const int64_t first = before + (int64_t)hr * WorkList::positions(nb) + kSegCost;
     return Partials<D, ROWS>{part, run_of(total, first, G), run_of(total, first + nb - 1, G)};
   };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // The lengths are older than the runs (the decode kernel itself started only when all before it was
   // done), so only what follows has to wait for them.
-  if ((int)blockIdx.x < segments) {
-    const int b = blockIdx.x / hr_count, hr = blockIdx.x - b * hr_count;
+  if ((int)blockIdx.x < joins) {
+    const int seg = blockIdx.x / SPLIT, ch0 = (blockIdx.x - seg * SPLIT) * CH;
+    const int b = seg / hr_count, hr = seg - b * hr_count;
     const int hk = hr / row_groups, rg = hr - hk * row_groups;
     const int rows = min(ROWS, R - rg * ROWS);
     const int64_t row0 = ((int64_t)b * a.hkv + hk) * R + rg * ROWS;
-    if (hr == 0 && threadIdx.x == 0 && clamp_len(a.lens[b], a.capacity) != a.lens[b])
+    if (hr == 0 && ch0 == 0 && threadIdx.x == 0 && clamp_len(a.lens[b], a.capacity) != a.lens[b])
       report_error(a.err, DERR_BAD_ARG, kSiteKv4Len);
     const int nb = wl.blocks(b);
     const int64_t before = wl.total(b);
+    Partials<D, ROWS> P{part, 0, 0};
+    if (nb > 0) {
+      P = partials(before, nb, hr);
+      // nothing to join (the first block stays, so that this launch is not over before the decode kernel is)
+      if (P.g0 == P.g1 && blockIdx.x > 0) return;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int row = threadIdx.x / (CH / 4), ch = ch0 + threadIdx.x % (CH / 4) * 4;  // this thread's four channels
+    uint2* dst = reinterpret_cast<uint2*>(a.o) + ((row0 + row) * D + ch) / 4;
     if (nb == 0) {
-      for (int i = threadIdx.x; i < rows * D / 2; i += kFinishThreads)
-        reinterpret_cast<uint32_t*>(a.o)[row0 * D / 2 + i] = 0u;
-      for (int i = threadIdx.x; i < rows; i += kFinishThreads) a.lse[row0 + i] = -INFINITY;
+      if (row < rows) *dst = make_uint2(0u, 0u);
+      if (ch0 == 0 && (int)threadIdx.x < rows) a.lse[row0 + threadIdx.x] = -INFINITY;
       return;
     }
-    const Partials<D, ROWS> P = partials(before, nb, hr);
     if (P.g0 == P.g1) return;
     const int n = P.g1 - P.g0 + 1;
-    // each row's reference and sum, and each partial's weight: one warp a row
-    for (int row = threadIdx.x >> 5; row < rows; row += kFinishThreads / 32) {
-      const int lane = threadIdx.x & 31;
-      float M = -INFINITY;
-      for (int j = lane; j < n; j += 32) M = fmaxf(M, P.of(P.g0 + j)[ROWS * D + row * 2]);
+    float4 x[kAhead];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      float l = 0.f;
-      for (int j = lane; j < n; j += 32) {
-        const float2 v = *reinterpret_cast<const float2*>(P.of(P.g0 + j) + ROWS * D + row * 2);
-        const float f = v.x == -INFINITY ? 1.f : ex2(v.x - M);  // (no maximum: nothing seen, or only NaN)
-        fac[row][j] = f;
-        l = fmaf(v.y, f, l);
-      }
+    for (int j = 0; j < kAhead; ++j)
+      if (row < rows && j < n) x[j] = *reinterpret_cast<const float4*>(P.of(P.g0 + j) + row * D + ch);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& y, float f) {
+      o.x = fmaf(y.x, f, o.x), o.y = fmaf(y.y, f, o.y), o.z = fmaf(y.z, f, o.z), o.w = fmaf(y.w, f, o.w);
+    };
+    for (int base = 0; base < n; base += kJoinAtOnce) {
+      // each row's reference and sum, and each partial's weight: one warp a row
+      const int count = min(n - base, kJoinAtOnce);
+      for (int r = warp; r < rows; r += kFinishThreads / 32) {
+        const auto ml = [&](int j) { return *reinterpret_cast<const float2*>(P.of(P.g0 + j) + ROWS * D + r * 2); };
+        float2 v = make_float2(-INFINITY, 0.f);
+        if (lane < count) v = ml(base + lane);
+        float M = v.x, l = 0.f;
+        if (base == 0) {
+          for (int j = lane + 32; j < n; j += 32) M = fmaxf(M, ml(j).x);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) {
-        stat[row] = make_float2(M, l);
-        a.lse[row0 + row] = log_sum(M, l) * kLn2;
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kFinishThreads) {
-      const int row = i / (D / 4), c = i - row * (D / 4);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const float f = fac[row][j];
-        const float4 x = *reinterpret_cast<const float4*>(P.of(P.g0 + j) + row * D + c * 4);
-        o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
-      }
-      const float l = stat[row].y, inv = l > 0.f ? 1.f / l : 0.f;
-      reinterpret_cast<uint2*>(a.o)[((row0 + row) * D + c * 4) / 4] =
-          make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
-    }
-    return;
-  }
-  // ---- weights
-  const int tiles = (a.capacity + kWeightSlots - 1) / kWeightSlots;
-  const int wb = (int)blockIdx.x - segments;
-  const int bh = wb / tiles, b = bh / a.hkv, hk = bh - b * a.hkv;
-  const int slot0 = (wb - bh * tiles) * kWeightSlots + threadIdx.x;  // this thread's slots: slot0 + i * kFinishThreads
-  const int len = clamp_len(a.lens[b], a.capacity);
-  if (slot0 - (int)threadIdx.x >= len) return;
-  const int nb = blocks_of(len);
-  const int64_t before = wl.total(b);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int WT = kWeightSlots / kFinishThreads;
-  const int64_t at = (int64_t)bh * a.capacity + slot0;
-  float w[WT], w_in[WT];
-#pragma unroll
-  for (int i = 0; i < WT; ++i) {
-    w[i] = 0.f;
-    w_in[i] = a.w_in && slot0 + i * kFinishThreads < len ? a.w_in[at + i * kFinishThreads] : 0.f;
-  }
-  const float* s = scores + (int64_t)bh * R * a.capacity + slot0;
-  for (int rg = 0; rg < row_groups; ++rg) {
-    // the group's log-sum-exps, from the partials where several CTAs have them (O's block writes L only now)
-    const Partials<D, ROWS> P = partials(before, nb, hk * row_groups + rg);
-    const int rows = min(ROWS, R - rg * ROWS);
-    __syncthreads();
-    for (int row = threadIdx.x >> 5; row < rows; row += kFinishThreads / 32) {
-      const int lane = threadIdx.x & 31;
-      float L;
-      if (P.g0 == P.g1) {
-        L = a.lse[(int64_t)bh * R + rg * ROWS + row] * kLog2e;
-      } else {
-        float M = -INFINITY, l = 0.f;
-        for (int j = P.g0 + lane; j <= P.g1; j += 32) M = fmaxf(M, P.of(j)[ROWS * D + row * 2]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int j = P.g0 + lane; j <= P.g1; j += 32) {
-          const float2 v = *reinterpret_cast<const float2*>(P.of(j) + ROWS * D + row * 2);
-          l = fmaf(v.y, v.x == -INFINITY ? 1.f : ex2(v.x - M), l);
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        } else {
+          M = stat[r].x;
+        }
+        for (int j = lane; j < count; j += 32) {
+          if (j >= 32) v = ml(base + j);
+          const float f = v.x == -INFINITY ? 1.f : ex2(v.x - M);  // (no maximum: nothing seen, or only NaN)
+          fac[r][j] = f;
+          l = fmaf(v.y, f, l);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        L = log_sum(M, l);
+        if (lane == 0) stat[r] = make_float2(M, base == 0 ? l : stat[r].y + l);
       }
-      if (lane == 0) stat[row].x = L;
-    }
-    __syncthreads();
-#pragma unroll 2
-    for (int r = 0; r < rows; ++r) {
-      const float L = stat[r].x;
-      if (L == -INFINITY) continue;
+      __syncthreads();
+      if (row < rows) {
+        if (base == 0) {
 #pragma unroll
-      for (int i = 0; i < WT; ++i)
-        if (slot0 + i * kFinishThreads < len)
-          w[i] += ex2(s[(int64_t)(rg * ROWS + r) * a.capacity + i * kFinishThreads] - L);
+          for (int j = 0; j < kAhead; ++j)
+            if (j < n) add(x[j], fac[row][j]);
+        }
+#pragma unroll 4
+        for (int j = base == 0 ? kAhead : 0; j < count; ++j)
+          add(*reinterpret_cast<const float4*>(P.of(P.g0 + base + j) + row * D + ch), fac[row][j]);
+      }
+      if (base + kJoinAtOnce < n) __syncthreads();
     }
+    if (ch0 == 0 && (int)threadIdx.x < rows)
+      a.lse[row0 + threadIdx.x] = log_sum(stat[threadIdx.x].x, stat[threadIdx.x].y) * kLn2;
+    if (row >= rows) return;
+    const float l = stat[row].y, inv = l > 0.f ? 1.f / l : 0.f;
+    *dst = make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+    return;
   }
+  // ---- weights
+  if constexpr (SCORES) {
+    const int tiles = (a.capacity + kWeightSlots - 1) / kWeightSlots;
+    const int wb = (int)blockIdx.x - joins;
+    const int bh = wb / tiles, b = bh / a.hkv, hk = bh - b * a.hkv;
+    const int slot0 = (wb - bh * tiles) * kWeightSlots + threadIdx.x;  // this thread's slots: slot0 + i * kFinishThreads
+    const int len = clamp_len(a.lens[b], a.capacity);
+    if (slot0 - (int)threadIdx.x >= len) return;
+    const int nb = blocks_of(len);
+    const int64_t before = wl.total(b);
+    Partials<D, ROWS> P = partials(before, nb, hk * row_groups);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int WT = kWeightSlots / kFinishThreads;
+    constexpr int RT = 4;  // rows whose scores are loaded together
+    const int64_t at = (int64_t)bh * a.capacity + slot0;
+    float w[WT], w_in[WT], x[RT][WT];
 #pragma unroll
-  for (int i = 0; i < WT; ++i)
-    if (slot0 + i * kFinishThreads < len) a.w_out[at + i * kFinishThreads] = w_in[i] + w[i];
+    for (int i = 0; i < WT; ++i) {
+      w[i] = 0.f;
+      w_in[i] = a.w_in && slot0 + i * kFinishThreads < len ? a.w_in[at + i * kFinishThreads] : 0.f;
+    }
+    const float* s = scores + (int64_t)bh * R * a.capacity + slot0;
+    auto load = [&](int row0, int rows) {  // scores of rows [row0, row0 + RT) of the head, those below row0 + rows
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < WT; ++i)
+          x[r][i] = r < rows && slot0 + i * kFinishThreads < len
+                        ? s[(int64_t)(row0 + r) * a.capacity + i * kFinishThreads] : -INFINITY;
+    };
+    for (int rg = 0; rg < row_groups; ++rg) {
+      // the group's log-sum-exps, from the partials where several CTAs have them (O's block writes L only now)
+      if (rg > 0) P = partials(before, nb, hk * row_groups + rg);
+      const int rows = min(ROWS, R - rg * ROWS), n = P.g1 - P.g0 + 1;
+      load(rg * ROWS, rows);
+      __syncthreads();
+      for (int row = warp; row < rows; row += kFinishThreads / 32) {
+        float L;
+        if (n == 1) {
+          L = a.lse[(int64_t)bh * R + rg * ROWS + row] * kLog2e;
+        } else {
+          float2 v = make_float2(-INFINITY, 0.f);
+          if (lane < n) v = *reinterpret_cast<const float2*>(P.of(P.g0 + lane) + ROWS * D + row * 2);
+          float M = v.x, l = 0.f;
+          for (int j = lane + 32; j < n; j += 32) M = fmaxf(M, P.of(P.g0 + j)[ROWS * D + row * 2]);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          for (int j = lane; j < n; j += 32) {
+            if (j >= 32) v = *reinterpret_cast<const float2*>(P.of(P.g0 + j) + ROWS * D + row * 2);
+            l = fmaf(v.y, v.x == -INFINITY ? 1.f : ex2(v.x - M), l);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          L = log_sum(M, l);
+        }
+        if (lane == 0) stat[row].x = L;
+      }
+      __syncthreads();
+      for (int r0 = 0; r0 < rows; r0 += RT) {
+        if (r0 > 0) load(rg * ROWS + r0, rows - r0);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          if (r0 + r >= rows) break;
+          const float L = stat[r0 + r].x;
+          if (L == -INFINITY) continue;
+#pragma unroll
+          for (int i = 0; i < WT; ++i) w[i] += ex2(x[r][i] - L);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < WT; ++i)
+      if (slot0 + i * kFinishThreads < len) a.w_out[at + i * kFinishThreads] = w_in[i] + w[i];
+  }
 }
 
 // Groups of 8 query rows that a CTA takes together: two when there are more than 8 rows, so that the cache is
@@ -938,7 +990,7 @@ cudaError_t launch_nt(const DecodeKv4Args& a) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the runs are still going (it waits for them before it reads anything)
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.b * a.hkv * row_groups));
+  cfg.gridDim = dim3((unsigned)(a.b * a.hkv * row_groups) * (D / finish_channels<D, NT>()));
   if (a.w_out) cfg.gridDim.x += (unsigned)((a.capacity + kWeightSlots - 1) / kWeightSlots) * a.b * a.hkv;
   cfg.blockDim = dim3(kFinishThreads);
   cfg.stream = a.stream;
@@ -947,7 +999,8 @@ cudaError_t launch_nt(const DecodeKv4Args& a) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_kv4_finish<D, BF16, NT>, a, (const float*)part, (const float*)scores,
+  auto finish = a.w_out ? decode_kv4_finish<D, BF16, NT, true> : decode_kv4_finish<D, BF16, NT, false>;
+  return cudaLaunchKernelEx(&cfg, finish, a, (const float*)part, (const float*)scores,
                             row_groups, G);
 }
 
