@@ -338,9 +338,8 @@ cudaError_t launch_rows(const Kv4RowArgs& a) {
 // only a row's parameters are used): 28 us, 5.4 TB/s.
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (isnan(w)) return 0xFFFFFFFFu;
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 -> +0
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return isnan(w) ? 0xFFFFFFFFu : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ int evict_len(const Kv4EvictArgs& a, int b) {
@@ -391,13 +390,17 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
   const int part = ((share + kSelThreads - 1) / kSelThreads) * 32;
   const int from = min(hi, lo + warp * part), to = min(hi, from + part);
   const int panels = (part + kSelKeys * 32 - 1) / (kSelKeys * 32);
-  uint32_t key[kSelKeys];
+  uint32_t key[kSelKeys];  // 0, which no number has, behind the candidates
   auto load_panel = [&](int p) {
+    // (all the loads, then the keys: a branch for each would make them wait for one another)
 #pragma unroll
     for (int u = 0; u < kSelKeys; ++u) {
       const int i = from + (p * kSelKeys + u) * 32 + lane;
-      key[u] = i < min(to, m) ? weight_key(w[i]) : 0u;
+      key[u] = __float_as_uint(w[max(min(i, min(to, m) - 1), 0)]);
     }
+#pragma unroll
+    for (int u = 0; u < kSelKeys; ++u)
+      key[u] = from + (p * kSelKeys + u) * 32 + lane < min(to, m) ? weight_key(__uint_as_float(key[u])) : 0u;
   };
   if (panels == 1 && k > 0) load_panel(0);
   // two histograms in turn: the other blocks may still read the last pass's while this one's is filled
@@ -420,8 +423,8 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
         if (panels > 1) load_panel(p);
 #pragma unroll
         for (int u = 0; u < kSelKeys; ++u) {
-          if (from + (p * kSelKeys + u) * 32 + lane >= min(to, m)) break;
-          if (pass == 0)
+          if (from + (p * kSelKeys + u) * 32 >= min(to, m)) break;
+          if (pass == 0)  // (bin 0 is no number's)
             atomicAdd(&copies[(key[u] >> shift) * kSelCopies + (lane & (kSelCopies - 1))], 1u);
           else if ((key[u] & mask) == prefix)
             atomicAdd(&mine[(key[u] >> shift) & digits], 1u);
@@ -451,8 +454,7 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
       }
       if (lane == 31) warp_sum[warp] = incl;
       __syncthreads();
-      unsigned before = incl - c0 - c1;
-      for (int j = 0; j < warp; ++j) before += warp_sum[j];
+      const unsigned before = incl - c0 - c1 + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
       if (before < left && before + c0 + c1 >= left) {
         const bool first = before + c0 >= left;
         sel_digit = (unsigned)(first ? top : top - 1);
@@ -464,21 +466,29 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
       left = sel_left;
     }
   }
-  // slots of key > prefix stay, the first `left` of those equal to it, and the newest
-  auto kind = [&](int i, uint32_t ky, bool* above, bool* equal) {
-    *above = i < to && (i >= m || (k > 0 && ky > prefix));
-    *equal = i < min(to, m) && k > 0 && ky == prefix;
-  };
-  unsigned na = 0, ne = 0;
-  for (int p = 0; p < panels; ++p) {
-    if (panels > 1 && k > 0) load_panel(p);
+  // slots of key > prefix stay, the first `left` of those equal to it, and the newest: of a panel's slots, bit u
+  // for this lane's u-th one
+  auto decide = [&](int p, unsigned* above, unsigned* equal) {
+    unsigned gt = 0, eq = 0;
 #pragma unroll
     for (int u = 0; u < kSelKeys; ++u) {
-      bool above, equal;
-      kind(from + (p * kSelKeys + u) * 32 + lane, key[u], &above, &equal);
-      na += above;
-      ne += equal;
+      gt |= key[u] > prefix ? 1u << u : 0u;
+      eq |= key[u] == prefix ? 1u << u : 0u;
     }
+    auto below = [&](int end) {  // bits of the slots in front of `end`
+      const int c = (end - (from + p * kSelKeys * 32 + lane) + 31) >> 5;
+      return (1u << min(max(c, 0), kSelKeys)) - 1u;
+    };
+    const unsigned old = below(min(to, m)), any = below(to);
+    *above = (any & ~old) | (k > 0 ? gt & old : 0u);
+    *equal = k > 0 ? eq & old : 0u;
+  };
+  unsigned na = 0, ne = 0, above = 0, equal = 0;
+  for (int p = 0; p < panels; ++p) {
+    if (panels > 1 && k > 0) load_panel(p);
+    decide(p, &above, &equal);
+    na += __popc(above);
+    ne += __popc(equal);
   }
   na = __reduce_add_sync(0xffffffffu, na);
   ne = __reduce_add_sync(0xffffffffu, ne);
@@ -488,37 +498,49 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
     warp_eq[warp] = ne;
   }
   __syncthreads();
-  unsigned above_before = 0, eq_before = 0, above_all = 0, eq_all = 0;
-  for (int j = 0; j < kSelWarps; ++j) {
-    if (j == warp) above_before = above_all, eq_before = eq_all;
-    above_all += warp_sum[j];
-    eq_all += warp_eq[j];
-  }
-  if (tid == 0) totals[0] = above_all, totals[1] = eq_all;
+  unsigned above_before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
+  unsigned eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? warp_eq[lane] : 0u);
+  if (tid == kSelThreads - 1) totals[0] = above_before + na, totals[1] = eq_before + ne;
   sync_all();
   for (int j = 0; j < rank; ++j) {
     const unsigned* t = remote(totals, j);
     above_before += t[0];
     eq_before += t[1];
   }
+  // no block leaves while another may read its shared memory
+  if constexpr (CLUSTER) cluster.barrier_arrive();
   const unsigned under = (1u << lane) - 1u;
   for (int p = 0; p < panels; ++p) {
-    if (panels > 1 && k > 0) load_panel(p);
+    if (panels > 1) {
+      if (k > 0) load_panel(p);
+      decide(p, &above, &equal);
+    }
+    int i = from + p * kSelKeys * 32 + lane;
+    if (ne == 0) {  // (none in the warp's share) four at a time
+      unsigned at = above_before + min(eq_before, left);
+#pragma unroll 1
+      for (int u = 0; u < kSelKeys && i - lane < to; u += 4, i += 128, above >>= 4) {
 #pragma unroll
-    for (int u = 0; u < kSelKeys; ++u) {
-      const int i = from + (p * kSelKeys + u) * 32 + lane;
-      if (i - lane >= to) break;
-      bool above, equal;
-      kind(i, key[u], &above, &equal);
-      const unsigned ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
+        for (int v = 0; v < 4; ++v) {
+          const unsigned ba = __ballot_sync(0xffffffffu, above >> v & 1u), pos = at + __popc(ba & under);
+          if ((above >> v & 1u) && pos < (unsigned)a.keep) kept[pos] = i + v * 32;
+          at += __popc(ba);
+        }
+      }
+      above_before = at - min(eq_before, left);
+      continue;
+    }
+#pragma unroll 1
+    for (int u = 0; u < kSelKeys && i - lane < to; ++u, i += 32, above >>= 1, equal >>= 1) {
+      const unsigned ba = __ballot_sync(0xffffffffu, above & 1u), be = __ballot_sync(0xffffffffu, equal & 1u);
       const unsigned my_eq = eq_before + __popc(be & under);  // equal ones in front of this slot
       const unsigned pos = above_before + __popc(ba & under) + min(my_eq, left);
-      if ((above || (equal && my_eq < left)) && pos < (unsigned)a.keep) kept[pos] = i;
+      if (((above & 1u) || ((equal & 1u) && my_eq < left)) && pos < (unsigned)a.keep) kept[pos] = i;
       above_before += __popc(ba);
       eq_before += __popc(be);
     }
   }
-  if constexpr (CLUSTER) cluster.sync();  // no block leaves while another may read its shared memory
+  if constexpr (CLUSTER) cluster.barrier_wait();
 }
 
 template <int D>
