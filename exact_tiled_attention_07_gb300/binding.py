@@ -187,6 +187,25 @@ def _on_device(*ts, strided=()):
             raise ValueError("all device arguments must be on one GPU")
 
 
+def _ready(*ts, strided=()):
+    """_on_device for the calls of a generation step, whose checks cost more than their kernels: one
+    query a tensor; where something is not as it should be, _on_device says what."""
+    first = strided[0] if strided else ts[0]
+    dev = first.get_device()
+    ok = dev >= 0 and dev == torch._C._cuda_getDevice()
+    for t in strided:
+        ok = ok and t.get_device() == dev
+    for t in ts:
+        ok = ok and (t is None or (t.get_device() == dev and t.is_contiguous()))
+    if not ok:
+        _on_device(*ts, strided=strided)
+
+
+def _current(stream):
+    """_stream after _ready (CUDA is up)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else _stream(stream)
+
+
 def _rows(L, n, what="L"):
     """L (or another per-row vector) is an fp32 tensor of n elements."""
     if L.dtype != torch.float32 or L.numel() != n:
@@ -448,18 +467,19 @@ def fa_fwd_varlen(Q, K, V, O, L, cu_seqlens, scale, causal, stream=None):
     Tk, Hkv, dk, k_ts, k_hs = _packed(K, "K")
     _, _, _, v_ts, v_hs = _packed(V, "V")
     _, _, _, o_ts, o_hs = _packed(O, "O")
-    _on_device(L, cu_seqlens, strided=(Q, K, V, O))
+    _ready(L, cu_seqlens, strided=(Q, K, V, O))
     if (Tk, dk) != (T, d) or Hkv < 1 or H % Hkv:
         raise ValueError("K must be [T, Hkv, d] with H a multiple of Hkv")
     if V.shape != K.shape or O.shape != Q.shape or not (Q.dtype == K.dtype == V.dtype == O.dtype):
         raise ValueError("V must have K's shape, O must have Q's, and all four one dtype")
     _rows(L, H * T)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    n = cu_seqlens.numel()
+    if cu_seqlens.dim() != 1 or n < 1:
         raise ValueError("cu_seqlens must be an int32 tensor of S + 1 elements")
-    _int32(cu_seqlens, cu_seqlens.numel(), "cu_seqlens")
-    _check(load_library().fa_fwd_varlen(_p(Q), _p(K), _p(V), _p(O), _p(L), _p(cu_seqlens), cu_seqlens.numel() - 1, T, H,
-                                        Hkv, d, q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs, float(scale),
-                                        int(bool(causal)), _dt(Q), _stream(stream)))
+    _int32(cu_seqlens, n, "cu_seqlens")
+    _check(load_library().fa_fwd_varlen(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(),
+                                        cu_seqlens.data_ptr(), n - 1, T, H, Hkv, d, q_ts, q_hs, k_ts, k_hs, v_ts, v_hs,
+                                        o_ts, o_hs, scale, bool(causal), _dt(Q), _current(stream)))
 
 
 def _kv4_shape(cache):
@@ -487,7 +507,7 @@ def _kv4_rows(K, V, cu_seqlens, lens, cache, weights):
     B, Hkv, capacity, d = _kv4_shape(cache)
     T, hk, dk, k_ts, k_hs = _packed(K, "K")
     _, _, _, v_ts, v_hs = _packed(V, "V")
-    _on_device(cu_seqlens, lens, cache, weights, strided=(K, V))
+    _ready(cu_seqlens, lens, cache, weights, strided=(K, V))
     if (hk, dk) != (Hkv, d) or V.shape != K.shape or V.dtype != K.dtype:
         raise ValueError("K, V must be [T, Hkv, d] of one dtype with the cache's heads and head dimension")
     _int32(cu_seqlens, B + 1, "cu_seqlens")
@@ -502,13 +522,13 @@ def fa_kv4_append(K, V, cu_seqlens, lens, cache, weights=None, stream=None):
     to 0 at the new slots."""
     args = _kv4_rows(K, V, cu_seqlens, lens, cache, weights)
     _check(load_library().fa_kv4_append(_p(K), _p(V), _p(cu_seqlens), _p(lens), _p(cache), _p(weights), *args,
-                                        _stream(stream)))
+                                        _current(stream)))
 
 
 def fa_kv4_read(cache, cu_seqlens, lens, K, V, stream=None):
     """The values of the newest slots into packed K, V [T, Hkv, d]: the inverse of fa_kv4_append."""
     args = _kv4_rows(K, V, cu_seqlens, lens, cache, None)
-    _check(load_library().fa_kv4_read(_p(cache), _p(cu_seqlens), _p(lens), _p(K), _p(V), *args, _stream(stream)))
+    _check(load_library().fa_kv4_read(_p(cache), _p(cu_seqlens), _p(lens), _p(K), _p(V), *args, _current(stream)))
 
 
 def fa_decode_kv4_workspace_size(B, H, Hkv, Nq, capacity, d, weights=False) -> int:
@@ -520,20 +540,22 @@ def fa_decode_kv4(Q, cache, lens, O, L, scale, causal=False, weights_in=None, we
     """Decode: Q, O [B, H, Nq, d] over a 4-bit cache with lens [B] slots in use; L [B, H, Nq].
     weights_out [B, Hkv, capacity] = weights_in + the attention each slot got (slots in use)."""
     shape = _kv4_decode_shape(Q, cache, lens, weights_in, weights_out)
-    _on_device(O, L, Q, workspace)
+    _ready(O, L, Q, workspace)
     _same(Q, O)
     _rows(L, O.numel() // O.shape[3])
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load_library().fa_decode_kv4(_p(Q), _p(cache), _p(lens), _p(O), _p(L), _p(weights_in), _p(weights_out),
                                         *shape, float(scale), int(bool(causal)), _dt(Q), _p(workspace), nbytes,
-                                        _stream(stream)))
+                                        _current(stream)))
 
 
 def _kv4_decode_shape(Q, cache, lens, weights_in, weights_out):
     """(B, H, Hkv, Nq, capacity, d) of a decode over a 4-bit cache, after checking what it reads."""
-    B, H, Nq, d = _shape4(Q)
+    if Q.dim() != 4 or not Q.is_contiguous():
+        _shape4(Q)
+    B, H, Nq, d = Q.shape
     Bc, Hkv, capacity, dc = _kv4_shape(cache)
-    _on_device(Q, cache, lens, weights_in, weights_out)
+    _ready(Q, cache, lens, weights_in, weights_out)
     if (Bc, dc) != (B, d):
         raise ValueError("the cache must have Q's batch and head dimension")
     _int32(lens, B, "lens")
@@ -547,7 +569,7 @@ def fa_kv4_evict(cache, weights, lens, keep, recent, out_cache, out_weights, out
     their order into another cache (with weights and lens); kept [B, Hkv, keep]: where they were."""
     B, Hkv, capacity, d = _kv4_shape(cache)
     Bo, ho, out_capacity, do = _kv4_shape(out_cache)
-    _on_device(cache, weights, lens, out_cache, out_weights, out_lens, kept)
+    _ready(cache, weights, lens, out_cache, out_weights, out_lens, kept)
     if (Bo, ho, do) != (B, Hkv, d):
         raise ValueError("out_cache must have the cache's batch, heads and head dimension")
     if weights is None or out_weights is None:
@@ -559,7 +581,7 @@ def fa_kv4_evict(cache, weights, lens, keep, recent, out_cache, out_weights, out
     _int32(kept, B * Hkv * int(keep), "kept")
     _check(load_library().fa_kv4_evict(_p(cache), _p(weights), _p(lens), int(keep), int(recent), _p(out_cache),
                                        _p(out_weights), _p(out_lens), _p(kept), B, Hkv, capacity, out_capacity, d,
-                                       _stream(stream)))
+                                       _current(stream)))
 
 
 def fa_selftest_bounded_wait(timeout_ms=20, arrive=False, stream=None):
@@ -709,13 +731,15 @@ def attention_decode_kv4(q, cache, lens, causal=False, scale=None, weights_in=No
     allocated with torch."""
     shape = B, H, Hkv, Nq, capacity, d = _kv4_decode_shape(q, cache, lens, weights_in, weights_out)
     lib = load_library()
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    nbytes = lib.fa_decode_kv4_workspace_size(*shape, int(weights_out is not None))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    _check(lib.fa_decode_kv4(_p(q), _p(cache), _p(lens), _p(o), _p(lse), _p(weights_in), _p(weights_out), *shape,
+    dev = q.device
+    o = torch.empty((B, H, Nq, d), dtype=q.dtype, device=dev)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    nbytes = lib.fa_decode_kv4_workspace_size(*shape, weights_out is not None)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _check(lib.fa_decode_kv4(q.data_ptr(), cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                             _p(weights_in), _p(weights_out), *shape,
                              d ** -0.5 if scale is None else float(scale), int(bool(causal)), _dt(q), _p(ws), nbytes,
-                             _stream(stream)))
+                             _current(stream)))
     _used_on(stream, o, lse, ws)
     return o, lse
 

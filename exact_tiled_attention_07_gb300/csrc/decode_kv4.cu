@@ -15,7 +15,7 @@
 // fp16, fp32 sums) operands.  Masked out of its word, a nibble is an fp16 subnormal, c 2^-24 where it stands
 // lowest and c 2^-20 next to that: 4 masks and a shift for 8 codes, nothing to convert; what the codes are
 // multiplied with and the sums carry the powers of two, and the offset of 8 is taken off in fp32.
-// Measured, 32 x 8 heads of 32,768 slots, d = 128, four rows a head (1.21 GB): 205 us, 5.9 TB/s, 0.87 of the
+// Measured, 32 x 8 heads of 32,768 slots, d = 128, four rows a head (1.21 GB): 211 us, 5.7 TB/s, 0.84 of the
 // measured copy rate; with the arithmetic left out 194.  Other forms of it:
 //   * codes to fp16 numbers by or-ing them into 1024 and taking that and 8 off (9 instructions for 8 codes): 236 us,
 //     313 with the or's constant as an immediate (each mask-and-or two instructions);

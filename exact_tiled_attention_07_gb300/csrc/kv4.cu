@@ -327,12 +327,15 @@ cudaError_t launch_rows(const Kv4RowArgs& a) {
 // as 32-bit keys that order like the numbers (NaN above everything, -0 as 0); the k-th largest key is found
 // digit by digit (10, 11 and 11 bits: three histogram passes over the keys, which stay in L2 or L1;
 // the blocks of a cluster add up each other's histograms through distributed shared memory, so all find the
-// same digit); then each warp walks its share of the slots twice, counting and writing those above
-// the threshold key, the first ones equal to it, and the newest.  Bound by the shared-memory atomics of
-// the first pass, whose digit (sign, exponent, one bit) takes few values: 16 copies of that histogram, one
-// per pair of lanes.
-// Measured for 8 x 8 heads of 32,768 slots, 8,192 to stay: 28 us (two blocks a head); 44 with one block a head
-// and the keys read again in every pass, 47 with four blocks, of which only half are resident.
+// same digit); then each lane decides over its slots, and each warp writes those above the threshold key, the
+// first ones equal to it, and the newest, behind what the warps and blocks before it keep.  Bound by latency:
+// 5,000 cycles until the weights are there, 7,000 for the first pass (its digit, sign, exponent and one bit, takes
+// few values: 16 copies of that histogram, one per pair of lanes), 5,000 for each of the others, 8,000 for
+// deciding and writing.
+// Measured for 8 x 8 heads of up to 32,768 slots, 8,192 to stay: 17 us (two blocks a head).  28 with a branch around
+// each weight's load, which made the loads wait for one another, sums over warps one by one, and blocks that stay
+// until their stores are done; in that form 44 with one block a head and the keys read again in every pass, 47 with
+// four blocks, of which only half are resident.
 // kv4_gather_kernel: one block per 64 kept slots of a head, a block of the new cache, all of a thread's loads
 // before its stores.  Bound: HBM (151 MB moved for those heads, and half as much again in sectors of which
 // only a row's parameters are used): 28 us, 5.4 TB/s.
