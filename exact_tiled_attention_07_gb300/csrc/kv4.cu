@@ -337,8 +337,9 @@ cudaError_t launch_rows(const Kv4RowArgs& a) {
 // until their stores are done; in that form 44 with one block a head and the keys read again in every pass, 47 with
 // four blocks, of which only half are resident.
 // kv4_gather_kernel: one block per 64 kept slots of a head, a block of the new cache, all of a thread's loads
-// before its stores.  Bound: HBM (151 MB moved for those heads, and half as much again in sectors of which
-// only a row's parameters are used): 28 us, 5.4 TB/s.
+// before its stores.  Bound: HBM: 151 MB moved for those heads, and more read beside it, as a kept row of codes is 64
+// bytes and its parameters 8: 25 us; 28 with plain loads of codes, for which L2 fetches 128 bytes (140 MB read instead
+// of 101 for sequences of 8,000 to 32,768).
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   const uint32_t u = __float_as_uint(w + 0.f);  // -0 -> +0
@@ -546,6 +547,15 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4EvictA
   if constexpr (CLUSTER) cluster.barrier_wait();
 }
 
+// 16 bytes whose neighbours beyond 64 are not wanted: L2 fetches 64 bytes instead of 128
+__device__ __forceinline__ uint4 load_alone(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, int blocks_per_head) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched while the selection is still going)
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(256) kv4_gather_kernel(const Kv4EvictArgs a, i
   for (int u = 0; u < N; ++u) {
     const int i = u * 256 + threadIdx.x, which = i / (kKv4Block * PER), row = (i / PER) % kKv4Block;
     if (from[row] >= 0)
-      codes[u] = *reinterpret_cast<const uint4*>(row_of(from[row], kv4_codes_at(D, which), kv4_code_bytes(D)) + i % PER * 16);
+      codes[u] = load_alone(row_of(from[row], kv4_codes_at(D, which), kv4_code_bytes(D)) + i % PER * 16);
   }
 #pragma unroll
   for (int u = 0; u < NP; ++u) {
