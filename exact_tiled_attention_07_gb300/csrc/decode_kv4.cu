@@ -34,6 +34,11 @@
 //     fp16 (2^-11), and what the offset of 8 takes off is counted with the rounded one, so the error is that of
 //     code - 8; for fp16 queries the rounding error is a second operand, so that only O's own
 //     rounding is left.  P^T comes out of the S^T accumulators by movmatrix.
+//     The codes' offset of 8 (with the middles, in fp32: corr) comes off the sums every kFold tokens of a warp, not only
+//     at the end: sums of codes 0 to 15 grow to hundreds of times what is left of them, and mma.sync truncates its
+//     fp32 sums at every step.  Relative to O's rms over 65,536 slots at 400 blocks a CTA (d = 64, fp16 queries) the
+//     error is 2.2e-4, of which 2e-4 are O's own rounding; 4.8e-3 with the offset taken off at the end.
+//     1.4 % of the time of the 1.21 GB case; 256 tokens measure the same within 1 us and err by twice as much.
 //     Range: P step_V is kept below 2^13 by a running exponent E of the steps met so far, which is part of the
 //     reference of the exponentials just as the running maximum is: P = 2^(S - m - E + 8), where m may lag
 //     behind the maximum by 4.
@@ -60,6 +65,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 8.f;  // P is kept as 2^(S - m + 8)
 constexpr float kRaise = 4.f;   // the reference m is raised when it is this far (log2) below the maximum
+constexpr int kFold = 128;      // tokens of a warp after which the codes' offset comes off its sums
 constexpr float kNoScore = 1e30f;  // off before the first score: 2^(-inf + 1e30) is still 0
 constexpr uint32_t kSiteKv4Full = 930, kSiteKv4Drain = 931, kSiteKv4Empty = 932, kSiteKv4Len = 933;
 
@@ -433,6 +439,27 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o_acc[i][nt][e] = 0.f;
 
+    // corr, which the lanes hold for tokens of their own, into the sums of O (in units of 2^-24 and 2^-20)
+    auto fold = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int gr = 0; gr < C::GROUPS; ++gr) {
+          float2 c = corr[gr][nt];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            c = fadd2(c, make_float2(__shfl_xor_sync(0xffffffffu, c.x, o), __shfl_xor_sync(0xffffffffu, c.y, o)));
+          const float2 even = fmul2(c, make_float2(0x1p-24f, 0x1p-24f)), odd = fmul2(c, make_float2(0x1p-20f, 0x1p-20f));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float(&x)[4] = o_acc[gr * 4 + i][nt];
+            const float2 a = fadd2(make_float2(x[0], x[1]), even), b = fadd2(make_float2(x[2], x[3]), odd);
+            x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+          }
+          corr[gr][nt] = make_float2(0.f, 0.f);
+        }
+    };
+
     for (int blk = blk0 + turn<C::TEAMS>(team - rot); ok && blk < blk1; blk += C::TEAMS) {
       const int s = uses % C::STAGES;
       ok = __all_sync(0xffffffffu, mbar_wait(full + s, (uint32_t)(uses / C::STAGES) & 1, ctx, kSiteKv4Full));
@@ -637,6 +664,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
       __syncwarp();
       if (C::TEAM > 1 && lane == 0) mbar_arrive(empty + s);
       load_next();
+      if (uses % (kFold / C::TOK) == 0) fold();
     }
 
     if (nan_seen[warp]) {  // rows that see one of the newest slots that hold NaN
@@ -658,6 +686,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
     }
 
     // ---- join the warps: rows' maxima and sums, then O 64 channels at a time
+    fold();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -666,15 +695,9 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
-        for (int gr = 0; gr < C::GROUPS; ++gr) {
-          float c = e ? corr[gr][nt].y : corr[gr][nt].x;
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o_acc[gr * 4 + i][nt][e] = fmaf(o_acc[gr * 4 + i][nt][e], 0x1p24f, c);
-            o_acc[gr * 4 + i][nt][e + 2] = fmaf(o_acc[gr * 4 + i][nt][e + 2], 0x1p20f, c);
-          }
+        for (int i = 0; i < D / 16; ++i) {
+          o_acc[i][nt][e] *= 0x1p24f;
+          o_acc[i][nt][e + 2] *= 0x1p20f;
         }
         const float r = e ? off[nt].y : off[nt].x;
         const float ref = r == kNoScore ? -INFINITY : kPShift - r;  // m + E of this warp's exponentials
