@@ -32,16 +32,21 @@
 //   O^T = V^T P^T: V^T is the A operand (16 channels x 16 tokens): a register holds one channel of two
 //     tokens, so the words of two tokens are interleaved by halves first.  P step_V is rounded to
 //     fp16 (2^-11), and what the offset of 8 takes off is counted with the rounded one, so the error is that of
-//     code - 8; for fp16 queries the rounding error is a second operand, so that only O's own
-//     rounding is left.  P^T comes out of the S^T accumulators by movmatrix.
+//     code - 8; for fp16 queries the rounding error is a second operand, so that little more than
+//     O's own rounding is left.  P^T comes out of the S^T accumulators by movmatrix.
 //     The codes' offset of 8 (with the middles, in fp32: corr) comes off the sums every kFold tokens of a warp, not only
 //     at the end: sums of codes 0 to 15 grow to hundreds of times what is left of them, and mma.sync truncates its
 //     fp32 sums at every step.  Relative to O's rms over 65,536 slots at 400 blocks a CTA (d = 64, fp16 queries) the
 //     error is 2.2e-4, of which 2e-4 are O's own rounding; 4.8e-3 with the offset taken off at the end.
 //     1.4 % of the time of the 1.21 GB case; 256 tokens measure the same within 1 us and err by twice as much.
-//     Range: P step_V is kept below 2^13 by a running exponent E of the steps met so far, which is part of the
-//     reference of the exponentials just as the running maximum is: P = 2^(S - m - E + 8), where m may lag
-//     behind the maximum by 4.
+//     Range: P = 2^(S - m + 8) with a reference m of each row that keeps the products P step_V, which are rounded,
+//     inside fp16's range, and not P alone: m is raised where a product might pass 2^15.5 and does pass 2^9, so that the
+//     step's largest comes to 2^8.  Whether one might is seen from the largest score and the block's largest step.  So
+//     each product keeps fp16's precision down to 2^-22 of the row's largest product (what is smaller, and the rounding
+//     error of fp16 queries, an absolute 2^-33 of it), whatever steps other rows' slots or slots of no weight
+//     have.  With m the largest score and the steps' largest exponent: 1 to 2.5 % off where a slot of step 4,096 and
+//     no weight stands among every 32 of step 0.002; a scale of each row's 64 channels on top of m: 4 to 8 % more time at
+//     d = 128 and 256.
 //
 // Work split: the 64-slot blocks of all (sequence, key/value head, group of 8 NT query rows) form one list;
 // each CTA takes an equal run of it, whatever the lengths of the sequences, found on the device
@@ -64,7 +69,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 8.f;  // P is kept as 2^(S - m + 8)
-constexpr float kRaise = 4.f;   // the reference m is raised when it is this far (log2) below the maximum
+constexpr float kMostProduct = 15.5f;  // log2 of P step, at most (fp16 ends below 2^16)
+constexpr float kMostP = 28.f;         // log2 of P where no step bounds it (fp16's smallest is 2^-24)
 constexpr int kFold = 128;      // tokens of a warp after which the codes' offset comes off its sums
 constexpr float kNoScore = 1e30f;  // off before the first score: 2^(-inf + 1e30) is still 0
 constexpr uint32_t kSiteKv4Full = 930, kSiteKv4Drain = 931, kSiteKv4Empty = 932, kSiteKv4Len = 933;
@@ -134,6 +140,13 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+
+// The offset (P = 2^(S + off)) that brings a step's largest product, prod + off, to 2^8 where it is above 2^9, and its
+// largest P, top + off, to 2^kMostP where it is more than the smallest step's bound lets by
+__device__ __forceinline__ float lowered(float off, float prod, float top) {
+  const float next = prod + off > 9.f ? 8.f - prod : off;
+  return top + next > kMostProduct + 14.f ? kMostP - top : next;
 }
 
 // The four nibbles of each half of x as four pairs of fp16: codes times 2^-24 (even) and 2^-20 (odd), as
@@ -342,9 +355,8 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
   for (int s = 0; s < C::STAGES; ++s) load_next();
 
   float o_acc[D / 16][NT][4];  // tile 4 gr + i: channels 64 gr + 8 g + 2 i (+ 1), rows 2t (+ 1)
-  // pairs: rows 2t, 2t + 1.  P = 2^(S + off), off = 8 - m - E for the m and E in use
+  // pairs: rows 2t, 2t + 1.  P = 2^(S + off), off = 8 - m for the m in use
   float2 off[NT], l_run[NT], corr[C::GROUPS][NT];
-  int e_run;  // exponent of the largest V step so far
   uint32_t qf[D / 16][NT][2];
   float2 qsum[C::GROUPS][NT], cf[NT];
   const int kap = (g >> 1) + (g & 1) * 4;  // token of operand row g: rows 2t, 2t + 1 are tokens t, t + 4
@@ -424,7 +436,6 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
         const int row = row0 + nt * 8 + 2 * t + e;
         last[nt][e] = a.causal ? sp.len - a.nq + row % a.nq + 1 : sp.len;
       }
-    e_run = -15;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       off[nt] = make_float2(kNoScore, kNoScore);
@@ -482,29 +493,15 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
       }
       const uint32_t* kpar = reinterpret_cast<const uint32_t*>(blkp + kv4_params_at(D, 0));
       const uint32_t* vpar = reinterpret_cast<const uint32_t*>(blkp + kv4_params_at(D, 1));
+      // log2 P up to which no product can be too large: from the largest V step of this warp's tokens (fp16 bits of
+      // numbers >= 0 order like the numbers; below 2^(exponent + 1))
+      float most;
       {
-        // the largest V step of this warp's tokens (fp16 bits of numbers >= 0 order like the numbers)
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < C::TOK * C::GROUPS / 32; ++i)
           top = max(top, vpar[half * C::TOK * C::GROUPS + i * 32 + lane] & 0x7FFFu);
-        const int e_blk = (int)(__reduce_max_sync(0xffffffffu, top) >> 10) - 15;
-        if (e_blk > e_run) {
-          const float down = __uint_as_float((uint32_t)(127 + e_run - e_blk) << 23);
-          const float drop = (float)(e_run - e_blk);
-          e_run = e_blk;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            off[nt] = fadd2(off[nt], make_float2(drop, drop));
-            l_run[nt] = fmul2(l_run[nt], make_float2(down, down));
-#pragma unroll
-            for (int gr = 0; gr < C::GROUPS; ++gr) corr[gr][nt] = fmul2(corr[gr][nt], make_float2(down, down));
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o_acc[i][nt][e] *= down;
-          }
-        }
+        most = kMostProduct - 1.f - (float)((int)(__reduce_max_sync(0xffffffffu, top) >> 10) - 15);
       }
 #pragma unroll 1
       for (int step = 0; step < C::TOK / 32; ++step) {
@@ -576,17 +573,31 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
           }
           float2 mx = make_float2(fmaxf(max3(sc[0][nt][0].x, sc[0][nt][1].x, sc[1][nt][0].x), sc[1][nt][1].x),
                                   fmaxf(max3(sc[0][nt][0].y, sc[0][nt][1].y, sc[1][nt][0].y), sc[1][nt][1].y));
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
-            mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
-          }
-          // the reference follows the maximum only when it has fallen kRaise behind it (P <= 2^(8 + kRaise - E))
           const float2 z = ffma2v(mx, cf[nt], off[nt]);
-          const float top = kPShift - (float)e_run;
-          if (__any_sync(0xffffffffu, fmaxf(z.x, z.y) > top + kRaise)) {
+          if (__any_sync(0xffffffffu, fmaxf(z.x, z.y) > most)) {
+            // largest score and largest product (log2, without the reference) of the step
+            float2 prod = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float st = 0.f;
+#pragma unroll
+                for (int gr = 0; gr < C::GROUPS; ++gr)  // (a NaN is left out)
+                  st = fmaxf(st, unpack2<false>(vpar[(tok0 + mt * 16 + kap + e * 8) * C::GROUPS + gr]).x);
+                st = __log2f(st);
+                prod.x = fmaxf(prod.x, fmaf(sc[mt][nt][e].x, cf[nt].x, st));
+                prod.y = fmaxf(prod.y, fmaf(sc[mt][nt][e].y, cf[nt].y, st));
+              }
             mx = fmul2(mx, cf[nt]);
-            const float2 next = make_float2(fminf(off[nt].x, top - mx.x), fminf(off[nt].y, top - mx.y));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+              mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
+              prod.x = fmaxf(prod.x, __shfl_xor_sync(0xffffffffu, prod.x, o));
+              prod.y = fmaxf(prod.y, __shfl_xor_sync(0xffffffffu, prod.y, o));
+            }
+            const float2 next = make_float2(lowered(off[nt].x, prod.x, mx.x), lowered(off[nt].y, prod.y, mx.y));
             const float2 alpha = make_float2(ex2(next.x - off[nt].x), ex2(next.y - off[nt].y));
             off[nt] = next;
             l_run[nt] = fmul2(l_run[nt], alpha);
@@ -700,7 +711,7 @@ __global__ void __launch_bounds__(Kv4Cfg<D, NT>::THREADS, Kv4Cfg<D, NT>::CTAS)
           o_acc[i][nt][e + 2] *= 0x1p20f;
         }
         const float r = e ? off[nt].y : off[nt].x;
-        const float ref = r == kNoScore ? -INFINITY : kPShift - r;  // m + E of this warp's exponentials
+        const float ref = r == kNoScore ? -INFINITY : kPShift - r;  // m of this warp's exponentials
         if (g == 0)
           *reinterpret_cast<float2*>(ml + (warp * C::ROWS + nt * 8 + 2 * t + e) * 2) = make_float2(ref, l);
       }

@@ -359,9 +359,10 @@ FA_API fa_status fa_kv4_read(const void* cache, const int32_t* cu_seqlens, const
  *   workspace fa_decode_kv4_workspace_size(...) bytes for the same arguments (weights: whether
  *             weights_out is given); its contents on entry do not matter. Calls that may overlap on the
  *             GPU need workspaces of their own.
- * Keys, values and scores are never rounded to 16 bits; bf16 queries' probabilities times the values' steps enter the
- * second product rounded to fp16 (relative 2^-11), fp16 queries' with the rounding error as a second operand. The work is cut into equal runs of blocks on the device, whatever
- * the lengths. Results do not depend on timing: two calls with the same arguments give the same bits.
+ * Keys, values and scores are never rounded to 16 bits; probabilities times the values' steps enter the second product
+ * rounded to fp16: for bf16 queries by 2^-11 of each, for fp16 queries, whose rounding errors are a second operand, by
+ * 2^-22, and in either case by no less than 2^-33 of the row's largest such product (2^-29 where all of its steps are
+ * below 2^-20). The work is cut into equal runs of blocks on the device, whatever the lengths. Results do not depend on timing: two calls with the same arguments give the same bits.
  */
 FA_API size_t fa_decode_kv4_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d, int weights);
 FA_API fa_status fa_decode_kv4(const void* Q, const void* cache, const int32_t* lens, void* O, float* L,
