@@ -156,7 +156,7 @@ __device__ __forceinline__ int warp_sequence(const int32_t* __restrict__ cu, int
 constexpr int kRowWarps = 8;  // rows of a block: one warp each
 
 // A warp takes CH x 32 words (8 channels each) of a row's key/value heads: a lane loads 16 bytes of
-// 16-bit elements, keys and values, before anything else is known; the 8 lanes of a group find its minimum
+// 16-bit elements, keys and values, before the row's sequence and slot are known; the 8 lanes of a group find its minimum
 // and maximum together and a lane's codes are one 32-bit word.  The quotient is taken as a product with an
 // approximate 1 / step (2^-23), which is within 2^-19 of the IEEE quotient for |quotient| <= 8.5;
 // where one lies within 2^-17 of a half (exact halves are one in 1,200 of bf16 data) or beyond the codes, the
@@ -171,8 +171,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv4_append_kernel(const Kv4Row
   constexpr int kWords = D / 8;  // of a row of one head
   const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= a.t) return;
+  // (rows of no sequence need not be there: nothing of them is read)
+  if (r < a.cu[0] || r >= a.cu[a.b]) return;
   const int words = a.hkv * kWords;
   const int w0 = blockIdx.y * (CH * 32) + lane;
+  int no_abort = 0;
+  if (!debug_check(r >= a.cu[0] && r < a.cu[a.b], ErrCtx{a.err, &no_abort}, kSiteAppend)) return;
   Raw<T> x[CH][2];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
