@@ -145,7 +145,8 @@ fa_status check_kv4(int B, int Hkv, int capacity, int d, bool* empty) {
     return fail(FA_ERR_UNSUPPORTED, "the 4-bit cache supports d in {64, 128, 256}, got %d", d);
   if (capacity < 64 || capacity % 64 != 0)
     return fail(FA_ERR_INVALID_ARG, "capacity=%d is not a positive multiple of 64", capacity);
-  if ((int64_t)B * Hkv > INT32_MAX / 4 || (int64_t)Hkv * (capacity / 64) > INT32_MAX ||
+  // (kernels count slots in 32 bits, up to a block's share of them behind the last)
+  if (capacity > INT32_MAX - 4096 || (int64_t)B * Hkv > INT32_MAX / 4 || (int64_t)Hkv * (capacity / 64) > INT32_MAX ||
       (double)B * Hkv * capacity * d > 4.0e15)
     return fail(FA_ERR_INVALID_ARG, "cache too large: B=%d Hkv=%d capacity=%d", B, Hkv, capacity);
   if (B == 0) *empty = true;

@@ -312,7 +312,7 @@ FA_API fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void
  * A key/value cache held in 4 bits an element (as the FP8 quantiser's block scales, "Lecture 8"
  * §8.1, with one step and one middle per 64 channels of a row; the cache and its decode of §8.2).
  *   cache     [B][Hkv][capacity / 64] blocks of 72 d bytes, 16-byte aligned; capacity (slots of a
- *             sequence) a positive multiple of 64; d in {64, 128, 256}. A block holds 64
+ *             sequence) a positive multiple of 64 below 2^31 - 4096; d in {64, 128, 256}. A block holds 64
  *             consecutive slots of one key/value head:
  *               K codes [64][d / 2], V codes [64][d / 2]   channel 2i in bits 0-3 of a byte, 2i + 1
  *                                                          in bits 4-7
