@@ -161,6 +161,15 @@ fa_status check_words(std::initializer_list<const void*> ptrs, const char* what)
   return FA_OK;
 }
 
+struct Bytes {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.n && y < x + a.n;
+}
+
 // Token and head strides of a packed [T][heads][d] tensor: rows may lie apart (a slice of a fused
 // projection) but each starts on 16 bytes.
 fa_status check_strides(std::initializer_list<int64_t> strides, int elem_bytes, const char* what) {
@@ -711,8 +720,19 @@ fa_status fa_kv4_evict(const void* cache, const float* weights, const int32_t* l
   if (empty) return FA_OK;
   if ((st = check_ptrs({cache, out_cache}, "fa_kv4_evict")) != FA_OK) return st;
   if ((st = check_words({weights, lens, out_weights, out_lens, kept}, "fa_kv4_evict")) != FA_OK) return st;
-  if (cache == out_cache || weights == out_weights)
-    return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: the kept rows go into another cache, not into their own");
+  // what is read while other blocks write; out_lens may be lens
+  const size_t heads = (size_t)B * Hkv;
+  const Bytes in[] = {{cache, heads * (capacity / 64) * 72 * d}, {weights, heads * capacity * 4}, {lens, (size_t)B * 4}};
+  const Bytes out[] = {{out_cache, heads * (out_capacity / 64) * 72 * d}, {out_weights, heads * out_capacity * 4},
+                       {kept, heads * keep * 4}, {out_lens, (size_t)B * 4}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Bytes& r : in)
+      if (overlap(out[i], r) && !(i == 3 && out_lens == lens && r.p == lens))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: the kept rows go into another cache, not into their own");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j]))
+        return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: an output lies in another one");
+  }
   if ((double)B * Hkv * ((keep + 63) / 64) > (double)INT32_MAX)
     return fail(FA_ERR_INVALID_ARG, "fa_kv4_evict: too many rows for one call");
   DeviceSyms syms;

@@ -378,8 +378,8 @@ FA_API fa_status fa_decode_kv4(const void* Q, const void* cache, const int32_t* 
  *   keep      1 .. out_capacity; recent 0 .. keep
  *   kept      out: int32 [B][Hkv][keep], the slot that each kept one came from, -1 behind the last
  *   out_lens  out: int32 [B], min(lens[b], keep) (may be lens)
- *   out_cache, out_weights: of out_capacity slots, not the source; slots behind the kept ones are left
- *             as they were.
+ *   out_cache, out_weights: of out_capacity slots; slots behind the kept ones are left as they were.
+ * No output may overlap an input or another output (but for out_lens = lens): FA_ERR_INVALID_ARG.
  * A length outside [0, capacity] is clamped to it and recorded as a device error.
  */
 FA_API fa_status fa_kv4_evict(const void* cache, const float* weights, const int32_t* lens, int keep, int recent,

@@ -48,3 +48,21 @@ def test_capacity_near_the_end_of_32_bits(lib, capacity):
         assert lib.fa_kv4_evict(*P[:3], 64, 3, *P[3:7], 1, 1, *caps, 64, None) == INVALID and "too large" in message(lib)
     # a capacity of 2^31 - 8192 is one
     assert lib.fa_decode_kv4_workspace_size(1, 1, 1, 1, 2 ** 31 - 8192, 64, 1) > 4 * (2 ** 31 - 8192)
+
+
+# cache of 1 x 2 heads of 128 slots: 2 x 2 x 72 x 64 bytes; out_cache of 64 slots: half of that
+@pytest.mark.parametrize("which,at", [
+    ("out_cache", ("cache", 16)), ("out_cache", ("cache", 2 * 2 * 72 * 64 - 16)), ("out_cache", ("cache", -16)),
+    ("out_weights", ("weights", 4)), ("out_weights", ("weights", -4)), ("out_weights", ("cache", 64)),
+    ("kept", ("weights", 0)), ("kept", ("lens", 0)), ("kept", ("out_cache", 2 * 72 * 64 - 4)), ("out_lens", ("kept", 8)),
+    ("out_weights", ("lens", -4)), ("out_lens", ("lens", 4)), ("out_lens", ("cache", 0)), ("kept", ("out_weights", 0))])
+def test_evict_refuses_overlaps(lib, which, at):
+    names = ("cache", "weights", "lens", "out_cache", "out_weights", "out_lens", "kept")
+    ptr = dict(zip(names, P))
+    ptr[which] = ptr[at[0]] + at[1]
+
+    def call(B=2):
+        return lib.fa_kv4_evict(ptr["cache"], ptr["weights"], ptr["lens"], 32, 3, ptr["out_cache"], ptr["out_weights"],
+                                ptr["out_lens"], ptr["kept"], B, 2, 128, 64, 64, None)
+
+    assert call() == INVALID and "another" in message(lib), message(lib)
