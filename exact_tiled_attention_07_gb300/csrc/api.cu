@@ -161,6 +161,17 @@ fa_status check_words(std::initializer_list<const void*> ptrs, const char* what)
   return FA_OK;
 }
 
+// Rows that lie over one another cannot all be written: one dimension's rows have to end before the other's next step.
+fa_status check_output_rows(int tokens, int64_t token_stride, int heads, int64_t head_stride, int d, const char* what) {
+  const int64_t small = std::min(token_stride, head_stride), large = std::max(token_stride, head_stride);
+  const int along = token_stride < head_stride ? tokens : heads;  // rows `small` apart
+  if (small < d) return fail(FA_ERR_INVALID_ARG, "%s: an output stride of %lld elements < d=%d", what, (long long)small, d);
+  if (tokens > 1 && heads > 1 && (double)(along - 1) * (double)small + d > (double)large)
+    return fail(FA_ERR_INVALID_ARG, "%s: output rows overlap (strides of %lld and %lld elements)", what,
+                (long long)token_stride, (long long)head_stride);
+  return FA_OK;
+}
+
 struct Bytes {
   const void* p;
   size_t n;
@@ -603,6 +614,7 @@ fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, fl
     if ((st = check_strides({v}, 2, "fa_fwd_varlen")) != FA_OK) return st;
     if (v < d) return fail(FA_ERR_INVALID_ARG, "fa_fwd_varlen: a stride of %lld elements < d=%d", (long long)v, d);
   }
+  if ((st = check_output_rows(T, o_token_stride, H, o_head_stride, d, "fa_fwd_varlen")) != FA_OK) return st;
   DeviceSyms syms;
   if ((st = device_syms(&syms)) != FA_OK) return st;
   VarlenFwdArgs a{Q, K, V, O, L, cu_seqlens, S, T, H, H / Hkv, d, q_token_stride, q_head_stride, k_token_stride,
@@ -627,9 +639,10 @@ static fa_status kv4_rows(bool read, const void* K, const void* V, const int32_t
   if (weights && (st = check_words({weights}, name)) != FA_OK) return st;
   const int eb = dtype == FA_FP32 ? 4 : 2;
   if ((st = check_strides({k_token_stride, k_head_stride, v_token_stride, v_head_stride}, eb, name)) != FA_OK) return st;
-  if (read)  // rows that lie over one another cannot all be written
-    for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
-      if (s < d) return fail(FA_ERR_INVALID_ARG, "%s: an output stride of %lld elements < d=%d", name, (long long)s, d);
+  if (read) {
+    if ((st = check_output_rows(T, k_token_stride, Hkv, k_head_stride, d, name)) != FA_OK) return st;
+    if ((st = check_output_rows(T, v_token_stride, Hkv, v_head_stride, d, name)) != FA_OK) return st;
+  }
   if (T > INT32_MAX - 64 || (int64_t)Hkv * (d / 8) > 65535 * 32)
     return fail(FA_ERR_INVALID_ARG, "%s: T=%d rows of %d heads are too many for one call", name, T, Hkv);
   DeviceSyms syms;

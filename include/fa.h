@@ -289,7 +289,7 @@ FA_API fa_status fa_fwd_fp8_gqa(const void* Q8, const void* K8, const void* V8, 
  * Forward pass over packed sequences of different lengths (whole prompts; fa_fwd_gqa without padding).
  *   Q, O      [T][H][d], K, V [T][Hkv][d] dtype (bf16 or fp16), the last dimension contiguous, with token and
  *             head strides in elements that are multiples of 16 bytes and at least d: Q, K and V may be
- *             slices of one fused projection
+ *             slices of one fused projection; rows of O must lie apart
  *   L         out: [H][T] fp32, as fa_fwd
  *   cu_seqlens  device int32 [S + 1], non-decreasing, in [0, T]: sequence s is rows [cu_seqlens[s], cu_seqlens[s + 1])
  *             and may be empty. A row sees keys of its own sequence only, with causal != 0 those up to its own
@@ -327,7 +327,7 @@ FA_API fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void
  *             stream. (The lengths are read on the device, so one captured graph serves any lengths.)
  *   rows      K, V of several sequences packed one behind the other, [T][Hkv][d] with the last
  *             dimension contiguous and any token and head strides that are multiples of 16 bytes (at
- *             least d where rows are written);
+ *             least d, and rows apart, where rows are written);
  *             cu_seqlens, device int32 [B + 1], non-decreasing: rows [cu_seqlens[b], cu_seqlens[b + 1]) belong
  *             to sequence b. Rows outside [cu_seqlens[0], cu_seqlens[B]) are neither read nor written.
  * fa_kv4_append writes a sequence's rows into its newest slots: n_b rows go to slots lens[b] - n_b ..

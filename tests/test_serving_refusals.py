@@ -1,7 +1,5 @@
 """Arguments that the serving calls refuse before anything is launched (no GPU: the pointers are not followed)."""
 
-import ctypes
-
 import pytest
 
 INVALID = 1
@@ -9,6 +7,9 @@ INVALID = 1
 
 @pytest.fixture(scope="module")
 def lib():
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("where there is a GPU, a call that is not refused would run on these pointers")
     from exact_tiled_attention_07_gb300 import binding, build
 
     build.build()
@@ -66,3 +67,21 @@ def test_evict_refuses_overlaps(lib, which, at):
                                 ptr["out_lens"], ptr["kept"], B, 2, 128, 64, 64, None)
 
     assert call() == INVALID and "another" in message(lib), message(lib)
+
+
+# (token stride, head stride) of 3 rows of 2 heads, d = 128, where two output rows share elements
+@pytest.mark.parametrize("ts,hs", [(128, 128), (128, 256), (192, 320), (256, 256), (312, 192)])
+def test_output_rows_over_one_another(lib, ts, hs):
+    good = (256, 128)
+    for k, v in (((ts, hs), good), (good, (ts, hs))):
+        assert lib.fa_kv4_read(*P[:5], 1, 3, 2, 128, 128, *k, *v, BF16, None) == INVALID and "output" in message(lib)
+    assert lib.fa_fwd_varlen(*P[:6], 1, 3, 2, 2, 128, *good, *good, *good, ts, hs, 0.1, 1, BF16, None) == INVALID
+    assert "output" in message(lib)
+
+
+# rows that lie apart pass this check (the call then ends at its number of rows)
+@pytest.mark.parametrize("ts,hs", [(256, 128), (1024, 128), (1024, 512), (384, 256)])
+def test_output_rows_apart(lib, ts, hs):
+    T = 2 ** 31 - 1
+    assert lib.fa_kv4_read(*P[:5], 1, T, 2, 128, 128, ts, hs, ts, hs, BF16, None) == INVALID
+    assert "too many" in message(lib)
