@@ -701,6 +701,8 @@ fa_status fa_decode_kv4(const void* Q, const void* cache, const int32_t* lens, v
   if (st != FA_OK) return st;
   if (dtype != FA_BF16 && dtype != FA_FP16)
     return fail(FA_ERR_UNSUPPORTED, "fa_decode_kv4 takes bf16 or fp16 queries, not dtype %d", (int)dtype);
+  if (empty && B > 0 && weights_out && weights_in != weights_out)
+    return fail(FA_ERR_INVALID_ARG, "fa_decode_kv4: weights without query rows");
   if (empty) return FA_OK;
   if ((st = check_ptrs({Q, cache, O, workspace}, "fa_decode_kv4")) != FA_OK) return st;
   if ((st = check_words({lens, L}, "fa_decode_kv4")) != FA_OK) return st;

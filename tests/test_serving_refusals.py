@@ -85,3 +85,13 @@ def test_output_rows_apart(lib, ts, hs):
     T = 2 ** 31 - 1
     assert lib.fa_kv4_read(*P[:5], 1, T, 2, 128, 128, ts, hs, ts, hs, BF16, None) == INVALID
     assert "too many" in message(lib)
+
+
+def test_weights_need_query_rows(lib):
+    # weights_out = weights_in + nothing is a copy that the call does not make; in place there is nothing to do
+    for H, nq in ((0, 1), (4, 0)):
+        decode = lambda w_in, w_out, B=1: lib.fa_decode_kv4(  # noqa: E731
+            *P[:5], w_in, w_out, B, H, 2, nq, 128, 64, 0.1, 0, BF16, P[7], 1 << 30, None)
+        assert decode(P[5], P[6]) == INVALID and "query rows" in message(lib)
+        assert decode(None, P[6]) == INVALID
+        assert decode(P[6], P[6]) == 0 and decode(None, None) == 0 and decode(P[5], P[6], B=0) == 0
