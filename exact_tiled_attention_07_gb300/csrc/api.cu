@@ -710,6 +710,9 @@ fa_status fa_decode_kv4(const void* Q, const void* cache, const int32_t* lens, v
     return fail(FA_ERR_INVALID_ARG, "fa_decode_kv4: weights_in without weights_out");
   if (weights_out && (st = check_words({weights_out}, "fa_decode_kv4")) != FA_OK) return st;
   if (weights_in && (st = check_words({weights_in}, "fa_decode_kv4")) != FA_OK) return st;
+  const size_t nw = (size_t)B * Hkv * capacity * 4;
+  if (weights_in && weights_in != weights_out && overlap({weights_in, nw}, {weights_out, nw}))
+    return fail(FA_ERR_INVALID_ARG, "fa_decode_kv4: weights_in overlaps weights_out without being it");
   if ((st = check_scale(scale)) != FA_OK) return st;
   const size_t need = decode_kv4_workspace_bytes(B, H, Hkv, Nq, capacity, d, weights_out != nullptr);
   if (workspace_bytes < need)

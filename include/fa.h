@@ -355,8 +355,8 @@ FA_API fa_status fa_kv4_read(const void* cache, const int32_t* cu_seqlens, const
  *             recorded as a device error.
  *   weights   weights_out non-NULL: weights_out[b][hkv][j] = weights_in[b][hkv][j] + the sum of the probabilities
  *             that slot j got from the H / Hkv x Nq rows of its key/value head, for j < lens[b]; the other
- *             slots of weights_out are left as they were. weights_in may be NULL (zeros) or weights_out itself.
- *             With H or Nq 0 and B > 0, weights_out must be NULL or weights_in.
+ *             slots of weights_out are left as they were. weights_in may be NULL (zeros) or weights_out itself, and
+ *             overlaps it in no other way. With H or Nq 0 and B > 0, weights_out must be NULL or weights_in.
  *   workspace fa_decode_kv4_workspace_size(...) bytes for the same arguments (weights: whether
  *             weights_out is given); its contents on entry do not matter. Calls that may overlap on the
  *             GPU need workspaces of their own.

@@ -95,3 +95,9 @@ def test_weights_need_query_rows(lib):
         assert decode(P[5], P[6]) == INVALID and "query rows" in message(lib)
         assert decode(None, P[6]) == INVALID
         assert decode(P[6], P[6]) == 0 and decode(None, None) == 0 and decode(P[5], P[6], B=0) == 0
+
+
+def test_weights_partly_over_one_another(lib):
+    for at in (4, -4, 4 * 127):
+        assert lib.fa_decode_kv4(*P[:5], P[6] + at, P[6], 1, 4, 1, 1, 128, 64, 0.1, 0, BF16, P[7], 1 << 30, None) == INVALID
+        assert "weights_in" in message(lib)
