@@ -538,12 +538,17 @@ def fa_decode_kv4_workspace_size(B, H, Hkv, Nq, capacity, d, weights=False) -> i
 def fa_decode_kv4(Q, cache, lens, O, L, scale, causal=False, weights_in=None, weights_out=None, workspace=None,
                   stream=None):
     """Decode: Q, O [B, H, Nq, d] over a 4-bit cache with lens [B] slots in use; L [B, H, Nq].
-    weights_out [B, Hkv, capacity] = weights_in + the attention each slot got (slots in use)."""
+    weights_out [B, Hkv, capacity] = weights_in + the attention each slot got (slots in use). workspace: of
+    fa_decode_kv4_workspace_size bytes; where none is given, one is allocated with torch."""
     shape = _kv4_decode_shape(Q, cache, lens, weights_in, weights_out)
     _ready(O, L, Q, workspace)
     _same(Q, O)
     _rows(L, O.numel() // O.shape[3])
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if workspace is None:
+        workspace = torch.empty(fa_decode_kv4_workspace_size(*shape, weights_out is not None), dtype=torch.uint8,
+                                device=Q.device)
+        _used_on(stream, workspace)
+    nbytes = workspace.numel() * workspace.element_size()
     _check(load_library().fa_decode_kv4(_p(Q), _p(cache), _p(lens), _p(O), _p(L), _p(weights_in), _p(weights_out),
                                         *shape, float(scale), int(bool(causal)), _dt(Q), _p(workspace), nbytes,
                                         _current(stream)))
