@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(kFinishThreads, 3)
           const float L = stat[r0 + r].x;
           if (L == -INFINITY) continue;
 #pragma unroll
-          for (int i = 0; i < WT; ++i) w[i] += ex2(x[r][i] - L);
+          for (int i = 0; i < WT; ++i) w[i] += x[r][i] == -INFINITY ? 0.f : ex2(x[r][i] - L);  // (unseen: not NaN with L)
         }
       }
     }
