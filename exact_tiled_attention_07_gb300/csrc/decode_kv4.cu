@@ -10,13 +10,13 @@
 // value in front of it, in fp32, so keys and values are not rounded.
 //
 // Bound: HBM (9/16 byte a channel of a key or value), then the instructions that turn codes into
-// numbers (283 for 16 tokens of 128 channels in all, half of them on the integer pipe, which has half the rate of
+// numbers (282 for 16 tokens of 128 channels in all, 130 of them on the integer pipe, which has half the rate of
 // the others).  So codes go from shared memory straight into the registers of mma.sync (m16n8k16,
 // fp16, fp32 sums) operands.  Masked out of its word, a nibble is an fp16 subnormal, c 2^-24 where it stands
 // lowest and c 2^-20 next to that: 4 masks and a shift for 8 codes, nothing to convert; what the codes are
 // multiplied with and the sums carry the powers of two, and the offset of 8 is taken off in fp32.
-// Measured, 32 x 8 heads of 32,768 slots, d = 128, four rows a head (1.21 GB): 211 us, 5.7 TB/s, 0.84 of the
-// measured copy rate; with the arithmetic left out 194.  Other forms of it:
+// Measured, 32 x 8 heads of 32,768 slots, d = 128, four rows a head (1.21 GB): 206 us, 5.9 TB/s, 0.86 of the
+// measured copy rate; with the arithmetic left out 194.  Other forms of it (beside 211):
 //   * codes to fp16 numbers by or-ing them into 1024 and taking that and 8 off (9 instructions for 8 codes): 236 us,
 //     313 with the or's constant as an immediate (each mask-and-or two instructions);
 //   * one CTA of 8, 12 or 16 warps an SM instead of four of 4, in that form: 248 to 256 us;
@@ -28,7 +28,8 @@
 //
 //   S^T = K Q^T: K is the A operand (16 tokens x 16 channels).  Channels may come in any order in a
 //     dot product, so Q is laid out to match; it is scaled by a power of two that puts the row's
-//     largest element in [2^14, 2^15), so a bf16 q is exact in fp16 down to 2^-29 of that.
+//     largest element in [2^14, 2^15), so a bf16 q is exact in fp16 down to 2^-31 of that (of an odd channel,
+//     which is multiplied by 2^-4 as odd codes count 16 times, down to 2^-27).
 //   O^T = V^T P^T: V^T is the A operand (16 channels x 16 tokens): a register holds one channel of two
 //     tokens, so the words of two tokens are interleaved by halves first.  P step_V is rounded to
 //     fp16 (2^-11), and what the offset of 8 takes off is counted with the rounded one, so the error is that of
@@ -38,15 +39,16 @@
 //     at the end: sums of codes 0 to 15 grow to hundreds of times what is left of them, and mma.sync truncates its
 //     fp32 sums at every step.  Relative to O's rms over 65,536 slots at 400 blocks a CTA (d = 64, fp16 queries) the
 //     error is 2.2e-4, of which 2e-4 are O's own rounding; 4.8e-3 with the offset taken off at the end.
-//     1.4 % of the time of the 1.21 GB case; 256 tokens measure the same within 1 us and err by twice as much.
+//     1.4 % of the time of the 1.21 GB case, every 256 tokens the same within 2 us.
 //     Range: P = 2^(S - m + 8) with a reference m of each row that keeps the products P step_V, which are rounded,
 //     inside fp16's range, and not P alone: m is raised where a product might pass 2^15.5 and does pass 2^9, so that the
 //     step's largest comes to 2^8.  Whether one might is seen from the largest score and the block's largest step.  So
 //     each product keeps fp16's precision down to 2^-22 of the row's largest product (what is smaller, and the rounding
 //     error of fp16 queries, an absolute 2^-33 of it), whatever steps other rows' slots or slots of no weight
 //     have.  With m the largest score and the steps' largest exponent: 1 to 2.5 % off where a slot of step 4,096 and
-//     no weight stands among every 32 of step 0.002; a scale of each row's 64 channels on top of m: 4 to 8 % more time at
-//     d = 128 and 256.
+//     no weight stands among every 32 of step 0.002; a scale of each row's 64 channels on top of m: 5 to 8 % more time at
+//     d = 128 and 256.  A block whose largest step does not allow for P is looked over
+//     step by step: where every 32nd slot is of that kind, 244 us instead of 212 for the 1.21 GB case.
 //
 // Work split: the 64-slot blocks of all (sequence, key/value head, group of 8 NT query rows) form one list;
 // each CTA takes an equal run of it, whatever the lengths of the sequences, found on the device
@@ -164,7 +166,9 @@ __device__ __forceinline__ int blocks_of(int n) { return (n + kKv4Block - 1) / k
 
 // The list: sequences, then their heads x row groups (segments), then the segment's nb blocks, each a
 // position, behind kSegCost positions that stand for what a segment costs whatever its length (its queries, joining
-// the warps, its output: about the time of that many blocks).
+// the warps, its output: about the time of that many blocks).  With 2, 4, 6, 9 and 12 in turn: 8 sequences of 1 to 32,768
+// slots, d = 64: 40, 34, 30, 30, 30 us; d = 128: 50, 40, 40, 40, 40; d = 256: 79, 69, 60, 58, 58; 64 of 300 and 64 of 3,000,
+// d = 128: 79, 69, 71, 71, 71.
 constexpr int kSegCost = 6;
 
 struct Cursor {

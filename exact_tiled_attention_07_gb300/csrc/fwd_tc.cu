@@ -164,9 +164,12 @@ struct F8Scales {
 // Key and query tiles start at the sequence's own first row, so only its last tile is ragged: scores of
 // keys behind the end are masked as in the plain kernel, the V rows there (another sequence's) are
 // set to zero in shared memory before P V, since 0 x NaN is NaN, and O rows are stored one by one.
-// Bound: tensor and softmax, as the plain kernel.  Measured (32 heads on 8, d = 128, causal): 1,536 TFLOP/s on
-// sequences of 16,384 and 5,001 tokens (the plain kernel 1,532 on 8 x 4,096); 1,198 on sixteen of 1 to 4,096,
-// whose ragged tiles cost a tenth more work and whose 2,400 items cost about 2.6 us each beside it.
+// Bound: tensor and softmax, as the plain kernel.  Measured (32 heads on 8, d = 128, causal): 1,526 to 1,558 TFLOP/s,
+// run by run, on sequences of 16,384 and 5,001 tokens (the plain kernel 1,532 on 8 x 4,096); 1,195 to 1,220 on sixteen of
+// 1 to 4,096, whose ragged tiles cost a tenth more work and whose 2,400 items cost about 2.6 us each beside it: a chain of
+// ticket, search, Q and K, S, softmax and P V, one behind the other where an item has one or two key tiles.
+// A captured launch has no ticket counter (its replays could overlap) and takes the slots, empty ones too, round by
+// round: 292 us instead of 267 on the sixteen, 1,537 instead of 1,449 on the two.
 struct VarlenSpec {
   const int32_t* cu = nullptr;  // [seqs + 1]
   int seqs = 0;

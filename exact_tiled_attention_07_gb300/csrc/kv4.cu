@@ -7,7 +7,8 @@
 //   step   = fp16((hi - lo) / 15), rounded up, so that 15 steps cover [lo, hi]
 //   middle = fp16(lo + 8 step), rounded to nearest
 //   code   = clamp(rint((x - middle) / step), -8, 7) + 8     (8 when step is 0)
-// so |middle + step (code - 8) - x| <= max(step / 2, 2^-11 |middle|) up to fp32 rounding.  The
+// so |middle + step (code - 8) - x| <= max(step / 2, 2^-11 |middle| + 2^-25) up to fp32 rounding
+// (2^-25: half of fp16's smallest number, which middles below 2^-14 are rounded by).  The
 // quotient and the two sums are IEEE operations: the codes are the same wherever they are taken.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -163,7 +164,7 @@ constexpr int kRowWarps = 8;  // rows of a block: one warp each
 // division is done for it.  Rounding to an integer is an addition of 1.5 2^23 and its subtraction,
 // and four codes are put together by multiply-adds.
 // Bound: instructions (160 for 32 words; HBM wants 26 us for 34,001 rows of 8 heads of 128 bf16
-// channels, 139 MB in and 39 MB out).  Measured there: 51 us (3.5 TB/s); 109 with conversions to int (16 a clock
+// channels, 139 MB in and 39 MB out).  Measured there: 52 us (3.4 TB/s); 109 with conversions to int (16 a clock
 // on an SM) and a division each, 58 with shifts and masks for the packing.  One chunk a warp instead of two 96
 // against 85 us with the read behind it, four 87.
 template <typename T, int D, int CH>

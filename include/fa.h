@@ -299,8 +299,9 @@ FA_API fa_status fa_fwd_fp8_gqa(const void* Q8, const void* K8, const void* V8, 
  * What the rows of one sequence hold (NaN, infinity) does not reach another one. (Within a causal sequence, as in
  * fa_fwd, a row's weights for later rows are exact zeros, so a V row that is not finite reaches the rows in front of it
  * whose 128-row tile of queries meets its 128-row tile of keys.) The lengths are read on
- * the device: one captured graph serves any lengths with the same T and S. Launches one kernel; results are
- * the same bits for the same arguments.
+ * the device: one captured graph serves any lengths with the same T and S. (Captured, the work is dealt out round by round
+ * instead of by a queue: the same bits, 6 to 9 % more time.) Launches one kernel; results are the same bits for the same
+ * arguments.
  */
 FA_API fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* L,
                                const int32_t* cu_seqlens, int S, int T, int H, int Hkv, int d, int64_t q_token_stride,
@@ -320,7 +321,7 @@ FA_API fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void
  *             and a code c stands for middle + step (c - 8). For a group x of 64 channels, in fp32
  *             rounded to nearest: step = fp16((max x - min x) / 15) rounded up, middle =
  *             fp16(min x + 8 step), c = clamp(rint((x - middle) / step), -8, 7) + 8 (8 when step is
- *             0), so a value is off by at most max(step / 2, 2^-11 |middle|) and fp32 roundings. A
+ *             0), so a value is off by at most max(step / 2, 2^-11 |middle| + 2^-25) and fp32 roundings. A
  *             group with a NaN or a magnitude above 32768 is held as NaN.
  *   lens      device int32 [B]: slots in use, slots [0, lens[b]) of sequence b. The cache itself keeps
  *             no length: the caller owns lens, counts it up and may change it between calls on the
@@ -351,8 +352,8 @@ FA_API fa_status fa_kv4_read(const void* cache, const int32_t* cu_seqlens, const
  *   Q, O      [B][H][Nq][d] dtype (bf16 or fp16), the new query rows; L [B][H][Nq] fp32
  *   lens      as above; a row sees slots [0, lens[b]), or with causal != 0 row i of the Nq sees slots
  *             [0, lens[b] - Nq + i + 1): the Nq rows are then the newest slots' own. A row that sees
- *             nothing gets O = 0, L = -inf; a NaN in a slot does not reach the rows that do not see it. A length outside [0, capacity] is clamped to it and
- *             recorded as a device error.
+ *             nothing gets O = 0, L = -inf; a NaN in a slot does not reach the rows that do not see it. A length
+ *             outside [0, capacity] is clamped to it and recorded as a device error.
  *   weights   weights_out non-NULL: weights_out[b][hkv][j] = weights_in[b][hkv][j] + the sum of the probabilities
  *             that slot j got from the H / Hkv x Nq rows of its key/value head, for j < lens[b]; the other
  *             slots of weights_out are left as they were. weights_in may be NULL (zeros) or weights_out itself, and
@@ -363,7 +364,8 @@ FA_API fa_status fa_kv4_read(const void* cache, const int32_t* cu_seqlens, const
  * Keys, values and scores are never rounded to 16 bits; probabilities times the values' steps enter the second product
  * rounded to fp16: for bf16 queries by 2^-11 of each, for fp16 queries, whose rounding errors are a second operand, by
  * 2^-22, and in either case by no less than 2^-33 of the row's largest such product (2^-29 where all of its steps are
- * below 2^-20). The work is cut into equal runs of blocks on the device, whatever the lengths. Results do not depend on timing: two calls with the same arguments give the same bits.
+ * below 2^-20). The work is cut into equal runs of blocks on the device, whatever the lengths. Results do not depend on
+ * timing: two calls with the same arguments give the same bits.
  */
 FA_API size_t fa_decode_kv4_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d, int weights);
 FA_API fa_status fa_decode_kv4(const void* Q, const void* cache, const int32_t* lens, void* O, float* L,

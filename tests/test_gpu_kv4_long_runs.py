@@ -49,7 +49,7 @@ def test_decode_error_relative_to_what_is_left(fa, B, H, hkv, cap, d, dtype):  #
     fa.fa_check_device_error()
     off = total = bias = 0.0
     n, mag = 0, 0.0
-    for b, h in ((0, 0), (B // 2, hkv // 2), (B - 1, hkv - 1)):
+    for b, h in ((0, 0), (1, hkv - 1), (B // 2, hkv // 2), (B - 1, hkv - 1)):
         k, v = values(cache[b, h], 0), values(cache[b, h], 1)
         x = q[b, h * rows:(h + 1) * rows, 0].double()
         s = x @ k.T * scale
