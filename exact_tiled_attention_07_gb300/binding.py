@@ -27,6 +27,8 @@ __all__ = [
     "attention_forward_fp8", "quantize_fp8", "EXPORTED_SYMBOLS", "NOALLOC_SCRATCH_BYTES",
     "fa_sm_clock_sample", "kv4_cache", "fa_kv4_append", "fa_kv4_read", "kv4_read", "fa_decode_kv4",
     "fa_decode_kv4_workspace_size", "attention_decode_kv4", "fa_kv4_evict", "fa_fwd_varlen", "attention_forward_varlen",
+    "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "rope_table", "qk_norm_rope",
+    "qk_norm_rope_backward",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,7 +44,8 @@ EXPORTED_SYMBOLS = (
     "fa_quantize_fp8", "fa_fwd_fp8", "fa_fwd_fp8_gqa", "fa_fwd_masked", "fa_bwd_masked",
     "fa_selftest_bounded_wait", "fa_fwd_bwd_host", "fa_fwd_bwd_host_workspace_size", "fa_sm_clock_sample",
     "fa_debug_build", "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4",
-    "fa_decode_kv4_workspace_size", "fa_kv4_evict", "fa_fwd_varlen",
+    "fa_decode_kv4_workspace_size", "fa_kv4_evict", "fa_fwd_varlen", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+    "fa_qk_norm_rope_bwd_workspace_size",
 )
 
 _lib = None
@@ -106,6 +109,10 @@ def load_library(path=None):
         lib.fa_decode_kv4_workspace_size.restype = sz
         lib.fa_decode_kv4.argtypes = [vp] * 7 + [i] * 6 + [f, i, i, vp, sz, vp]
         lib.fa_kv4_evict.argtypes = [vp] * 3 + [i, i] + [vp] * 4 + [i] * 5 + [vp]
+        lib.fa_qk_norm_rope.argtypes = [vp] * 9 + [i] * 8 + [f, i, i, vp]
+        lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+        lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+        lib.fa_qk_norm_rope_bwd.argtypes = [vp] * 13 + [sz, vp] + [i] * 8 + [f, i, i, vp]
         lib.fa_check_device_error.argtypes = [vp]
         lib.fa_sm_clock_sample.argtypes = [vp, i, vp]
         lib.fa_debug_build.argtypes = []
@@ -124,7 +131,7 @@ def load_library(path=None):
                      "fa_bwd_main", "fa_bwd_dq_convert",
                      "fa_check_device_error", "fa_tile_counter", "fa_uses_tensor_cores", "fa_sm_clock_sample",
                      "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_kv4_evict",
-                     "fa_fwd_varlen"):
+                     "fa_fwd_varlen", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -589,6 +596,83 @@ def fa_kv4_evict(cache, weights, lens, keep, recent, out_cache, out_weights, out
                                        _current(stream)))
 
 
+def _token_rows(t, heads, ref, what):
+    """(batch, token, head stride) of a [B, N, heads, d] tensor, or of a packed [T, heads, d] one (one batch)
+    of ref's tokens, head dimension and dtype."""
+    if t.dim() != ref.dim() or t.shape[:-2] != ref.shape[:-2] or t.shape[-1] != ref.shape[-1] or t.dtype != ref.dtype:
+        raise ValueError(f"{what} must have Q's batch, tokens, head dimension and dtype")
+    if heads is not None and t.shape[-2] != heads:
+        raise ValueError(f"{what} must have {heads} heads")
+    st, d = t.stride(), t.shape[-1]
+    if d > 1 and st[-1] != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if t.dim() == 3:
+        return 0, (st[0] if t.shape[0] > 1 else 0), (st[1] if t.shape[1] > 1 else 0)
+    return (st[0] if t.shape[0] > 1 else 0), (st[1] if t.shape[1] > 1 else 0), (st[2] if t.shape[2] > 1 else 0)
+
+
+def _norm_rope_args(rows, wq, wk, table, positions, eps, interleaved, extra=()):
+    """What fa_qk_norm_rope and its backward are called with behind their pointers; rows: the queries' and the
+    keys' tensors by turns, as their strides are passed."""
+    q, k = rows[0], rows[1]
+    if q.dim() not in (3, 4):
+        raise ValueError(f"expected [B, N, H, d] or packed [T, H, d] queries, got shape {tuple(q.shape)}")
+    strides = []
+    for n, t in enumerate(rows):
+        strides += _token_rows(t, (k if n & 1 else q).shape[-2], q, "keys" if n & 1 else "queries")
+    _ready(wq, wk, table, positions, *extra, strided=rows)
+    B, N = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
+    d = q.shape[-1]
+    wdt = q.dtype
+    for w in (wq, wk):
+        if w is not None:
+            wdt = w.dtype
+            if w.numel() != d or w.dtype != (wq if wq is not None else wk).dtype:
+                raise ValueError("weights must be [d] tensors of one dtype, fp32 or the rows'")
+    if table is None:
+        rotary, length = 0, 0
+    else:
+        if table.dtype != torch.float32 or table.dim() != 2:
+            raise ValueError("the rotation table must be an fp32 tensor [positions, rotary] (rope_table)")
+        length, rotary = table.shape
+    if positions is not None:
+        _int32(positions, B * N, "positions")
+    return ((ctypes.c_int64 * len(strides))(*strides), B, N, q.shape[-2], k.shape[-2], d, rotary, bool(interleaved), length,
+            float(eps), _dt(q), DTYPE_CODES[wdt] if wdt in DTYPE_CODES else _dt(wq))
+
+
+def fa_qk_norm_rope(Q, K, wq, wk, table, Qo, Ko, positions=None, eps=1e-6, interleaved=False, stream=None):
+    """Qo, Ko = the heads of Q [B, N, H, d] and K [B, N, Hkv, d] (or packed [T, heads, d]; any strides between rows)
+    normed with the weights wq, wk [d] (None: ones) and rotated by position with table [positions, rotary] (None: not
+    rotated). positions: int32, one a token; None: 0 .. N - 1."""
+    args = _norm_rope_args((Q, K, Qo, Ko), wq, wk, table, positions, eps, interleaved)
+    _check(load_library().fa_qk_norm_rope(_p(Q), _p(K), _p(wq), _p(wk), _p(table), _p(positions), _p(Qo), _p(Ko), *args,
+                                          _current(stream)))
+
+
+def fa_qk_norm_rope_bwd_workspace_size(d) -> int:
+    return int(load_library().fa_qk_norm_rope_bwd_workspace_size(int(d)))
+
+
+def fa_qk_norm_rope_bwd(dQo, dKo, Q, K, wq, wk, table, dQ, dK, dwq, dwk, positions=None, eps=1e-6, interleaved=False,
+                        workspace=None, stream=None):
+    """Gradients of fa_qk_norm_rope: dQ, dK (as Q, K) and dwq, dwk ([d] of the weights' dtype, or None) from dQo, dKo."""
+    for w, dw in ((wq, dwq), (wk, dwk)):
+        if dw is not None and (dw.numel() != Q.shape[-1] or (w is not None and dw.dtype != w.dtype)):
+            raise ValueError("weight gradients must be [d] tensors of their weights' dtype")
+    if wq is None and wk is None and (dwq is not None or dwk is not None):
+        raise ValueError("a weight gradient without weights")
+    args = _norm_rope_args((dQo, dKo, Q, K, dQ, dK), wq, wk, table, positions, eps, interleaved,
+                           (dwq, dwk, workspace))
+    lib = load_library()
+    if workspace is None:
+        workspace = torch.empty(lib.fa_qk_norm_rope_bwd_workspace_size(Q.shape[-1]), dtype=torch.uint8, device=Q.device)
+        _used_on(stream, workspace)
+    _check(lib.fa_qk_norm_rope_bwd(_p(dQo), _p(dKo), _p(Q), _p(K), _p(wq), _p(wk), _p(table), _p(positions), _p(dQ), _p(dK),
+                                   _p(dwq), _p(dwk), _p(workspace), workspace.numel() * workspace.element_size(), *args,
+                                   _current(stream)))
+
+
 def fa_selftest_bounded_wait(timeout_ms=20, arrive=False, stream=None):
     """Launch the bounded-wait self-test (see include/fa.h); read the outcome with fa_check_device_error."""
     _check(load_library().fa_selftest_bounded_wait(int(timeout_ms), int(bool(arrive)), _stream(stream)))
@@ -719,6 +803,47 @@ def _used_on(stream, *ts):
     for t in ts:
         if t is not None:
             t.record_stream(stream)
+
+
+def rope_table(positions, rotary, base=10000.0, device="cuda"):
+    """The fp32 rotation table [positions, rotary] of qk_norm_rope: cos of the angles p base^(-2 i / rotary), i < rotary / 2,
+    then their sin; angles in 64 bits (in 32, far positions' angles are off by more than the table's rounding)."""
+    freq = float(base) ** (-torch.arange(0, rotary, 2, dtype=torch.float64, device=device) / max(int(rotary), 1))
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat((angle.cos(), angle.sin()), -1).float()
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, table, positions=None, eps=1e-6, interleaved=False, stream=None):
+    """fa_qk_norm_rope into new tensors: from q [B, N, H, d], k [B, N, Hkv, d] (slices of a fused projection's output, say)
+    [B, H, N, d] and [B, Hkv, N, d], what attention_forward takes; from packed [T, heads, d] the same, packed, what
+    attention_forward_varlen takes."""
+    if q.dim() == 4 and k.dim() == 4:
+        (B, N, H, d), Hkv = q.shape, k.shape[2]
+        qo = torch.empty((B, H, N, d), dtype=q.dtype, device=q.device)
+        ko = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=q.device)
+        fa_qk_norm_rope(q, k, q_weight, k_weight, table, qo.transpose(1, 2), ko.transpose(1, 2), positions, eps, interleaved,
+                        stream)
+    else:
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ko = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        fa_qk_norm_rope(q, k, q_weight, k_weight, table, qo, ko, positions, eps, interleaved, stream)
+    _used_on(stream, qo, ko)
+    return qo, ko
+
+
+def qk_norm_rope_backward(dqo, dko, q, k, q_weight, k_weight, table, positions=None, eps=1e-6, interleaved=False,
+                          stream=None, out=None):
+    """dq, dk, dq_weight, dk_weight = the gradients of qk_norm_rope from those of its results (dqo, dko as it returns them). dq
+    and dk have q's and k's shapes; out: tensors (slices of a fused gradient, say) that take them. A weight's gradient
+    has its dtype and is None where there is no weight."""
+    dq, dk = out if out is not None else (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
+    if dqo.dim() == 4 and dko.dim() == 4:
+        dqo, dko = dqo.transpose(1, 2), dko.transpose(1, 2)
+    fa_qk_norm_rope_bwd(dqo, dko, q, k, q_weight, k_weight, table, dq, dk, dwq, dwk, positions, eps, interleaved, None,
+                        stream)
+    _used_on(stream, dwq, dwk, *(() if out is not None else (dq, dk)))
+    return dq, dk, dwq, dwk
 
 
 def kv4_read(cache, cu_seqlens, lens, total, dtype=torch.bfloat16, stream=None):

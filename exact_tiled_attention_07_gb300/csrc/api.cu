@@ -191,6 +191,62 @@ fa_status check_strides(std::initializer_list<int64_t> strides, int elem_bytes, 
   return FA_OK;
 }
 
+// A [B][N][heads][d] tensor of rows: where it lies and its strides in elements.
+struct RowTensor {
+  const char* name;
+  const void* p;
+  NormRopeStrides st;
+  int heads;
+};
+
+// Rows of an output lie apart: from the smallest stride up, a dimension's rows end before the next one's first step.
+fa_status check_rows_apart(const RowTensor& t, int B, int N, int d, const char* what) {
+  struct Dim {
+    int64_t stride;
+    int n;
+  } dims[3] = {{t.st.batch, B}, {t.st.token, N}, {t.st.head, t.heads}};
+  std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  double extent = d;
+  for (const Dim& x : dims) {
+    if (x.n <= 1) continue;
+    if ((double)x.stride < extent)
+      return fail(FA_ERR_INVALID_ARG, "%s: rows of %s overlap (a stride of %lld elements)", what, t.name, (long long)x.stride);
+    extent += (double)(x.n - 1) * (double)x.stride;
+  }
+  return FA_OK;
+}
+
+// An output and another tensor (of one element size) that do not meet: apart in memory, or side by side inside a token.
+bool rows_meet(const RowTensor& a, const RowTensor& b, int B, int N, int d, int eb) {
+  auto bytes = [&](const RowTensor& t) {
+    return (size_t)((B - 1) * t.st.batch + (N - 1) * t.st.token + (t.heads - 1) * t.st.head + d) * eb;
+  };
+  if (!overlap({a.p, bytes(a)}, {b.p, bytes(b)})) return false;
+  if ((B > 1 && a.st.batch != b.st.batch) || (N > 1 && a.st.token != b.st.token)) return true;
+  const bool a_first = reinterpret_cast<uintptr_t>(a.p) <= reinterpret_cast<uintptr_t>(b.p);
+  const RowTensor &lo = a_first ? a : b, &hi = a_first ? b : a;
+  const int64_t off = (int64_t)((reinterpret_cast<uintptr_t>(hi.p) - reinterpret_cast<uintptr_t>(lo.p)) / eb);
+  const int64_t lo_end = (lo.heads - 1) * lo.st.head + d, hi_end = off + (hi.heads - 1) * hi.st.head + d;
+  if (off < lo_end) return true;
+  // the smaller step of the token and the batch dimension repeats the pattern; the larger one has to leave room for it
+  int64_t small = INT64_MAX, large = INT64_MAX;
+  int n_small = 1;
+  if (N > 1) small = a.st.token, n_small = N;
+  if (B > 1 && a.st.batch < small) {
+    large = small;
+    small = a.st.batch;
+    n_small = B;
+  } else if (B > 1) {
+    large = a.st.batch;
+  }
+  if (small != INT64_MAX && hi_end > small) return true;
+  return large != INT64_MAX && (double)(n_small - 1) * (double)small + hi_end > (double)large;
+}
+bool same_rows(const RowTensor& a, const RowTensor& b, int B, int N) {
+  return a.p == b.p && a.heads == b.heads && (B <= 1 || a.st.batch == b.st.batch) && (N <= 1 || a.st.token == b.st.token) &&
+         (a.heads <= 1 || a.st.head == b.st.head);
+}
+
 }  // namespace
 
 unsigned long long current_context_id() {
@@ -759,6 +815,125 @@ fa_status fa_kv4_evict(const void* cache, const float* weights, const int32_t* l
                  out_lens, kept, B, Hkv, capacity, out_capacity, d, keep, recent, syms.err,
                  static_cast<cudaStream_t>(stream)};
   return launched(launch_kv4_evict(a), "fa_kv4_evict");
+}
+
+// The checks of fa_qk_norm_rope and fa_qk_norm_rope_bwd. `in` and `out` hold the queries' and the keys' tensors by turns.
+static fa_status norm_rope_impl(NormRopeArgs* a, std::initializer_list<RowTensor> in, std::initializer_list<RowTensor> out,
+                                const char* name) {
+  if (a->dtype != FA_BF16 && a->dtype != FA_FP16 && a->dtype != FA_FP32)
+    return fail(FA_ERR_UNSUPPORTED, "unknown dtype %d", a->dtype);
+  if (a->wdtype != FA_FP32 && a->wdtype != a->dtype)
+    return fail(FA_ERR_UNSUPPORTED, "%s: weights are fp32 or of the rows' dtype", name);
+  if (a->b < 0 || a->n < 0 || a->h < 0 || a->hkv < 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: negative size B=%d N=%d H=%d Hkv=%d", name, a->b, a->n, a->h, a->hkv);
+  if (a->d < 8 || a->d > 256 || a->d % 8 != 0)
+    return fail(FA_ERR_UNSUPPORTED, "%s: d=%d is not a multiple of 8 in [8, 256]", name, a->d);
+  if (a->rotary < 0 || a->rotary > a->d || a->rotary % 8 != 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: rotary=%d is not a multiple of 8 in [0, d=%d]", name, a->rotary, a->d);
+  if (!std::isfinite(a->eps) || a->eps < 0.f) return fail(FA_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", name);
+  // units of work are counted in 32 bits, up to a grid's share behind the last
+  if ((double)a->b * a->n * ((double)a->h + a->hkv) > 1.0e9)
+    return fail(FA_ERR_INVALID_ARG, "%s: B=%d N=%d H=%d Hkv=%d: too many rows for one call", name, a->b, a->n, a->h, a->hkv);
+  const bool rows = (int64_t)a->b * a->n > 0;
+  const int eb = a->dtype == FA_FP32 ? 4 : 2;
+  fa_status st;
+  if (rows && a->h + a->hkv > 0) {
+    for (const auto* list : {&in, &out})
+      for (const RowTensor& t : *list) {
+        if (t.heads == 0) continue;
+        if ((st = check_ptrs({t.p}, name)) != FA_OK) return st;
+        if ((st = check_strides({t.st.batch, t.st.token, t.st.head}, eb, name)) != FA_OK) return st;
+        if ((double)(a->b - 1) * t.st.batch + (double)(a->n - 1) * t.st.token + (double)(t.heads - 1) * t.st.head > 1.0e18)
+          return fail(FA_ERR_INVALID_ARG, "%s: %s reaches too far", name, t.name);
+      }
+    for (auto o = out.begin(); o != out.end(); ++o) {
+      if (o->heads == 0) continue;
+      if ((st = check_rows_apart(*o, a->b, a->n, a->d, name)) != FA_OK) return st;
+      const int kind = (int)(o - out.begin()) & 1;
+      for (auto i = in.begin(); i != in.end(); ++i)
+        if (i->heads && !(((int)(i - in.begin()) & 1) == kind && same_rows(*o, *i, a->b, a->n)) &&
+            rows_meet(*o, *i, a->b, a->n, a->d, eb))
+          return fail(FA_ERR_INVALID_ARG, "%s: %s overlaps %s", name, o->name, i->name);
+      for (auto o2 = out.begin(); o2 != o; ++o2)
+        if (o2->heads && rows_meet(*o, *o2, a->b, a->n, a->d, eb))
+          return fail(FA_ERR_INVALID_ARG, "%s: %s overlaps %s", name, o->name, o2->name);
+    }
+    if (a->rotary > 0) {
+      if ((st = check_ptrs({a->table}, name)) != FA_OK) return st;
+      if (a->table_len < 1) return fail(FA_ERR_INVALID_ARG, "%s: an empty table", name);
+      if (a->positions) {
+        if ((st = check_words({a->positions}, name)) != FA_OK) return st;
+      } else if (a->n > a->table_len) {
+        return fail(FA_ERR_INVALID_ARG, "%s: N=%d positions but table_len=%d", name, a->n, a->table_len);
+      }
+    }
+  }
+  const uintptr_t weight_align = a->wdtype == FA_FP32 ? 3u : 1u;
+  for (const void* w : {a->wq, a->wk, (const void*)a->dwq, (const void*)a->dwk})
+    if ((reinterpret_cast<uintptr_t>(w) & weight_align) != 0)
+      return fail(FA_ERR_INVALID_ARG, "%s: a weight is not aligned to its elements", name);
+  return FA_OK;
+}
+
+static NormRopeStrides strides_at(const int64_t* s, int i) { return {s[3 * i], s[3 * i + 1], s[3 * i + 2]}; }
+
+fa_status fa_qk_norm_rope(const void* Q, const void* K, const void* wq, const void* wk, const float* table,
+                          const int32_t* positions, void* Qo, void* Ko, const int64_t* strides, int B, int N, int H, int Hkv,
+                          int d, int rotary, int adjacent, int table_len, float eps, fa_dtype dtype, fa_dtype weight_dtype,
+                          void* stream) {
+  if (!strides) return fail(FA_ERR_INVALID_ARG, "fa_qk_norm_rope: strides is null");
+  NormRopeArgs a{};
+  a.q = Q, a.k = K, a.wq = wq, a.wk = wk, a.table = table, a.positions = positions, a.qo = Qo, a.ko = Ko;
+  a.q_st = strides_at(strides, 0), a.k_st = strides_at(strides, 1);
+  a.qo_st = strides_at(strides, 2), a.ko_st = strides_at(strides, 3);
+  a.b = B, a.n = N, a.h = H, a.hkv = Hkv, a.d = d, a.rotary = rotary, a.adjacent = adjacent ? 1 : 0;
+  a.table_len = table_len, a.eps = eps, a.dtype = (int)dtype, a.wdtype = (int)weight_dtype;
+  a.stream = static_cast<cudaStream_t>(stream);
+  fa_status st = norm_rope_impl(&a, {{"Q", Q, a.q_st, H}, {"K", K, a.k_st, Hkv}},
+                                {{"Qo", Qo, a.qo_st, H}, {"Ko", Ko, a.ko_st, Hkv}}, "fa_qk_norm_rope");
+  if (st != FA_OK || (int64_t)B * N == 0 || H + Hkv == 0) return st;
+  DeviceSyms syms;
+  if ((st = device_syms(&syms)) != FA_OK) return st;
+  a.err = syms.err;
+  return launched(launch_norm_rope(a), "fa_qk_norm_rope");
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
+  // a row of sums for each block, for as many as the largest GPU of this kind takes
+  return d < 8 || d > 256 || d % 8 != 0 ? 0 : (size_t)norm_rope_bwd_blocks() * d * 4;
+}
+
+fa_status fa_qk_norm_rope_bwd(const void* dQo, const void* dKo, const void* Q, const void* K, const void* wq,
+                              const void* wk, const float* table, const int32_t* positions, void* dQ, void* dK, void* dwq,
+                              void* dwk, void* workspace, size_t workspace_bytes, const int64_t* strides, int B, int N,
+                              int H, int Hkv, int d, int rotary, int adjacent, int table_len, float eps, fa_dtype dtype,
+                              fa_dtype weight_dtype, void* stream) {
+  if (!strides) return fail(FA_ERR_INVALID_ARG, "fa_qk_norm_rope_bwd: strides is null");
+  NormRopeArgs a{};
+  a.q = Q, a.k = K, a.wq = wq, a.wk = wk, a.table = table, a.positions = positions, a.qo = dQo, a.ko = dKo;
+  a.dq = dQ, a.dk = dK, a.dwq = dwq, a.dwk = dwk;
+  a.qo_st = strides_at(strides, 0), a.ko_st = strides_at(strides, 1);
+  a.q_st = strides_at(strides, 2), a.k_st = strides_at(strides, 3);
+  a.dq_st = strides_at(strides, 4), a.dk_st = strides_at(strides, 5);
+  a.b = B, a.n = N, a.h = H, a.hkv = Hkv, a.d = d, a.rotary = rotary, a.adjacent = adjacent ? 1 : 0;
+  a.table_len = table_len, a.eps = eps, a.dtype = (int)dtype, a.wdtype = (int)weight_dtype, a.backward = 1;
+  a.stream = static_cast<cudaStream_t>(stream);
+  fa_status st = norm_rope_impl(
+      &a, {{"dQo", dQo, a.qo_st, H}, {"dKo", dKo, a.ko_st, Hkv}, {"Q", Q, a.q_st, H}, {"K", K, a.k_st, Hkv}},
+      {{"dQ", dQ, a.dq_st, H}, {"dK", dK, a.dk_st, Hkv}}, "fa_qk_norm_rope_bwd");
+  if (st != FA_OK) return st;
+  const bool rows = (int64_t)B * N > 0 && H + Hkv > 0;
+  if (!rows && !dwq && !dwk) return FA_OK;
+  if (dwq && dwq == dwk) return fail(FA_ERR_INVALID_ARG, "fa_qk_norm_rope_bwd: dwq is dwk");
+  if ((st = check_ptrs({workspace}, "fa_qk_norm_rope_bwd")) != FA_OK) return st;
+  DeviceSyms syms;
+  if ((st = device_syms(&syms)) != FA_OK) return st;
+  a.err = syms.err;
+  const size_t need = fa_qk_norm_rope_bwd_workspace_size(d);
+  if (workspace_bytes < need)
+    return fail(FA_ERR_INVALID_ARG, "fa_qk_norm_rope_bwd: workspace of %zu bytes < %zu required", workspace_bytes, need);
+  a.partials = static_cast<float*>(workspace);
+  return launched(launch_norm_rope(a), "fa_qk_norm_rope_bwd");
 }
 
 fa_status fa_check_device_error(void* stream) {

@@ -270,6 +270,30 @@ struct Kv4EvictArgs {
 };
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a);
 
+// Norms of query and key heads with the rotation by position (norm_rope.cu): element strides of [b][n][heads][d] tensors
+// whose rows are contiguous.
+struct NormRopeStrides {
+  int64_t batch, token, head;
+};
+struct NormRopeArgs {
+  const void *q, *k;            // inputs of the forward
+  const void *wq, *wk;          // [d] of wdtype, or null (ones)
+  const float* table;           // [table_len][rotary]: cos of the rotary / 2 pairs, then sin
+  const int32_t* positions;     // [b][n], or null: 0 .. n - 1
+  const void *qo, *ko;          // forward: outputs; backward: their gradients
+  void *dq, *dk;                // backward: gradients of q, k
+  void *dwq, *dwk;              // backward: [d] of wdtype, or null
+  float* partials;              // backward: [norm_rope_bwd_blocks()][d]
+  NormRopeStrides q_st, k_st, qo_st, ko_st, dq_st, dk_st;
+  int b, n, h, hkv, d, rotary, adjacent, table_len, backward;
+  float eps;
+  int dtype, wdtype;
+  unsigned long long* err;
+  cudaStream_t stream;
+};
+int norm_rope_bwd_blocks();  // blocks of the backward, at most
+cudaError_t launch_norm_rope(const NormRopeArgs& a);
+
 bool fwd_tc_supported(int dtype, int d);
 bool bwd_tc_supported(int dtype, int d);
 bool bwd_masked_fits(int group, int n, int d);  // masked backward's step list fits (tensor-core path)

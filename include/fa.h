@@ -390,6 +390,40 @@ FA_API fa_status fa_kv4_evict(const void* cache, const float* weights, const int
                               int capacity, int out_capacity, int d, void* stream);
 
 /*
+ * Norms of queries and keys for each head, with the rotation by position in the same pass (what a model does to a
+ * projection's output before attention), and its gradients.
+ *   Q, K      [B][N][H][d] and [B][N][Hkv][d] dtype (bf16, fp16 or fp32), rows of d contiguous elements; either may have no
+ *             heads (its pointers are then not looked at)
+ *   Qo, Ko    out: the same, normed and rotated: y = x w / sqrt(mean(x^2) + eps) over the row's d elements, then each of
+ *             the rotary / 2 pairs of channels (a, b) becomes (a cos - b sin, b cos + a sin). In 32 bits, rounded once.
+ *   wq, wk    [d] weight_dtype (fp32 or dtype), or NULL: ones
+ *   table     [table_len][rotary] fp32: cos of the rotary / 2 pairs' angles at a position, then their sin
+ *   positions device int32 [B][N], or NULL: token n of every sequence is at position n (then N <= table_len). A position
+ *             outside [0, table_len) is clamped to it and recorded as a device error.
+ *   rotary    a multiple of 8 in [0, d]; pairs are channels (i, i + rotary / 2), or (2i, 2i + 1) with adjacent != 0;
+ *             channels from rotary on are normed only. d a multiple of 8 in [8, 256].
+ *   strides   HOST int64, three for each tensor (batch, token, head), in elements, for Q, K, Qo, Ko in this order (backward:
+ *             dQo, dKo, Q, K, dQ, dK): multiples of 16 bytes; rows of outputs lie apart. So Q and K may be slices of
+ *             one fused projection, packed sequences are one batch, and Qo may be [B][H][N][d] as fa_fwd takes it.
+ * Outputs overlap no input and no other output, but for an output that is the input of its own kind (Qo = Q; backward: dQ =
+ * dQo or dQ = Q, and so on) with the same strides, and for tensors that share their token and batch strides and lie side by side
+ * inside a token.
+ * Backward: dQ, dK (gradients of Q and K from dQo and dKo) and dwq, dwk ([d] weight_dtype; NULL: not wanted), which are sums over
+ * all tokens and heads, in 32 bits in an order that does not depend on timing. Two launches; the workspace takes
+ * fa_qk_norm_rope_bwd_workspace_size(d) bytes, its contents on entry do not matter. No tokens: dwq and dwk are 0.
+ */
+FA_API fa_status fa_qk_norm_rope(const void* Q, const void* K, const void* wq, const void* wk, const float* table,
+                                 const int32_t* positions, void* Qo, void* Ko, const int64_t* strides, int B, int N, int H,
+                                 int Hkv, int d, int rotary, int adjacent, int table_len, float eps, fa_dtype dtype,
+                                 fa_dtype weight_dtype, void* stream);
+FA_API size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+FA_API fa_status fa_qk_norm_rope_bwd(const void* dQo, const void* dKo, const void* Q, const void* K, const void* wq,
+                                     const void* wk, const float* table, const int32_t* positions, void* dQ, void* dK,
+                                     void* dwq, void* dwk, void* workspace, size_t workspace_bytes, const int64_t* strides,
+                                     int B, int N, int H, int Hkv, int d, int rotary, int adjacent, int table_len,
+                                     float eps, fa_dtype dtype, fa_dtype weight_dtype, void* stream);
+
+/*
  * Synchronises `stream` and reports device-side failures of earlier calls on the
  * current device: FA_ERR_CUDA for a CUDA error, FA_ERR_TIMEOUT / FA_ERR_DEVICE for a
  * failure a kernel recorded. The recorded failure is cleared.
