@@ -596,58 +596,61 @@ def fa_kv4_evict(cache, weights, lens, keep, recent, out_cache, out_weights, out
                                        _current(stream)))
 
 
-def _token_rows(t, heads, ref, what):
-    """(batch, token, head stride) of a [B, N, heads, d] tensor, or of a packed [T, heads, d] one (one batch)
-    of ref's tokens, head dimension and dtype."""
-    if t.dim() != ref.dim() or t.shape[:-2] != ref.shape[:-2] or t.shape[-1] != ref.shape[-1] or t.dtype != ref.dtype:
-        raise ValueError(f"{what} must have Q's batch, tokens, head dimension and dtype")
-    if heads is not None and t.shape[-2] != heads:
-        raise ValueError(f"{what} must have {heads} heads")
-    st, d = t.stride(), t.shape[-1]
-    if d > 1 and st[-1] != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    if t.dim() == 3:
-        return 0, (st[0] if t.shape[0] > 1 else 0), (st[1] if t.shape[1] > 1 else 0)
-    return (st[0] if t.shape[0] > 1 else 0), (st[1] if t.shape[1] > 1 else 0), (st[2] if t.shape[2] > 1 else 0)
+def _token_rows(t):
+    """(batch, token, head stride) of a [B, N, heads, d] tensor, or of a packed [T, heads, d] one (one batch); 0 where there
+    is one step only (torch leaves the strides of one-sized dimensions open)."""
+    sh, st = t.shape, t.stride()
+    if st[-1] != 1 and sh[-1] > 1:
+        raise ValueError("the last dimension must be contiguous")
+    if len(sh) == 3:
+        return 0, (st[0] if sh[0] > 1 else 0), (st[1] if sh[1] > 1 else 0)
+    return (st[0] if sh[0] > 1 else 0), (st[1] if sh[1] > 1 else 0), (st[2] if sh[2] > 1 else 0)
 
 
-def _norm_rope_args(rows, wq, wk, table, positions, eps, interleaved, extra=()):
-    """What fa_qk_norm_rope and its backward are called with behind their pointers; rows: the queries' and the
-    keys' tensors by turns, as their strides are passed."""
-    q, k = rows[0], rows[1]
-    if q.dim() not in (3, 4):
-        raise ValueError(f"expected [B, N, H, d] or packed [T, H, d] queries, got shape {tuple(q.shape)}")
-    strides = []
-    for n, t in enumerate(rows):
-        strides += _token_rows(t, (k if n & 1 else q).shape[-2], q, "keys" if n & 1 else "queries")
-    _ready(wq, wk, table, positions, *extra, strided=rows)
-    B, N = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
-    d = q.shape[-1]
-    wdt = q.dtype
-    for w in (wq, wk):
-        if w is not None:
-            wdt = w.dtype
-            if w.numel() != d or w.dtype != (wq if wq is not None else wk).dtype:
-                raise ValueError("weights must be [d] tensors of one dtype, fp32 or the rows'")
+def _norm_rope_sizes(q, k, wq, wk, table, positions, eps, interleaved, more=()):
+    """What fa_qk_norm_rope and its backward are called with behind their strides, after checking all but the
+    outputs; more: gradients, shaped as q and k by turns."""
+    shape, dt = q.shape, q.dtype
+    if len(shape) == 4:
+        B, N, H, d = shape
+    elif len(shape) == 3:
+        B, (N, H, d) = 1, shape
+    else:
+        raise ValueError(f"expected [B, N, H, d] or packed [T, H, d] queries, got shape {tuple(shape)}")
+    ks = k.shape
+    if len(ks) != len(shape) or ks[-1] != d or ks[:-2] != shape[:-2] or k.dtype != dt:
+        raise ValueError("the keys must have the queries' batch, tokens, head dimension and dtype")
+    for n, t in enumerate(more):
+        if t.shape != (ks if n & 1 else shape) or t.dtype != dt:
+            raise ValueError("outputs and gradients must have their rows' heads, shape and dtype")
+    wdt = wq.dtype if wq is not None else dt if wk is None else wk.dtype
+    if (wq is not None and wq.numel() != d) or (wk is not None and (wk.numel() != d or wk.dtype != wdt)):
+        raise ValueError("weights must be [d] tensors of one dtype, fp32 or the rows'")
     if table is None:
-        rotary, length = 0, 0
+        length = rotary = 0
     else:
         if table.dtype != torch.float32 or table.dim() != 2:
             raise ValueError("the rotation table must be an fp32 tensor [positions, rotary] (rope_table)")
         length, rotary = table.shape
     if positions is not None:
         _int32(positions, B * N, "positions")
-    return ((ctypes.c_int64 * len(strides))(*strides), B, N, q.shape[-2], k.shape[-2], d, rotary, bool(interleaved), length,
-            float(eps), _dt(q), DTYPE_CODES[wdt] if wdt in DTYPE_CODES else _dt(wq))
+    _ready(wq, wk, table, positions, strided=(q, k, *more))
+    if wdt not in DTYPE_CODES or dt not in DTYPE_CODES:
+        raise ValueError(f"unsupported dtype {dt} or {wdt}")
+    return (B, N, H, ks[-2], d, rotary, bool(interleaved), length, float(eps), DTYPE_CODES[dt], DTYPE_CODES[wdt])
+
+
+_Strides4, _Strides6 = ctypes.c_int64 * 12, ctypes.c_int64 * 18
 
 
 def fa_qk_norm_rope(Q, K, wq, wk, table, Qo, Ko, positions=None, eps=1e-6, interleaved=False, stream=None):
     """Qo, Ko = the heads of Q [B, N, H, d] and K [B, N, Hkv, d] (or packed [T, heads, d]; any strides between rows)
     normed with the weights wq, wk [d] (None: ones) and rotated by position with table [positions, rotary] (None: not
     rotated). positions: int32, one a token; None: 0 .. N - 1."""
-    args = _norm_rope_args((Q, K, Qo, Ko), wq, wk, table, positions, eps, interleaved)
-    _check(load_library().fa_qk_norm_rope(_p(Q), _p(K), _p(wq), _p(wk), _p(table), _p(positions), _p(Qo), _p(Ko), *args,
-                                          _current(stream)))
+    strides = _Strides4(*_token_rows(Q), *_token_rows(K), *_token_rows(Qo), *_token_rows(Ko))
+    sizes = _norm_rope_sizes(Q, K, wq, wk, table, positions, eps, interleaved, (Qo, Ko))
+    _check(load_library().fa_qk_norm_rope(Q.data_ptr(), K.data_ptr(), _p(wq), _p(wk), _p(table), _p(positions), Qo.data_ptr(),
+                                          Ko.data_ptr(), strides, *sizes, _current(stream)))
 
 
 def fa_qk_norm_rope_bwd_workspace_size(d) -> int:
@@ -662,14 +665,21 @@ def fa_qk_norm_rope_bwd(dQo, dKo, Q, K, wq, wk, table, dQ, dK, dwq, dwk, positio
             raise ValueError("weight gradients must be [d] tensors of their weights' dtype")
     if wq is None and wk is None and (dwq is not None or dwk is not None):
         raise ValueError("a weight gradient without weights")
-    args = _norm_rope_args((dQo, dKo, Q, K, dQ, dK), wq, wk, table, positions, eps, interleaved,
-                           (dwq, dwk, workspace))
+    sizes = _norm_rope_sizes(Q, K, wq, wk, table, positions, eps, interleaved, (dQo, dKo, dQ, dK))
+    _ready(dwq, dwk, workspace, strided=(Q,))
+    _norm_rope_bwd(dQo, dKo, Q, K, wq, wk, table, positions, dQ, dK, dwq, dwk, workspace,
+                   (*_token_rows(dQo), *_token_rows(dKo), *_token_rows(Q), *_token_rows(K), *_token_rows(dQ),
+                    *_token_rows(dK)), sizes, stream)
+
+
+def _norm_rope_bwd(dQo, dKo, Q, K, wq, wk, table, positions, dQ, dK, dwq, dwk, workspace, strides, sizes, stream):
     lib = load_library()
     if workspace is None:
-        workspace = torch.empty(lib.fa_qk_norm_rope_bwd_workspace_size(Q.shape[-1]), dtype=torch.uint8, device=Q.device)
+        workspace = torch.empty(lib.fa_qk_norm_rope_bwd_workspace_size(sizes[4]), dtype=torch.uint8, device=Q.device)
         _used_on(stream, workspace)
-    _check(lib.fa_qk_norm_rope_bwd(_p(dQo), _p(dKo), _p(Q), _p(K), _p(wq), _p(wk), _p(table), _p(positions), _p(dQ), _p(dK),
-                                   _p(dwq), _p(dwk), _p(workspace), workspace.numel() * workspace.element_size(), *args,
+    _check(lib.fa_qk_norm_rope_bwd(dQo.data_ptr(), dKo.data_ptr(), Q.data_ptr(), K.data_ptr(), _p(wq), _p(wk), _p(table),
+                                   _p(positions), dQ.data_ptr(), dK.data_ptr(), _p(dwq), _p(dwk), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _Strides6(*strides), *sizes,
                                    _current(stream)))
 
 
@@ -817,16 +827,20 @@ def qk_norm_rope(q, k, q_weight, k_weight, table, positions=None, eps=1e-6, inte
     """fa_qk_norm_rope into new tensors: from q [B, N, H, d], k [B, N, Hkv, d] (slices of a fused projection's output, say)
     [B, H, N, d] and [B, Hkv, N, d], what attention_forward takes; from packed [T, heads, d] the same, packed, what
     attention_forward_varlen takes."""
-    if q.dim() == 4 and k.dim() == 4:
-        (B, N, H, d), Hkv = q.shape, k.shape[2]
-        qo = torch.empty((B, H, N, d), dtype=q.dtype, device=q.device)
-        ko = torch.empty((B, Hkv, N, d), dtype=q.dtype, device=q.device)
-        fa_qk_norm_rope(q, k, q_weight, k_weight, table, qo.transpose(1, 2), ko.transpose(1, 2), positions, eps, interleaved,
-                        stream)
+    sizes = _norm_rope_sizes(q, k, q_weight, k_weight, table, positions, eps, interleaved)
+    B, N, H, Hkv, d = sizes[:5]
+    dt, dev = q.dtype, q.device
+    if q.dim() == 4:
+        qo = torch.empty((B, H, N, d), dtype=dt, device=dev)
+        ko = torch.empty((B, Hkv, N, d), dtype=dt, device=dev)
+        out = (H * N * d, d, N * d, Hkv * N * d, d, N * d)
     else:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ko = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        fa_qk_norm_rope(q, k, q_weight, k_weight, table, qo, ko, positions, eps, interleaved, stream)
+        qo = torch.empty((N, H, d), dtype=dt, device=dev)
+        ko = torch.empty((N, Hkv, d), dtype=dt, device=dev)
+        out = (0, H * d, d, 0, Hkv * d, d)
+    _check(load_library().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(table), _p(positions),
+                                          qo.data_ptr(), ko.data_ptr(), _Strides4(*_token_rows(q), *_token_rows(k), *out),
+                                          *sizes, _current(stream)))
     _used_on(stream, qo, ko)
     return qo, ko
 
@@ -836,12 +850,19 @@ def qk_norm_rope_backward(dqo, dko, q, k, q_weight, k_weight, table, positions=N
     """dq, dk, dq_weight, dk_weight = the gradients of qk_norm_rope from those of its results (dqo, dko as it returns them). dq
     and dk have q's and k's shapes; out: tensors (slices of a fused gradient, say) that take them. A weight's gradient
     has its dtype and is None where there is no weight."""
-    dq, dk = out if out is not None else (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
+    if out is not None:
+        dq, dk = out
+    else:
+        dt, dev = q.dtype, q.device
+        dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+    dwq = None if q_weight is None else torch.empty_like(q_weight)
+    dwk = None if k_weight is None else torch.empty_like(k_weight)
     if dqo.dim() == 4 and dko.dim() == 4:
         dqo, dko = dqo.transpose(1, 2), dko.transpose(1, 2)
-    fa_qk_norm_rope_bwd(dqo, dko, q, k, q_weight, k_weight, table, dq, dk, dwq, dwk, positions, eps, interleaved, None,
-                        stream)
+    sizes = _norm_rope_sizes(q, k, q_weight, k_weight, table, positions, eps, interleaved, (dqo, dko, dq, dk))
+    _norm_rope_bwd(dqo, dko, q, k, q_weight, k_weight, table, positions, dq, dk, dwq, dwk, None,
+                   (*_token_rows(dqo), *_token_rows(dko), *_token_rows(q), *_token_rows(k), *_token_rows(dq),
+                    *_token_rows(dk)), sizes, stream)
     _used_on(stream, dwq, dwk, *(() if out is not None else (dq, dk)))
     return dq, dk, dwq, dwk
 

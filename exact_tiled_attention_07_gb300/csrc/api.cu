@@ -868,10 +868,8 @@ static fa_status norm_rope_impl(NormRopeArgs* a, std::initializer_list<RowTensor
       }
     }
   }
-  const uintptr_t weight_align = a->wdtype == FA_FP32 ? 3u : 1u;
   for (const void* w : {a->wq, a->wk, (const void*)a->dwq, (const void*)a->dwk})
-    if ((reinterpret_cast<uintptr_t>(w) & weight_align) != 0)
-      return fail(FA_ERR_INVALID_ARG, "%s: a weight is not aligned to its elements", name);
+    if (!aligned16(w)) return fail(FA_ERR_INVALID_ARG, "%s: a weight is not 16-byte aligned", name);
   return FA_OK;
 }
 

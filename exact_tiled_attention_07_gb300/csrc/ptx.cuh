@@ -463,6 +463,16 @@ __device__ __forceinline__ float2 ffma2(float2 a, float b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
   return d;
 }
+// (a.x b.x + c.x, a.y b.y + c.y)
+__device__ __forceinline__ float2 ffma2v(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
