@@ -28,7 +28,7 @@ __all__ = [
     "fa_sm_clock_sample", "kv4_cache", "fa_kv4_append", "fa_kv4_read", "kv4_read", "fa_decode_kv4",
     "fa_decode_kv4_workspace_size", "attention_decode_kv4", "fa_kv4_evict", "fa_fwd_varlen", "attention_forward_varlen",
     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "rope_table", "qk_norm_rope",
-    "qk_norm_rope_backward",
+    "qk_norm_rope_backward", "fa_fwd_window", "fa_bwd_window", "fa_fwd_varlen_window",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -45,7 +45,7 @@ EXPORTED_SYMBOLS = (
     "fa_selftest_bounded_wait", "fa_fwd_bwd_host", "fa_fwd_bwd_host_workspace_size", "fa_sm_clock_sample",
     "fa_debug_build", "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4",
     "fa_decode_kv4_workspace_size", "fa_kv4_evict", "fa_fwd_varlen", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
-    "fa_qk_norm_rope_bwd_workspace_size",
+    "fa_qk_norm_rope_bwd_workspace_size", "fa_fwd_window", "fa_bwd_window", "fa_fwd_varlen_window",
 )
 
 _lib = None
@@ -109,6 +109,9 @@ def load_library(path=None):
         lib.fa_decode_kv4_workspace_size.restype = sz
         lib.fa_decode_kv4.argtypes = [vp] * 7 + [i] * 6 + [f, i, i, vp, sz, vp]
         lib.fa_kv4_evict.argtypes = [vp] * 3 + [i, i] + [vp] * 4 + [i] * 5 + [vp]
+        lib.fa_fwd_window.argtypes = [vp] * 5 + [i] * 5 + [f, i, i, i, vp]
+        lib.fa_bwd_window.argtypes = [vp] * 10 + [sz] + [i] * 5 + [f, i, i, i, vp]
+        lib.fa_fwd_varlen_window.argtypes = [vp] * 6 + [i] * 5 + [i64] * 8 + [f, i, i, i, vp]
         lib.fa_qk_norm_rope.argtypes = [vp] * 9 + [i] * 8 + [f, i, i, vp]
         lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
         lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
@@ -131,7 +134,8 @@ def load_library(path=None):
                      "fa_bwd_main", "fa_bwd_dq_convert",
                      "fa_check_device_error", "fa_tile_counter", "fa_uses_tensor_cores", "fa_sm_clock_sample",
                      "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_kv4_evict",
-                     "fa_fwd_varlen", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd"):
+                     "fa_fwd_varlen", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_fwd_window", "fa_bwd_window",
+                     "fa_fwd_varlen_window"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -450,6 +454,29 @@ def fa_bwd_masked(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, causal, windo
                                         int(window), mp, mh, _dt(Q), _stream(stream)))
 
 
+def fa_fwd_window(Q, K, V, O, L, scale, window, sinks=0, stream=None):
+    """Causal forward with a sliding window and the first `sinks` keys always visible."""
+    B, H, N, d = _shape4(Q)
+    _on_device(Q, K, V, O, L)
+    Hkv = _kv_heads(Q, K, V)
+    _same(Q, O)
+    _rows(L, B * H * N)
+    _check(load_library().fa_fwd_window(_p(Q), _p(K), _p(V), _p(O), _p(L), B, H, Hkv, N, d, float(scale), int(window),
+                                        int(sinks), _dt(Q), _stream(stream)))
+
+
+def fa_bwd_window(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, window, sinks=0, stream=None):
+    """Backward of fa_fwd_window."""
+    B, H, N, d = _shape4(Q)
+    _on_device(Q, K, V, O, dO, L, dQ, dK, dV, workspace)
+    Hkv = _kv_heads(Q, K, V, dK, dV)
+    _same(Q, O, dO, dQ)
+    _rows(L, B * H * N)
+    _check(load_library().fa_bwd_window(_p(Q), _p(K), _p(V), _p(O), _p(dO), _p(L), _p(dQ), _p(dK), _p(dV), _p(workspace),
+                                        workspace.numel() * workspace.element_size(), B, H, Hkv, N, d, float(scale),
+                                        int(window), int(sinks), _dt(Q), _stream(stream)))
+
+
 def _packed(t, what):
     """(T, heads, d, token stride, head stride) of a packed [T, heads, d] tensor whose rows are
     contiguous; strides of one-sized dimensions, which torch leaves open, as if contiguous."""
@@ -467,9 +494,8 @@ def _int32(t, n, what):
         raise ValueError(f"{what} must be an int32 tensor of {n} elements")
 
 
-def fa_fwd_varlen(Q, K, V, O, L, cu_seqlens, scale, causal, stream=None):
-    """Forward over packed sequences: Q, O [T, H, d], K, V [T, Hkv, d] (rows of contiguous d, any
-    strides between them), L [H, T]; sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] (int32)."""
+def _varlen_args(Q, K, V, O, L, cu_seqlens):
+    """What the calls over packed sequences take up to their scale, after checking it."""
     T, H, d, q_ts, q_hs = _packed(Q, "Q")
     Tk, Hkv, dk, k_ts, k_hs = _packed(K, "K")
     _, _, _, v_ts, v_hs = _packed(V, "V")
@@ -484,9 +510,21 @@ def fa_fwd_varlen(Q, K, V, O, L, cu_seqlens, scale, causal, stream=None):
     if cu_seqlens.dim() != 1 or n < 1:
         raise ValueError("cu_seqlens must be an int32 tensor of S + 1 elements")
     _int32(cu_seqlens, n, "cu_seqlens")
-    _check(load_library().fa_fwd_varlen(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(),
-                                        cu_seqlens.data_ptr(), n - 1, T, H, Hkv, d, q_ts, q_hs, k_ts, k_hs, v_ts, v_hs,
-                                        o_ts, o_hs, scale, bool(causal), _dt(Q), _current(stream)))
+    return (Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), cu_seqlens.data_ptr(), n - 1, T, H, Hkv, d,
+            q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs)
+
+
+def fa_fwd_varlen(Q, K, V, O, L, cu_seqlens, scale, causal, stream=None):
+    """Forward over packed sequences: Q, O [T, H, d], K, V [T, Hkv, d] (rows of contiguous d, any
+    strides between them), L [H, T]; sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] (int32)."""
+    args = _varlen_args(Q, K, V, O, L, cu_seqlens)
+    _check(load_library().fa_fwd_varlen(*args, scale, bool(causal), _dt(Q), _current(stream)))
+
+
+def fa_fwd_varlen_window(Q, K, V, O, L, cu_seqlens, scale, window, sinks=0, stream=None):
+    """fa_fwd_varlen, causal, with a sliding window and the first `sinks` rows of each sequence always visible."""
+    args = _varlen_args(Q, K, V, O, L, cu_seqlens)
+    _check(load_library().fa_fwd_varlen_window(*args, scale, int(window), int(sinks), _dt(Q), _current(stream)))
 
 
 def _kv4_shape(cache):
@@ -742,15 +780,26 @@ def _warn_cuda_core(pass_, t, d):
                       f"kernels (fp32 arithmetic): no tensor-core kernel for this head dimension", stacklevel=3)
 
 
-def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, block_mask=None):
+def _sinks_allowed(causal, window, sinks, block_mask=None):
+    """Whether a call is one of a window with sinks (fa_fwd_window and its kind)."""
+    if not sinks:
+        return False
+    if not causal or window < 1 or block_mask is not None:
+        raise ValueError("sinks go with causal attention and a window, without a block mask")
+    return True
+
+
+def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, block_mask=None, sinks=0):
     """O, L = fa_fwd(q, k, v) (fa_fwd_gqa when k, v have fewer heads than q; fa_fwd_masked with a
-    window or a block mask); outputs on q's device."""
+    window or a block mask; fa_fwd_window with a window, causal, and sinks); outputs on q's device."""
     B, H, N, d = _shape4(q)
     _warn_cuda_core("fwd", q, d)
     scale = d ** -0.5 if scale is None else scale
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    if window or block_mask is not None:
+    if _sinks_allowed(causal, window, sinks, block_mask):
+        fa_fwd_window(q, k, v, o, lse, scale, window, sinks, stream)
+    elif window or block_mask is not None:
         fa_fwd_masked(q, k, v, o, lse, scale, causal, window, block_mask, stream)
     elif k.shape[1] != H:
         fa_fwd_gqa(q, k, v, o, lse, scale, causal, stream)
@@ -760,9 +809,9 @@ def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, 
 
 
 def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=None, stream=None, window=0,
-                       block_mask=None):
-    """dQ, dK, dV = fa_bwd(...) (fa_bwd_masked with a window or a block mask); outputs (and
-    workspace, unless given) allocated with torch."""
+                       block_mask=None, sinks=0):
+    """dQ, dK, dV = fa_bwd(...) (fa_bwd_masked with a window or a block mask; fa_bwd_window with a window
+    and sinks); outputs (and workspace, unless given) allocated with torch."""
     B, H, N, d = _shape4(q)
     _warn_cuda_core("bwd", q, d)
     scale = d ** -0.5 if scale is None else scale
@@ -770,7 +819,9 @@ def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=
     if workspace is None:
         nbytes = fa_bwd_workspace_size(B, H, N, d)
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    if window or block_mask is not None:
+    if _sinks_allowed(causal, window, sinks, block_mask):
+        fa_bwd_window(q, k, v, o, do, lse, dq, dk, dv, workspace, scale, window, sinks, stream)
+    elif window or block_mask is not None:
         fa_bwd_masked(q, k, v, o, do, lse, dq, dk, dv, workspace, scale, causal, window, block_mask, stream)
     elif k.shape[1] != H:
         fa_bwd_gqa(q, k, v, o, do, lse, dq, dk, dv, workspace, scale, causal, stream)
@@ -792,13 +843,20 @@ def attention_decode(q, k, v, scale=None, splits=0, stream=None):
     return o, lse
 
 
-def attention_forward_varlen(q, k, v, cu_seqlens, causal=False, scale=None, stream=None):
-    """O [T, H, d], L [H, T] = fa_fwd_varlen(...) for packed q [T, H, d], k, v [T, Hkv, d]."""
+def attention_forward_varlen(q, k, v, cu_seqlens, causal=False, scale=None, stream=None, window=0, sinks=0):
+    """O [T, H, d], L [H, T] = fa_fwd_varlen(...) for packed q [T, H, d], k, v [T, Hkv, d]; fa_fwd_varlen_window with a
+    window (causal), and sinks."""
+    if window and not causal:
+        raise ValueError("a window over packed sequences is causal")
+    _sinks_allowed(causal, window, sinks)
     T, H, d, _, _ = _packed(q, "Q")
     scale = d ** -0.5 if scale is None else scale
     o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    fa_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale, causal, stream)
+    if window:
+        fa_fwd_varlen_window(q, k, v, o, lse, cu_seqlens, scale, window, sinks, stream)
+    else:
+        fa_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale, causal, stream)
     _used_on(stream, o, lse)
     return o, lse
 

@@ -309,8 +309,16 @@ struct MaskSpec {
   int window = 0;
   const uint8_t* block_mask = nullptr;
   int mask_heads = 0;
+  bool band = false;  // causal with `window` and the first `sinks` keys always visible
+  int sinks = 0;
   bool any() const { return window > 0 || block_mask != nullptr; }
 };
+
+fa_status check_band(int window, int sinks, const char* what) {
+  if (window < 1) return fail(FA_ERR_INVALID_ARG, "%s: window must be >= 1, got %d", what, window);
+  if (sinks < 0) return fail(FA_ERR_INVALID_ARG, "%s: sinks must be >= 0, got %d", what, sinks);
+  return FA_OK;
+}
 
 fa_status check_mask(const MaskSpec& m, int H, int Hkv, int N, int d, fa_dtype dtype, bool backward) {
   if (m.window < 0) return fail(FA_ERR_INVALID_ARG, "window must be >= 0 (0: none), got %d", m.window);
@@ -319,6 +327,13 @@ fa_status check_mask(const MaskSpec& m, int H, int Hkv, int N, int d, fa_dtype d
       return fail(FA_ERR_INVALID_ARG, "mask_heads must be 1 or H=%d, got %d", H, m.mask_heads);
   } else if (m.mask_heads != 0) {
     return fail(FA_ERR_INVALID_ARG, "mask_heads=%d without a block mask (must be 0)", m.mask_heads);
+  }
+  if (m.band) {
+    const fa_status st = check_band(m.window, m.sinks, backward ? "fa_bwd_window" : "fa_fwd_window");
+    if (st != FA_OK) return st;
+    if (!fwd_tc_supported((int)dtype, d))
+      return fail(FA_ERR_UNSUPPORTED, "windows with sinks run on the tensor-core kernels (bf16/fp16, d in {64, 128, 256})");
+    return FA_OK;
   }
   if (!m.any()) return FA_OK;
   const bool tc = backward ? bwd_tc_supported((int)dtype, d) : fwd_tc_supported((int)dtype, d);
@@ -349,6 +364,8 @@ fa_status fwd_impl(const void* Q, const void* K, const void* V, void* O, float* 
   a.block_mask = mask.block_mask;
   a.mask_heads = mask.mask_heads;
   a.heads = H;
+  a.band = mask.band;
+  a.sinks = mask.sinks;
   if (fwd_tc_supported(a.dtype, d)) return launched(launch_fwd_tc(a), "forward (tensor-core kernel)");
   return note_cuda_core_path(launched(launch_fwd_simt(a), "forward (CUDA-core kernel)"), "forward", dtype, d);
 }
@@ -387,6 +404,8 @@ fa_status bwd_main_impl(const void* Q, const void* K, const void* V, const void*
   a.block_mask = mask.block_mask;
   a.mask_heads = mask.mask_heads;
   a.heads = H;
+  a.band = mask.band;
+  a.sinks = mask.sinks;
   if (bwd_tc_supported(a.dtype, d)) return launched(launch_bwd_tc(a), "backward (tensor-core kernel)");
   return note_cuda_core_path(launched(launch_bwd_simt(a), "backward (CUDA-core kernels)"), "backward", dtype, d);
 }
@@ -501,6 +520,36 @@ fa_status fa_bwd_masked(const void* Q, const void* K, const void* V, const void*
   if ((st = fa_bwd_preprocess(O, dO, L, workspace, workspace_bytes, B, H, N, d, dtype, stream)) != FA_OK) return st;
   if ((st = bwd_main_impl(Q, K, V, dO, dK, dV, workspace, workspace_bytes, B, H, Hkv, N, d, scale, causal, dtype,
                           stream, "fa_bwd_masked", m)) != FA_OK)
+    return st;
+  return fa_bwd_dq_convert(workspace, workspace_bytes, dQ, B, H, N, d, scale, dtype, stream);
+}
+
+fa_status fa_fwd_window(const void* Q, const void* K, const void* V, void* O, float* L, int B, int H, int Hkv, int N, int d,
+                        float scale, int window, int sinks, fa_dtype dtype, void* stream) {
+  MaskSpec m;
+  m.band = true;
+  m.window = window;
+  m.sinks = sinks;
+  return fwd_impl(Q, K, V, O, L, B, H, Hkv, N, d, scale, 1, dtype, stream, "fa_fwd_window", m);
+}
+
+fa_status fa_bwd_window(const void* Q, const void* K, const void* V, const void* O, const void* dO, const float* L,
+                        void* dQ, void* dK, void* dV, void* workspace, size_t workspace_bytes, int B, int H, int Hkv,
+                        int N, int d, float scale, int window, int sinks, fa_dtype dtype, void* stream) {
+  MaskSpec m;
+  m.band = true;
+  m.window = window;
+  m.sinks = sinks;
+  bool empty;
+  fa_status st = check_common(B, H, N, d, dtype, &empty);
+  if (st != FA_OK || empty) return st;
+  if ((st = check_heads(H, Hkv)) != FA_OK) return st;
+  if ((st = check_ptrs({Q, K, V, O, dO, L, dQ, dK, dV, workspace}, "fa_bwd_window")) != FA_OK) return st;
+  if ((st = check_scale(scale)) != FA_OK) return st;
+  if ((st = check_mask(m, H, Hkv, N, d, dtype, true)) != FA_OK) return st;
+  if ((st = fa_bwd_preprocess(O, dO, L, workspace, workspace_bytes, B, H, N, d, dtype, stream)) != FA_OK) return st;
+  if ((st = bwd_main_impl(Q, K, V, dO, dK, dV, workspace, workspace_bytes, B, H, Hkv, N, d, scale, 1, dtype, stream,
+                          "fa_bwd_window", m)) != FA_OK)
     return st;
   return fa_bwd_dq_convert(workspace, workspace_bytes, dQ, B, H, N, d, scale, dtype, stream);
 }
@@ -646,37 +695,59 @@ fa_status fa_fwd_fp8(const void* Q8, const void* K8, const void* V8, const float
                         stream);
 }
 
-fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* L, const int32_t* cu_seqlens, int S,
-                        int T, int H, int Hkv, int d, int64_t q_token_stride, int64_t q_head_stride,
-                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
-                        int64_t o_token_stride, int64_t o_head_stride, float scale, int causal, fa_dtype dtype,
-                        void* stream) {
+static fa_status varlen_impl(const void* Q, const void* K, const void* V, void* O, float* L, const int32_t* cu_seqlens, int S,
+                             int T, int H, int Hkv, int d, int64_t q_token_stride, int64_t q_head_stride,
+                             int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                             int64_t o_token_stride, int64_t o_head_stride, float scale, int causal, int window, int sinks,
+                             fa_dtype dtype, void* stream, const char* name) {
   if (dtype != FA_BF16 && dtype != FA_FP16)
-    return fail(FA_ERR_UNSUPPORTED, "fa_fwd_varlen takes bf16 or fp16, not dtype %d", (int)dtype);
+    return fail(FA_ERR_UNSUPPORTED, "%s takes bf16 or fp16, not dtype %d", name, (int)dtype);
   if (S < 0 || T < 0 || H < 0) return fail(FA_ERR_INVALID_ARG, "negative size S=%d T=%d H=%d", S, T, H);
   if (!fwd_tc_supported((int)dtype, d))
-    return fail(FA_ERR_UNSUPPORTED, "fa_fwd_varlen supports d in {64, 128, 256}, got %d", d);
+    return fail(FA_ERR_UNSUPPORTED, "%s supports d in {64, 128, 256}, got %d", name, d);
   if (S == 0 || T == 0 || H == 0) return FA_OK;
   fa_status st = check_heads(H, Hkv);
   if (st != FA_OK) return st;
   if ((double)H * ((double)T / 128 + S) > 1.0e9 || T > INT32_MAX - 512)
     return fail(FA_ERR_INVALID_ARG, "problem too large: S=%d T=%d H=%d", S, T, H);
-  if ((st = check_ptrs({Q, K, V, O}, "fa_fwd_varlen")) != FA_OK) return st;
-  if ((st = check_words({L, cu_seqlens}, "fa_fwd_varlen")) != FA_OK) return st;
+  if ((st = check_ptrs({Q, K, V, O}, name)) != FA_OK) return st;
+  if ((st = check_words({L, cu_seqlens}, name)) != FA_OK) return st;
   if ((st = check_scale(scale)) != FA_OK) return st;
   const int64_t strides[] = {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
                              v_token_stride, v_head_stride, o_token_stride, o_head_stride};
   for (int64_t v : strides) {
-    if ((st = check_strides({v}, 2, "fa_fwd_varlen")) != FA_OK) return st;
-    if (v < d) return fail(FA_ERR_INVALID_ARG, "fa_fwd_varlen: a stride of %lld elements < d=%d", (long long)v, d);
+    if ((st = check_strides({v}, 2, name)) != FA_OK) return st;
+    if (v < d) return fail(FA_ERR_INVALID_ARG, "%s: a stride of %lld elements < d=%d", name, (long long)v, d);
   }
-  if ((st = check_output_rows(T, o_token_stride, H, o_head_stride, d, "fa_fwd_varlen")) != FA_OK) return st;
+  if ((st = check_output_rows(T, o_token_stride, H, o_head_stride, d, name)) != FA_OK) return st;
   DeviceSyms syms;
   if ((st = device_syms(&syms)) != FA_OK) return st;
   VarlenFwdArgs a{Q, K, V, O, L, cu_seqlens, S, T, H, H / Hkv, d, q_token_stride, q_head_stride, k_token_stride,
                   k_head_stride, v_token_stride, v_head_stride, o_token_stride, o_head_stride, scale, causal ? 1 : 0,
-                  (int)dtype, syms.err, syms.counter, static_cast<cudaStream_t>(stream)};
-  return launched(launch_fwd_varlen(a), "fa_fwd_varlen");
+                  (int)dtype, syms.err, syms.counter, static_cast<cudaStream_t>(stream), window, sinks};
+  return launched(launch_fwd_varlen(a), name);
+}
+
+fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* L, const int32_t* cu_seqlens, int S,
+                        int T, int H, int Hkv, int d, int64_t q_token_stride, int64_t q_head_stride,
+                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                        int64_t o_token_stride, int64_t o_head_stride, float scale, int causal, fa_dtype dtype,
+                        void* stream) {
+  return varlen_impl(Q, K, V, O, L, cu_seqlens, S, T, H, Hkv, d, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                     v_token_stride, v_head_stride, o_token_stride, o_head_stride, scale, causal, 0, 0, dtype, stream,
+                     "fa_fwd_varlen");
+}
+
+fa_status fa_fwd_varlen_window(const void* Q, const void* K, const void* V, void* O, float* L, const int32_t* cu_seqlens,
+                               int S, int T, int H, int Hkv, int d, int64_t q_token_stride, int64_t q_head_stride,
+                               int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                               int64_t v_head_stride, int64_t o_token_stride, int64_t o_head_stride, float scale,
+                               int window, int sinks, fa_dtype dtype, void* stream) {
+  const fa_status st = check_band(window, sinks, "fa_fwd_varlen_window");
+  if (st != FA_OK) return st;
+  return varlen_impl(Q, K, V, O, L, cu_seqlens, S, T, H, Hkv, d, q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                     v_token_stride, v_head_stride, o_token_stride, o_head_stride, scale, 1, window, sinks, dtype, stream,
+                     "fa_fwd_varlen_window");
 }
 
 static fa_status kv4_rows(bool read, const void* K, const void* V, const int32_t* cu_seqlens, const int32_t* lens,

@@ -177,7 +177,11 @@ struct BwdItem {
 // roles start, the (query head of the group, 128-row query block) pairs that can see the key
 // tile (block-mask byte set and some pair inside the causal and window bounds); every role
 // walks that list.
-template <int D, bool BF16, bool MASKED>
+// Window variant (WINDOW, causal): query i sees key j when j <= i and (i - j < window or j < sinks).  A key tile without sinks
+// meets the query tiles from its diagonal to the end of its last key's window, one with sinks all from its diagonal on: a
+// range again, so the persistent grid and its queue stay.  Items with sinks are the longest by far (N rows against
+// window + 127) and come first, for all heads; the others follow in the groups of heads that stay in L2.
+template <int D, bool BF16, bool MASKED, bool WINDOW = false>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -186,8 +190,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                   const float* __restrict__ delta, int n, int npad, int bh_count, int ktiles, float scale,
                   int causal, int group, unsigned long long* err, int window,
                   const uint8_t* __restrict__ block_mask, int mask_heads, int heads, unsigned* __restrict__ sched,
-                  int hgroup) {
+                  int hgroup, int sinks) {
   using C = BwdCfg<D>;
+  static_assert(!(MASKED && WINDOW), "one kind of mask");
   constexpr int BM = C::BM;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
@@ -205,7 +210,18 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   const int64_t total_items = (int64_t)bh_count * ktiles * kHalves;
   // work item -> key/value head and key tile: head-major (CTAs running together share Q/dO in
   // L2); causal: heaviest (first) key tiles first within groups of heads
+  const int sink_tiles = WINDOW ? min(ktiles, sinks / BN + (sinks % BN != 0)) : 0;
   auto tile_of = [&](int item, int* kvh, int* kt) {
+    if constexpr (WINDOW) {
+      if (item < sink_tiles * bh_count) {
+        *kt = item / bh_count;
+        *kvh = item - *kt * bh_count;
+      } else {
+        grouped_work_item(item - sink_tiles * bh_count, bh_count, ktiles - sink_tiles, hgroup, kvh, kt);
+        *kt += sink_tiles;
+      }
+      return;
+    }
     if (causal) {
       grouped_work_item(item, bh_count, ktiles, hgroup, kvh, kt);
     } else {
@@ -292,6 +308,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     w.k0 = kt * BN;
     w.i_start = causal ? kt * (BN / BM) : 0;
     w.nsteps_head = qtiles - w.i_start;
+    if constexpr (WINDOW) {  // up to the last query that sees the tile's last key (keys behind N have no queries)
+      if (w.k0 >= sinks) {
+        const int64_t last = (int64_t)w.k0 + BN - 2 + window;
+        if (last < n) w.nsteps_head = (int)last / BM + 1 - w.i_start;
+      }
+    }
     w.nsteps = MASKED ? list_hdr[0] * C::SUB : group * w.nsteps_head;
     return w;
   };
@@ -809,6 +831,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
               mask_above = key + window - q0;
             }
           }
+          if constexpr (WINDOW) {
+            if (key >= sinks) mask_above = (int)min((int64_t)key + window - q0, (int64_t)INT32_MAX);
+          }
           // the whole warp sees every query of the step: no masking of P
           const bool all_visible = __all_sync(0xffffffffu, key_ok && mask_below <= 0 && mask_above >= BM);
           // P^T of this key against this half's queries, kept as packed 16-bit pairs: the same
@@ -949,7 +974,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
   }
 }
 
-template <int D, bool BF16, bool MASKED>
+template <int D, bool BF16, bool MASKED, bool WINDOW = false>
 cudaError_t launch_bwd_d(const BwdArgs& a) {
   using C = BwdCfg<D>;
   const int npad = (int)padded_rows(a.n);
@@ -961,7 +986,7 @@ cudaError_t launch_bwd_d(const BwdArgs& a) {
       !make_tmap_f32_3d(&tdq, a.dq_acc, D, npad, a.bh, C::DQT ? C::DH : 32, C::BM, !C::DQT) ||
       !make_tmap_16bit_3d(&tdk, a.dk, BF16, D, a.n, bh_kv, BN) || !make_tmap_16bit_3d(&tdv, a.dv, BF16, D, a.n, bh_kv, BN))
     return cudaErrorInvalidValue;
-  auto kern = bwd_tc_kernel<D, BF16, MASKED>;
+  auto kern = bwd_tc_kernel<D, BF16, MASKED, WINDOW>;
   const int nblk = (a.n + 127) / 128;
   if (MASKED && !bwd_masked_fits(a.group, a.n, D)) return cudaErrorInvalidValue;
   const int smem = C::SMEM + (MASKED ? C::list_bytes(a.group * nblk) : 0);
@@ -976,12 +1001,13 @@ cudaError_t launch_bwd_d(const BwdArgs& a) {
   const int hgroup = head_group_for_l2((int64_t)a.group * ((int64_t)npad * D * 8 + (int64_t)npad * 8), kL2HeadBudgetBwd);
   kern<<<(unsigned)grid, C::THREADS, smem, a.stream>>>(tq, tk, tv, tdo, tdq, tdk, tdv, a.lse2, a.delta, a.n, npad,
                                                        bh_kv, ktiles, a.scale, a.causal, a.group, a.err, a.window,
-                                                       a.block_mask, a.mask_heads, a.heads, a.sched, hgroup);
+                                                       a.block_mask, a.mask_heads, a.heads, a.sched, hgroup, a.sinks);
   return cudaGetLastError();
 }
 
 template <int D, bool BF16>
 cudaError_t launch_bwd_dm(const BwdArgs& a) {
+  if (a.band) return launch_bwd_d<D, BF16, false, true>(a);
   return a.masked() ? launch_bwd_d<D, BF16, true>(a) : launch_bwd_d<D, BF16, false>(a);
 }
 

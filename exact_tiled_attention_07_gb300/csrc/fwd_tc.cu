@@ -176,16 +176,24 @@ struct VarlenSpec {
   int64_t o_ts = 0, o_hs = 0;  // O's token and head strides, elements
 };
 
-template <int D, bool BF16, bool MASKED, bool QUEUE, bool F8 = false, bool VARLEN = false>
+// Window variant (WINDOW, causal): query i sees key j when j <= i and (i - j < window or j < sinks).  The key tiles that an
+// item meets follow from its rows alone, the tiles of the sinks in front of its window and then the window's own, so nothing is
+// listed beforehand (as the block mask's variant does) and the items come from the queue as in the plain kernel (static order
+// where there is no counter).  The two query tiles of an item walk the union of their tiles: of the second one's
+// window / 128 + 2 tiles the first is masked whole.
+// Bound: tensor and softmax, as the plain kernel.
+template <int D, bool BF16, bool MASKED, bool QUEUE, bool F8 = false, bool VARLEN = false, bool WINDOW = false>
 __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, void* __restrict__ out, float* __restrict__ lse, int n,
                   int bh_count, int tiles_per_head, float scale_log2, int causal, int group, unsigned long long* err,
                   unsigned long long* counter, int window, const uint8_t* __restrict__ block_mask, int mask_heads,
-                  int heads, int snake, unsigned* __restrict__ sched, int hgroup, F8Scales f8s, VarlenSpec vl) {
+                  int heads, int snake, unsigned* __restrict__ sched, int hgroup, F8Scales f8s, VarlenSpec vl,
+                  int sinks) {
   using C = FwdCfg<D, F8>;
   static_assert(!(F8 && MASKED), "the FP8 variant has no masks");
   static_assert(!VARLEN || (QUEUE && !MASKED && !F8), "the packed variant publishes its items");
+  static_assert(!WINDOW || (QUEUE && !MASKED && !F8), "the window variant publishes its items");
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -223,17 +231,23 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     int head, kvhead, qrow0;
     int nq[2];  // key tiles of each query tile
     int base, n, nblk;  // first row of the sequence, its length and its key tiles
+    int ns, j0;         // (window) tiles of sinks in front of the window, first tile of the window
   };
   // key tiles of each query tile of an item whose head, qrow0, n and nblk are set
   auto count_tiles = [&](Item& w) {
     w.kvhead = w.head / group;  // grouped-query attention: key/value head shared by `group` query heads
+    w.ns = w.j0 = 0;
+    if constexpr (WINDOW) {
+      w.j0 = max(0, w.qrow0 - window + 1) / BN;
+      w.ns = min(w.j0, min(sinks, w.n) / BN + (min(sinks, w.n) % BN != 0));
+    }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int first = w.qrow0 + q * BM;
       if (q >= C::NQ || first >= w.n) {
         w.nq[q] = 0;
       } else if (causal) {
-        w.nq[q] = min(w.nblk, (min(first + BM, w.n) - 1) / BN + 1);
+        w.nq[q] = min(w.nblk, (min(first + BM, w.n) - 1) / BN + 1) - w.j0 + w.ns;
       } else {
         w.nq[q] = w.nblk;
       }
@@ -397,7 +411,10 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     return w;
   };
   // key tile at position t of an item's sequence
-  auto tile_at = [&](int t) { return MASKED ? (int)jlist[t] : t; };
+  auto tile_at = [&](const Item& w, int t) {
+    if constexpr (WINDOW) return t < w.ns ? t : t - w.ns + w.j0;
+    return MASKED ? (int)jlist[t] : t;
+  };
   // order of an item's K and V tiles in the ring (n key tiles): K0 V0 K1 V1 ... with two query
   // tiles (both tiles' GEMMs use a pair in turn); with one (S double-buffered) the order in which
   // the tensor core uses them, K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1), so that the ring is
@@ -473,8 +490,12 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
           mbar_arrive(B.item_full + (r & 1));
           return -1;
         }
-        const unsigned ticket = atomicAdd(sched, 1u);
-        const int item = ticket < (unsigned)total_items ? (int)ticket : -1;
+        int64_t ticket;
+        if (!WINDOW || sched)
+          ticket = atomicAdd(sched, 1u);
+        else
+          ticket = (int64_t)(static_turn++) * grid_dim_x() + cta_id_x();
+        const int item = ticket < total_items ? (int)ticket : -1;
         item_slot[r & 1] = item;
         mbar_arrive(B.item_full + (r & 1));
         return item;
@@ -498,7 +519,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
           bool is_v;
           int j;
           ring_tile(idx, nmax, &is_v, &j);
-          if (!(ok = debug_check(j >= 0 && j < nmax && tile_at(j) >= 0 && tile_at(j) < w.nblk, ctx, 61))) break;
+          if (!(ok = debug_check(j >= 0 && j < nmax && tile_at(w, j) >= 0 && tile_at(w, j) < w.nblk, ctx, 61))) break;
           const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
           for (int e = 0; e < C::RB; ++e) {
             const uint32_t g = ring_pos;
@@ -509,7 +530,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
             constexpr int kbs = C::KB / C::RB;  // column blocks per entry
             for (int kb = 0; kb < kbs; ++kb)
               tma_load_3d(dst + kb * (BN * C::SW), tm, B.kv_full + slot, (e * kbs + kb) * C::BLK_COLS,
-                          w.base + tile_at(j) * BN, w.kvhead);
+                          w.base + tile_at(w, j) * BN, w.kvhead);
             ++ring_pos;
           }
         }
@@ -641,7 +662,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
       // (packed) the V rows of the item's last key tile that lie behind the sequence: zero
       auto clear_tail = [&](const Item& w, int j, int vidx) {
         if constexpr (VARLEN) {
-          const int rem = w.n - j * BN;
+          const int rem = w.n - tile_at(w, j) * BN;
           if (rem >= BN) return;
           uint8_t* vt = smem + C::OFF_RING + slot_of(vidx) * C::ENTRY_BYTES;
           for (int i = rem * 8 + lane; i < BN * 8; i += 32)
@@ -867,7 +888,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
         }
         // visible columns [lo, hi) of this row: keys before N, (causal) not after the row,
         // (window) within the window; none when the tile is listed only for the other query tile
-        const int jt = tile_at(j);
+        const int jt = tile_at(w, j);
         int lo = 0, hi = w.n - jt * BN;
         if (causal) hi = min(hi, row - jt * BN + 1);
         if constexpr (MASKED) {
@@ -877,7 +898,14 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
           }
           if (!((jflag[j] >> q) & 1)) hi = lo = 0;
         }
-        if (lo > 0 || hi < BN) {
+        if constexpr (WINDOW) lo = row - window + 1 - jt * BN;
+        if (WINDOW && lo > 0 && sinks > jt * BN) {
+          // a tile of sinks (keys below `sinks` stay visible) behind which a window begins or that it has left
+          const int top = sinks - jt * BN;
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c >= hi || (c >= top && c < lo)) s[c] = -INFINITY;
+        } else if (lo > 0 || hi < BN) {
 #pragma unroll
           for (int c = 0; c < BN; ++c)
             if (c < lo || c >= hi) s[c] = -INFINITY;
@@ -1077,7 +1105,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
-  if (queue && (!VARLEN || sched) && threadIdx.x == 0) {  // (queue: a compile-time constant)
+  if (queue && ((!VARLEN && !WINDOW) || sched) && threadIdx.x == 0) {  // (queue: a compile-time constant)
     // this CTA draws no more tickets; the last one to get here empties the queue for the next
     // launch that uses it (every CTA has drawn its last ticket by then)
     __threadfence();
@@ -1111,7 +1139,7 @@ int64_t max_cta_tiles(int bh, int tiles_per_head, int n, int nq_tiles, int g, bo
 
 // Launch of the persistent forward (16-bit, or FP8 when f8 carries the block scales; then
 // Q, K, V of `a` are E4M3 codes and BF16 is O's type).
-template <int D, bool BF16, bool MASKED, bool F8 = false>
+template <int D, bool BF16, bool MASKED, bool F8 = false, bool WINDOW = false>
 cudaError_t launch_fwd_d(const FwdArgs& a, F8Scales f8 = F8Scales()) {
   using C = FwdCfg<D, F8>;
   CUtensorMap tq, tk, tv, to;
@@ -1135,7 +1163,7 @@ cudaError_t launch_fwd_d(const FwdArgs& a, F8Scales f8 = F8Scales()) {
   const int64_t grid = MASKED ? items : std::min<int64_t>(items, device_sm_count());
   // causal order: groups of query heads whose K, V (shared by `group` query heads) stay in L2
   const int hgroup = head_group_for_l2((int64_t)2 * a.n * C::ROW / a.group, kL2HeadBudgetFwd);
-  const int snake = (!MASKED && a.causal && grid < items &&
+  const int snake = (!MASKED && !WINDOW && a.causal && grid < items &&
                      max_cta_tiles(a.bh, tiles, a.n, C::NQ, (int)grid, true, hgroup) <
                          max_cta_tiles(a.bh, tiles, a.n, C::NQ, (int)grid, false, hgroup))
                         ? 1
@@ -1144,8 +1172,8 @@ cudaError_t launch_fwd_d(const FwdArgs& a, F8Scales f8 = F8Scales()) {
   // items, whatever the cause), else the static order
   QueueSlot qs;
   if (!MASKED && grid < items) qs = queue_slot_take(a.stream);
-  auto kern = fwd_tc_kernel<D, BF16, MASKED, false, F8>;
-  if constexpr (!MASKED) {
+  auto kern = fwd_tc_kernel<D, BF16, MASKED, WINDOW, F8, false, WINDOW>;
+  if constexpr (!MASKED && !WINDOW) {
     if (qs.slot >= 0) kern = fwd_tc_kernel<D, BF16, false, true, F8>;
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1153,14 +1181,14 @@ cudaError_t launch_fwd_d(const FwdArgs& a, F8Scales f8 = F8Scales()) {
     kern<<<(unsigned)grid, C::THREADS, smem, a.stream>>>(tq, tk, tv, to, a.o, a.lse, a.n, a.bh, tiles, scale_log2,
                                                          a.causal, a.group, a.err, a.counter, a.window, a.block_mask,
                                                          a.mask_heads, a.heads, snake, qs.counters, hgroup, f8,
-                                                         VarlenSpec());
+                                                         VarlenSpec(), a.sinks);
     e = cudaGetLastError();
   }
   return queue_slot_done(qs, e, a.stream);
 }
 
-template <int D, bool BF16>
-cudaError_t launch_fwd_varlen_d(const VarlenFwdArgs& a) {
+template <int D, bool BF16, bool WINDOW>
+cudaError_t launch_fwd_varlen_dw(const VarlenFwdArgs& a) {
   using C = FwdCfg<D>;
   CUtensorMap tq, tk, tv, to;
   const int hkv = a.h / a.group;
@@ -1177,7 +1205,7 @@ cudaError_t launch_fwd_varlen_d(const VarlenFwdArgs& a) {
   const int hgroup = head_group_for_l2((int64_t)2 * a.t * C::ROW / a.group, kL2HeadBudgetFwd);
   QueueSlot qs;
   if (grid < items) qs = queue_slot_take(a.stream);
-  auto kern = fwd_tc_kernel<D, BF16, false, true, false, true>;
+  auto kern = fwd_tc_kernel<D, BF16, false, true, false, true, WINDOW>;
   static std::atomic<unsigned long long> allowed;
   cudaError_t e = allow_smem(kern, smem, &allowed);
   if (e == cudaSuccess) {
@@ -1188,15 +1216,21 @@ cudaError_t launch_fwd_varlen_d(const VarlenFwdArgs& a) {
     vl.o_hs = a.o_hs;
     kern<<<(unsigned)grid, C::THREADS, smem, a.stream>>>(tq, tk, tv, to, a.o, a.lse, a.t, a.h, tiles,
                                                          a.scale * 1.4426950408889634f, a.causal, a.group, a.err,
-                                                         a.counter, 0, nullptr, 0, a.h, 0, qs.counters, hgroup,
-                                                         F8Scales(), vl);
+                                                         a.counter, a.window, nullptr, 0, a.h, 0, qs.counters, hgroup,
+                                                         F8Scales(), vl, a.sinks);
     e = cudaGetLastError();
   }
   return queue_slot_done(qs, e, a.stream);
 }
 
 template <int D, bool BF16>
+cudaError_t launch_fwd_varlen_d(const VarlenFwdArgs& a) {
+  return a.window > 0 ? launch_fwd_varlen_dw<D, BF16, true>(a) : launch_fwd_varlen_dw<D, BF16, false>(a);
+}
+
+template <int D, bool BF16>
 cudaError_t launch_fwd_dm(const FwdArgs& a) {
+  if (a.band) return launch_fwd_d<D, BF16, false, false, true>(a);
   return a.masked() ? launch_fwd_d<D, BF16, true>(a) : launch_fwd_d<D, BF16, false>(a);
 }
 

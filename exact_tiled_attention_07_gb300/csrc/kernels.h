@@ -35,6 +35,9 @@ struct FwdArgs {
   int mask_heads = 0;
   int heads = 1;
   bool masked() const { return window > 0 || block_mask != nullptr; }
+  // band: causal with `window` and the first `sinks` keys always visible, instead of the masks above
+  bool band = false;
+  int sinks = 0;
 };
 
 // Backward workspace, carved from one caller buffer of fa_bwd_workspace_size bytes:
@@ -70,6 +73,8 @@ struct BwdArgs {
   int mask_heads = 0;
   int heads = 1;
   bool masked() const { return window > 0 || block_mask != nullptr; }
+  bool band = false;  // as in FwdArgs
+  int sinks = 0;
 };
 
 // Decode over a key/value cache: Q, O [b][h][nq][d], K, V [b][hkv][nk][d], L [b][h][nq].
@@ -213,6 +218,8 @@ struct VarlenFwdArgs {
   unsigned long long* err;
   unsigned long long* counter;
   cudaStream_t stream;
+  int window = 0;  // > 0 (causal): a sliding window, and the first `sinks` rows of the sequence stay visible
+  int sinks = 0;
 };
 cudaError_t launch_fwd_varlen(const VarlenFwdArgs& a);
 

@@ -31,7 +31,8 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxOcc = 6;
+constexpr int kMaxOcc = 3;
+
 // P consecutive channels of a row as they lie in memory, and as P / 2 pairs of floats.
 template <typename T, int P>
 struct Piece {

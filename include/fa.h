@@ -242,6 +242,21 @@ FA_API fa_status fa_bwd_masked(const void* Q, const void* K, const void* V, cons
                                const uint8_t* block_mask, int mask_heads, fa_dtype dtype, void* stream);
 
 /*
+ * Causal attention with a sliding window and a few first keys (sinks) that stay visible: query i sees key j when j <= i
+ * and (i - j < window or j < sinks). Layouts, grouped heads, workspace and errors as fa_fwd_gqa / fa_bwd_gqa; window >= 1,
+ * sinks >= 0 (either may exceed N: a window of N or more is causal attention). bf16 and fp16 with d in {64, 128, 256}; others
+ * return FA_ERR_UNSUPPORTED. Key tiles outside the window and the sinks are neither loaded nor multiplied. (Inside a 128-row tile
+ * that is visible in part, a hidden key's weight is an exact zero, as in fa_fwd: a V row that is not finite reaches the
+ * queries whose 128-row tiles meet its tile.) One launch forward, the three of fa_bwd backward.
+ */
+FA_API fa_status fa_fwd_window(const void* Q, const void* K, const void* V, void* O, float* L, int B, int H, int Hkv,
+                               int N, int d, float scale, int window, int sinks, fa_dtype dtype, void* stream);
+FA_API fa_status fa_bwd_window(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                               const float* L, void* dQ, void* dK, void* dV, void* workspace, size_t workspace_bytes,
+                               int B, int H, int Hkv, int N, int d, float scale, int window, int sinks, fa_dtype dtype,
+                               void* stream);
+
+/*
  * FP8 (E4M3) block quantisation ("Lecture 8" §8.1, "FlashAttention and GPU memory" §11: the
  * third generation runs attention in 8-bit floating point with one scale per block).
  *   X        in:  [B][H][N][d] dtype (bf16, fp16 or fp32)
@@ -308,6 +323,17 @@ FA_API fa_status fa_fwd_varlen(const void* Q, const void* K, const void* V, void
                                int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
                                int64_t v_token_stride, int64_t v_head_stride, int64_t o_token_stride,
                                int64_t o_head_stride, float scale, int causal, fa_dtype dtype, void* stream);
+
+/*
+ * fa_fwd_varlen, causal, with a sliding window and sinks in each sequence (fa_fwd_window): a row sees the `window` newest rows of
+ * its own sequence up to its own and the sequence's first `sinks`. window >= 1, sinks >= 0.
+ */
+FA_API fa_status fa_fwd_varlen_window(const void* Q, const void* K, const void* V, void* O, float* L,
+                                      const int32_t* cu_seqlens, int S, int T, int H, int Hkv, int d,
+                                      int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                                      int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                                      int64_t o_token_stride, int64_t o_head_stride, float scale, int window, int sinks,
+                                      fa_dtype dtype, void* stream);
 
 /*
  * A key/value cache held in 4 bits an element (as the FP8 quantiser's block scales, "Lecture 8"

@@ -136,3 +136,45 @@ def test_binding_refuses_what_does_not_fit():
         fa.fa_qk_norm_rope(q, k, w, w, t, q, q)
     with pytest.raises(ValueError, match="without weights"):
         fa.fa_qk_norm_rope_bwd(q, k, q, k, None, None, t, q, k, w, w)
+
+
+# ------------------------------------------------------------------------------------------------ window with sinks
+
+
+def fwd_window(lib, window=10, sinks=2, d=64, dtype=BF16, H=4, Hkv=2, scale=0.125, ptrs=P[:5], N=100):
+    return lib.fa_fwd_window(*ptrs, 1, H, Hkv, N, d, scale, window, sinks, dtype, None)
+
+
+def bwd_window(lib, window=10, sinks=2, d=64, dtype=BF16, H=4, Hkv=2, scale=0.125, ptrs=P[:10], N=100, size=1 << 40):
+    return lib.fa_bwd_window(*ptrs, size, 1, H, Hkv, N, d, scale, window, sinks, dtype, None)
+
+
+def varlen_window(lib, window=10, sinks=2, d=64, dtype=BF16, H=4, Hkv=2, scale=0.125, ptrs=P[:6], T=100, strides=(256, 64) * 4):
+    return lib.fa_fwd_varlen_window(*ptrs, 3, T, H, Hkv, d, *strides, scale, window, sinks, dtype, None)
+
+
+@pytest.mark.parametrize("call,n", [(fwd_window, 5), (bwd_window, 10), (varlen_window, 6)])
+def test_window_arguments(lib, call, n):
+    for bad in ({"window": 0}, {"window": -1}):
+        assert call(lib, **bad) == INVALID and "window" in message(lib)
+    assert call(lib, sinks=-1) == INVALID and "sinks" in message(lib)
+    assert call(lib, H=3) == INVALID and "multiple of Hkv" in message(lib)
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(lib, scale=scale) == INVALID and "scale" in message(lib)
+    assert call(lib, dtype=FP32) == UNSUPPORTED and call(lib, d=96) == UNSUPPORTED and call(lib, d=512) == UNSUPPORTED
+    for i in range(n):
+        assert call(lib, ptrs=[None if j == i else P[j] for j in range(n)]) == INVALID and "null" in message(lib)
+        assert call(lib, ptrs=[P[j] + (2 if j == i else 0) for j in range(n)]) == INVALID and "aligned" in message(lib)
+    assert bwd_window(lib, size=1000) == INVALID and "workspace" in message(lib)
+    assert varlen_window(lib, strides=(256, 64) * 3 + (64, 64)) == INVALID and "overlap" in message(lib)
+    assert fwd_window(lib, N=0, ptrs=[None] * 5) == OK and bwd_window(lib, N=0, ptrs=[None] * 10) == OK
+    assert varlen_window(lib, T=0, ptrs=[None] * 6) == OK
+
+
+def test_binding_keeps_sinks_to_causal_windows():
+    from exact_tiled_attention_07_gb300 import binding as fa
+
+    assert not fa._sinks_allowed(False, 0, 0) and fa._sinks_allowed(True, 5, 1)
+    for causal, window, mask in ((False, 5, None), (True, 0, None), (True, 5, object())):
+        with pytest.raises(ValueError, match="sinks go with"):
+            fa._sinks_allowed(causal, window, 3, mask)
