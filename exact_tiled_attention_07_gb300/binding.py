@@ -29,6 +29,8 @@ __all__ = [
     "fa_decode_kv4_workspace_size", "attention_decode_kv4", "fa_kv4_evict", "fa_fwd_varlen", "attention_forward_varlen",
     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "rope_table", "qk_norm_rope",
     "qk_norm_rope_backward", "fa_fwd_window", "fa_bwd_window", "fa_fwd_varlen_window",
+    "fa_decode_window", "fa_decode_window_workspace_size", "fa_decode_prefix", "fa_decode_prefix_workspace_size",
+    "attention_decode_window", "attention_decode_prefix",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -45,7 +47,8 @@ EXPORTED_SYMBOLS = (
     "fa_selftest_bounded_wait", "fa_fwd_bwd_host", "fa_fwd_bwd_host_workspace_size", "fa_sm_clock_sample",
     "fa_debug_build", "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4",
     "fa_decode_kv4_workspace_size", "fa_kv4_evict", "fa_fwd_varlen", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
-    "fa_qk_norm_rope_bwd_workspace_size", "fa_fwd_window", "fa_bwd_window", "fa_fwd_varlen_window",
+    "fa_qk_norm_rope_bwd_workspace_size", "fa_fwd_window", "fa_bwd_window", "fa_fwd_varlen_window", "fa_decode_window",
+    "fa_decode_window_workspace_size", "fa_decode_prefix", "fa_decode_prefix_workspace_size",
 )
 
 _lib = None
@@ -112,6 +115,12 @@ def load_library(path=None):
         lib.fa_fwd_window.argtypes = [vp] * 5 + [i] * 5 + [f, i, i, i, vp]
         lib.fa_bwd_window.argtypes = [vp] * 10 + [sz] + [i] * 5 + [f, i, i, i, vp]
         lib.fa_fwd_varlen_window.argtypes = [vp] * 6 + [i] * 5 + [i64] * 8 + [f, i, i, i, vp]
+        lib.fa_decode_window_workspace_size.argtypes = [i] * 6
+        lib.fa_decode_window_workspace_size.restype = sz
+        lib.fa_decode_window.argtypes = [vp] * 6 + [i] * 6 + [f, i, i, i, vp, sz, vp]
+        lib.fa_decode_prefix_workspace_size.argtypes = [i] * 7
+        lib.fa_decode_prefix_workspace_size.restype = sz
+        lib.fa_decode_prefix.argtypes = [vp] * 8 + [i] * 7 + [f, i, vp, sz, vp]
         lib.fa_qk_norm_rope.argtypes = [vp] * 9 + [i] * 8 + [f, i, i, vp]
         lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
         lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
@@ -135,7 +144,7 @@ def load_library(path=None):
                      "fa_check_device_error", "fa_tile_counter", "fa_uses_tensor_cores", "fa_sm_clock_sample",
                      "fa_selftest_debug_check", "fa_kv4_append", "fa_kv4_read", "fa_decode_kv4", "fa_kv4_evict",
                      "fa_fwd_varlen", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_fwd_window", "fa_bwd_window",
-                     "fa_fwd_varlen_window"):
+                     "fa_fwd_varlen_window", "fa_decode_window", "fa_decode_prefix"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -634,6 +643,68 @@ def fa_kv4_evict(cache, weights, lens, keep, recent, out_cache, out_weights, out
                                        _current(stream)))
 
 
+def _cache_shape(Q, K, V, lens):
+    """(B, H, Hkv, Nq, capacity, d) of a decode over 16-bit caches of different lengths, after checking what it reads."""
+    if Q.dim() != 4 or K.dim() != 4:
+        raise ValueError("expected Q [B, H, Nq, d] and caches [B, Hkv, capacity, d]")
+    B, H, Nq, d = Q.shape
+    Bk, Hkv, capacity, dk = K.shape
+    _ready(Q, K, V, lens)
+    if (Bk, dk) != (B, d) or V.shape != K.shape or not (Q.dtype == K.dtype == V.dtype):
+        raise ValueError("K, V must be [B, Hkv, capacity, d] of Q's batch, head dimension and dtype")
+    _int32(lens, B, "lens")
+    return B, H, Hkv, Nq, capacity, d
+
+
+def _prefix_shape(shape, Q, KP, VP):
+    """shape with the prefix' length behind Nq, after checking KP, VP [Hkv, P, d]."""
+    B, H, Hkv, Nq, capacity, d = shape
+    if KP.dim() != 3 or (KP.shape[0], KP.shape[2]) != (Hkv, d) or VP.shape != KP.shape or not (
+            KP.dtype == VP.dtype == Q.dtype):
+        raise ValueError("the prefix must be [Hkv, P, d] of the caches' heads, head dimension and dtype")
+    _ready(Q, KP, VP)
+    return B, H, Hkv, Nq, KP.shape[1], capacity, d
+
+
+def fa_decode_window_workspace_size(B, H, Hkv, Nq, capacity, d) -> int:
+    return int(load_library().fa_decode_window_workspace_size(B, H, Hkv, Nq, capacity, d))
+
+
+def fa_decode_prefix_workspace_size(B, H, Hkv, Nq, P, capacity, d) -> int:
+    return int(load_library().fa_decode_prefix_workspace_size(B, H, Hkv, Nq, P, capacity, d))
+
+
+def _cache_workspace(workspace, nbytes, Q, stream):
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
+        _used_on(stream, workspace)
+    return workspace
+
+
+def fa_decode_window(Q, K, V, lens, O, L, scale, window=0, sinks=0, workspace=None, stream=None):
+    """Decode: Q, O [B, H, Nq, d] over caches K, V [B, Hkv, capacity, d] with lens [B] slots in use, the newest of them
+    the Nq rows' own; window > 0: each row sees its `window` newest slots and the first `sinks`. L [B, H, Nq]. workspace: of
+    fa_decode_window_workspace_size bytes; where none is given, one is allocated with torch."""
+    shape = _cache_shape(Q, K, V, lens)
+    _ready(O, L, Q, workspace)
+    _same(Q, O)
+    _rows(L, O.numel() // max(1, O.shape[3]))
+    ws = _cache_workspace(workspace, fa_decode_window_workspace_size(*shape), Q, stream)
+    _check(load_library().fa_decode_window(_p(Q), _p(K), _p(V), _p(lens), _p(O), _p(L), *shape, float(scale), int(window),
+                                           int(sinks), _dt(Q), _p(ws), ws.numel() * ws.element_size(), _current(stream)))
+
+
+def fa_decode_prefix(Q, KP, VP, K, V, lens, O, L, scale, workspace=None, stream=None):
+    """Decode behind a shared prefix: as fa_decode_window without a window, and each row sees all of KP, VP [Hkv, P, d] too."""
+    shape = _prefix_shape(_cache_shape(Q, K, V, lens), Q, KP, VP)
+    _ready(O, L, Q, workspace)
+    _same(Q, O)
+    _rows(L, O.numel() // max(1, O.shape[3]))
+    ws = _cache_workspace(workspace, fa_decode_prefix_workspace_size(*shape), Q, stream)
+    _check(load_library().fa_decode_prefix(_p(Q), _p(KP), _p(VP), _p(K), _p(V), _p(lens), _p(O), _p(L), *shape, float(scale),
+                                           _dt(Q), _p(ws), ws.numel() * ws.element_size(), _current(stream)))
+
+
 def _token_rows(t):
     """(batch, token, head stride) of a [B, N, heads, d] tensor, or of a packed [T, heads, d] one (one batch); 0 where there
     is one step only (torch leaves the strides of one-sized dimensions open)."""
@@ -871,6 +942,43 @@ def _used_on(stream, *ts):
     for t in ts:
         if t is not None:
             t.record_stream(stream)
+
+
+def attention_decode_window(q, k, v, lens, window=0, sinks=0, scale=None, stream=None):
+    """O, L = fa_decode_window(...) for q [B, H, Nq, d] over caches k, v [B, Hkv, capacity, d]; outputs and workspace
+    allocated with torch."""
+    shape = _cache_shape(q, k, v, lens)
+    lib = load_library()
+    B, H, _, Nq, _, d = shape
+    dev = q.device
+    o = torch.empty((B, H, Nq, d), dtype=q.dtype, device=dev)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    nbytes = lib.fa_decode_window_workspace_size(*shape)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check(lib.fa_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), *shape,
+                                d ** -0.5 if scale is None else float(scale), int(window), int(sinks), _dt(q),
+                                ws.data_ptr(), nbytes, _current(stream)))
+    _used_on(stream, o, lse, ws)
+    return o, lse
+
+
+def attention_decode_prefix(q, k_prefix, v_prefix, k, v, lens, scale=None, stream=None):
+    """O, L = fa_decode_prefix(...) for q [B, H, Nq, d] behind a prefix k_prefix, v_prefix [Hkv, P, d] and over caches
+    k, v [B, Hkv, capacity, d]; outputs and workspace allocated with torch."""
+    shape = _prefix_shape(_cache_shape(q, k, v, lens), q, k_prefix, v_prefix)
+    lib = load_library()
+    B, H, _, Nq, _, _, d = shape
+    dev = q.device
+    o = torch.empty((B, H, Nq, d), dtype=q.dtype, device=dev)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    nbytes = lib.fa_decode_prefix_workspace_size(*shape)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check(lib.fa_decode_prefix(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                lens.data_ptr(), o.data_ptr(), lse.data_ptr(), *shape,
+                                d ** -0.5 if scale is None else float(scale), _dt(q), ws.data_ptr(), nbytes,
+                                _current(stream)))
+    _used_on(stream, o, lse, ws)
+    return o, lse
 
 
 def rope_table(positions, rotary, base=10000.0, device="cuda"):

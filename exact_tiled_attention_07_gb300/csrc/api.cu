@@ -888,6 +888,79 @@ fa_status fa_kv4_evict(const void* cache, const float* weights, const int32_t* l
   return launched(launch_kv4_evict(a), "fa_kv4_evict");
 }
 
+static fa_status check_decode_cache(int B, int H, int Hkv, int Nq, int P, int capacity, int d, bool* empty, const char* name) {
+  *empty = false;
+  if (B < 0 || H < 0 || Nq < 0 || P < 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: negative size B=%d H=%d Nq=%d P=%d", name, B, H, Nq, P);
+  if (d != 64 && d != 128 && d != 256)
+    return fail(FA_ERR_UNSUPPORTED, "%s supports d in {64, 128, 256}, got %d", name, d);
+  if (capacity < 1) return fail(FA_ERR_INVALID_ARG, "%s: capacity=%d slots: at least one", name, capacity);
+  if ((int64_t)B * H * Nq == 0) {
+    *empty = true;
+    return FA_OK;
+  }
+  const fa_status st = check_heads(H, Hkv);
+  if (st != FA_OK) return st;
+  // rows, entries and, some tiles behind the last, keys are counted in 32 bits
+  if ((double)B * H * Nq > 2.0e8 || (double)B * Hkv > 1.0e8 || capacity > INT32_MAX - 4096 || P > INT32_MAX - 4096 ||
+      (double)B * Hkv * capacity * d > 4.0e15 || (double)Hkv * P * d > 4.0e15)
+    return fail(FA_ERR_INVALID_ARG, "%s: problem too large: B=%d H=%d Hkv=%d Nq=%d P=%d capacity=%d", name, B, H, Hkv, Nq, P,
+                capacity);
+  return FA_OK;
+}
+
+static fa_status decode_cache_impl(CacheDecodeArgs* a, size_t workspace_bytes, const char* name) {
+  bool empty;
+  fa_status st = check_decode_cache(a->b, a->h, a->hkv, a->nq, a->p, a->capacity, a->d, &empty, name);
+  if (st != FA_OK) return st;
+  if (a->dtype != FA_BF16 && a->dtype != FA_FP16)
+    return fail(FA_ERR_UNSUPPORTED, "%s takes bf16 or fp16, not dtype %d", name, a->dtype);
+  if (empty) return FA_OK;
+  if ((st = check_ptrs({a->q, a->k, a->v, a->o, a->ws}, name)) != FA_OK) return st;
+  if (a->p > 0 && (st = check_ptrs({a->kp, a->vp}, name)) != FA_OK) return st;
+  if ((st = check_words({a->lens, a->lse}, name)) != FA_OK) return st;
+  if ((st = check_scale(a->scale)) != FA_OK) return st;
+  const size_t need = decode_cache_workspace_bytes(a->b, a->h, a->hkv, a->nq, a->p, a->d);
+  if (workspace_bytes < need)
+    return fail(FA_ERR_INVALID_ARG, "%s: workspace of %zu bytes < %zu required", name, workspace_bytes, need);
+  DeviceSyms syms;
+  if ((st = device_syms(&syms)) != FA_OK) return st;
+  a->err = syms.err;
+  a->counter = syms.counter;
+  return launched(launch_decode_cache(*a), name);
+}
+
+size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d) {
+  bool empty;
+  if (check_decode_cache(B, H, Hkv, Nq, 0, capacity, d, &empty, "fa_decode_window") != FA_OK || empty) return 0;
+  return decode_cache_workspace_bytes(B, H, Hkv, Nq, 0, d);
+}
+
+fa_status fa_decode_window(const void* Q, const void* K, const void* V, const int32_t* lens, void* O, float* L, int B, int H,
+                           int Hkv, int Nq, int capacity, int d, float scale, int window, int sinks, fa_dtype dtype,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (window < 0) return fail(FA_ERR_INVALID_ARG, "fa_decode_window: window must be >= 0 (0: none), got %d", window);
+  if (sinks < 0 || (sinks > 0 && window == 0))
+    return fail(FA_ERR_INVALID_ARG, "fa_decode_window: sinks=%d: >= 0, and 0 without a window", sinks);
+  CacheDecodeArgs a{Q, K, V, nullptr, nullptr, lens, O, L, workspace, B, H, Hkv, Nq, capacity, 0, d, window, sinks, scale,
+                    (int)dtype, nullptr, nullptr, static_cast<cudaStream_t>(stream)};
+  return decode_cache_impl(&a, workspace_bytes, "fa_decode_window");
+}
+
+size_t fa_decode_prefix_workspace_size(int B, int H, int Hkv, int Nq, int P, int capacity, int d) {
+  bool empty;
+  if (check_decode_cache(B, H, Hkv, Nq, P, capacity, d, &empty, "fa_decode_prefix") != FA_OK || empty) return 0;
+  return decode_cache_workspace_bytes(B, H, Hkv, Nq, P, d);
+}
+
+fa_status fa_decode_prefix(const void* Q, const void* KP, const void* VP, const void* K, const void* V, const int32_t* lens,
+                           void* O, float* L, int B, int H, int Hkv, int Nq, int P, int capacity, int d, float scale,
+                           fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  CacheDecodeArgs a{Q, K, V, KP, VP, lens, O, L, workspace, B, H, Hkv, Nq, capacity, P, d, 0, 0, scale,
+                    (int)dtype, nullptr, nullptr, static_cast<cudaStream_t>(stream)};
+  return decode_cache_impl(&a, workspace_bytes, "fa_decode_prefix");
+}
+
 // The checks of fa_qk_norm_rope and fa_qk_norm_rope_bwd. `in` and `out` hold the queries' and the keys' tensors by turns.
 static fa_status norm_rope_impl(NormRopeArgs* a, std::initializer_list<RowTensor> in, std::initializer_list<RowTensor> out,
                                 const char* name) {

@@ -277,6 +277,24 @@ struct Kv4EvictArgs {
 };
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a);
 
+// Decode over 16-bit caches of different lengths (decode_cache.cu): Q, O [b][h][nq][d], K, V [b][hkv][capacity][d], L [b][h][nq],
+// lens [b] on the device; window > 0: a sliding window with sinks; p > 0: a prefix KP, VP [hkv][p][d] that all rows see.
+struct CacheDecodeArgs {
+  const void *q, *k, *v, *kp, *vp;
+  const int32_t* lens;
+  void* o;
+  float* lse;
+  void* ws;
+  int b, h, hkv, nq, capacity, p, d, window, sinks;
+  float scale;
+  int dtype;
+  unsigned long long* err;
+  unsigned long long* counter;
+  cudaStream_t stream;
+};
+size_t decode_cache_workspace_bytes(int b, int h, int hkv, int nq, int p, int d);
+cudaError_t launch_decode_cache(const CacheDecodeArgs& a);
+
 // Norms of query and key heads with the rotation by position (norm_rope.cu): element strides of [b][n][heads][d] tensors
 // whose rows are contiguous.
 struct NormRopeStrides {

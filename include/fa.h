@@ -416,6 +416,35 @@ FA_API fa_status fa_kv4_evict(const void* cache, const float* weights, const int
                               int capacity, int out_capacity, int d, void* stream);
 
 /*
+ * Decode attention over 16-bit key/value caches of sequences of different lengths (fa_decode with lengths), with a sliding
+ * window and sinks, or behind a prefix that all sequences share.
+ *   Q, O      [B][H][Nq][d] dtype (bf16 or fp16), the new query rows; L [B][H][Nq] fp32
+ *   K, V      [B][Hkv][capacity][d] dtype, the caches; capacity >= 1
+ *   lens      device int32 [B]: slots in use, [0, lens[b]) of sequence b, those of the Nq new rows among them: row i
+ *             sees slots [0, hi) with hi = lens[b] - Nq + i + 1 (nothing where that is not above 0). The caller owns lens; a
+ *             length outside [0, capacity] is clamped to it and recorded as a device error. Slots from lens[b] on are not
+ *             looked at (they may hold NaN).
+ *   window    (fa_decode_window) > 0: row i sees slots [hi - window, hi) and the first `sinks` below hi; slots in front of
+ *             every row's window and behind the sinks are not read. 0: no window, and sinks must be 0.
+ *   KP, VP    (fa_decode_prefix) [Hkv][P][d] dtype: keys and values of the P >= 0 tokens that stand in front of every
+ *             sequence; each row sees all of them. They are read once for up to 128 rows of all sequences.
+ *   d         64, 128 or 256; H a positive multiple of Hkv, query head h reads key/value head h / (H / Hkv).
+ * A row that sees nothing gets O = 0, L = -inf. (A slot that some of a call's Nq rows see and others do not has weight 0 for the
+ * others: what is not finite in its V reaches them, as in fa_fwd.) Probabilities are rounded to dtype before they
+ * meet V, sums are in 32 bits. The lengths are read on the device: one captured graph serves any. Results do not depend on
+ * timing. Two launches; the workspace takes ..._workspace_size(...) bytes for the same arguments, its contents on entry do not
+ * matter, and calls that may overlap on the GPU need workspaces of their own.
+ */
+FA_API size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d);
+FA_API fa_status fa_decode_window(const void* Q, const void* K, const void* V, const int32_t* lens, void* O, float* L, int B,
+                                  int H, int Hkv, int Nq, int capacity, int d, float scale, int window, int sinks,
+                                  fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+FA_API size_t fa_decode_prefix_workspace_size(int B, int H, int Hkv, int Nq, int P, int capacity, int d);
+FA_API fa_status fa_decode_prefix(const void* Q, const void* KP, const void* VP, const void* K, const void* V,
+                                  const int32_t* lens, void* O, float* L, int B, int H, int Hkv, int Nq, int P, int capacity,
+                                  int d, float scale, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Norms of queries and keys for each head, with the rotation by position in the same pass (what a model does to a
  * projection's output before attention), and its gradients.
  *   Q, K      [B][N][H][d] and [B][N][Hkv][d] dtype (bf16, fp16 or fp32), rows of d contiguous elements; either may have no

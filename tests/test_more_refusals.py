@@ -178,3 +178,47 @@ def test_binding_keeps_sinks_to_causal_windows():
     for causal, window, mask in ((False, 5, None), (True, 0, None), (True, 5, object())):
         with pytest.raises(ValueError, match="sinks go with"):
             fa._sinks_allowed(causal, window, 3, mask)
+
+
+# ------------------------------------------------------------------------------------------------ decode over caches
+
+
+def decode_window(lib, B=2, H=4, Hkv=2, Nq=1, C=100, d=64, scale=0.125, window=10, sinks=2, dtype=BF16, ptrs=P[:6], ws=P[6],
+                  size=1 << 50):
+    return lib.fa_decode_window(*ptrs, B, H, Hkv, Nq, C, d, scale, window, sinks, dtype, ws, size, None)
+
+
+def decode_prefix(lib, B=2, H=4, Hkv=2, Nq=1, C=100, d=64, scale=0.125, dtype=BF16, ptrs=P[:8], ws=P[8], size=1 << 50, Pn=50):
+    return lib.fa_decode_prefix(*ptrs, B, H, Hkv, Nq, Pn, C, d, scale, dtype, ws, size, None)
+
+
+@pytest.mark.parametrize("call,n,words", [(decode_window, 6, (3, 5)), (decode_prefix, 8, (5, 7))])
+def test_decode_arguments(lib, call, n, words):
+    for bad in ({"B": -1}, {"H": -2}, {"Nq": -1}):
+        assert call(lib, **bad) == INVALID and "negative" in message(lib)
+    assert call(lib, C=0) == INVALID and "capacity" in message(lib)
+    assert call(lib, H=3) == INVALID and call(lib, Hkv=0) == INVALID
+    assert call(lib, d=96) == UNSUPPORTED and call(lib, dtype=FP32) == UNSUPPORTED
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(lib, scale=scale) == INVALID and "scale" in message(lib)
+    for big in ({"C": 2 ** 31 - 100}, {"B": 2 ** 20, "Nq": 2 ** 10}, {"B": 2 ** 28, "Hkv": 4, "Nq": 1}):
+        assert call(lib, **big) == INVALID and "too large" in message(lib)
+    for i in range(n):
+        assert call(lib, ptrs=[None if j == i else P[j] for j in range(n)]) == INVALID and "null" in message(lib)
+        off = 2 if i in words else 8
+        assert call(lib, ptrs=[P[j] + (off if j == i else 0) for j in range(n)]) == INVALID and "aligned" in message(lib)
+    assert call(lib, ws=None) == INVALID and "null" in message(lib)
+    assert call(lib, size=100) == INVALID and "workspace" in message(lib)
+    for nothing in ({"B": 0}, {"H": 0}, {"Nq": 0}):
+        assert call(lib, ptrs=[None] * n, ws=None, size=0, **nothing) == OK
+    assert lib.fa_decode_window_workspace_size(2, 4, 2, 1, 100, 64) > 0
+    assert lib.fa_decode_prefix_workspace_size(2, 4, 2, 1, 50, 100, 64) > lib.fa_decode_window_workspace_size(2, 4, 2, 1, 100, 64)
+    assert lib.fa_decode_window_workspace_size(2, 3, 2, 1, 100, 64) == 0
+
+
+def test_decode_window_and_prefix_sizes(lib):
+    assert decode_window(lib, window=-1) == INVALID and "window" in message(lib)
+    assert decode_window(lib, sinks=-1) == INVALID and "sinks" in message(lib)
+    assert decode_window(lib, window=0, sinks=1) == INVALID and "sinks" in message(lib)
+    assert decode_prefix(lib, Pn=-1) == INVALID and "negative" in message(lib)
+    assert decode_prefix(lib, Pn=2 ** 31 - 1) == INVALID and "too large" in message(lib)
