@@ -46,7 +46,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kLoadRows = 16;   // rows of the loads that end a tile early
 constexpr int kSegCost = 2;     // what a segment's start and end cost, in tiles
 constexpr int kSegs = 4;        // published segments, and row statistics, in flight
-constexpr int kFinishThreads = 256;
+constexpr int kFinishThreads = 128;
+constexpr int kMostSlots = 1024;  // segments that a row has in the prefix, at most (pieces + CTAs)
+constexpr int kMostCtas = 512;
+constexpr int kFewSequences = 512;
+constexpr int kDrainBarrier = 1;  // named barrier of the four drain warps
 
 template <int D>
 struct CacheCfg {
@@ -67,7 +71,10 @@ struct CacheCfg {
   static constexpr int OFF_SEG = OFF_BAR + NBAR * 8 + 16;  // [kSegs] Seg
   static constexpr int OFF_STAT = OFF_SEG + kSegs * 64;    // [kSegs][128] (m, l)
   static constexpr int OFF_RED = OFF_STAT + kSegs * BM * 8;
-  static constexpr int SMEM = OFF_RED + 16 * 8;
+  // copies of rows meet here, 32 columns at a time (rows of 36 floats: no two of a quarter warp in one bank)
+  static constexpr int XROW = 36;
+  static constexpr int OFF_X = (OFF_RED + 16 * 8 + 15) & ~15;
+  static constexpr int SMEM = OFF_X + (D == 256 ? 0 : BM * (XROW + 1) * 4);  // and the weights of copies
   static_assert(STAGES >= 4, "the products run two tiles ahead");
   static_assert(SMEM <= 232448 && OFF_SEG % 8 == 0 && OFF_STAT % 8 == 0 && OFF_RED % 8 == 0, "shared memory");
 };
@@ -82,6 +89,7 @@ struct Seg {
   int ns, sk;   // its first ns tiles hold the sinks, keys [0, sk)
   int lo, end;  // the others keys [lo, end)
   int slot;     // of the partial results
+  int whole;    // all there is for its rows: O and L are final
 };
 static_assert(sizeof(Seg) <= 64, "Seg");
 
@@ -112,24 +120,54 @@ struct List {
   __device__ int len_of(int s) const { return min(max(lens[s], 0), capacity); }
   __host__ __device__ static int64_t cost(int tiles) { return tiles > 0 ? tiles + kSegCost : 0; }
   __host__ __device__ int prefix_tiles() const { return (int)(((int64_t)p + bn - 1) / bn); }
-  __host__ __device__ int prefix_entries() const { return p > 0 ? hkv * rt_pre : 0; }
-  __host__ __device__ int64_t prefix_total() const { return prefix_entries() * cost(prefix_tiles()); }
   __device__ int64_t own_total(int s) const { return (int64_t)hkv * rt_own * cost(keys(len_of(s)).tiles); }
 };
+
+// The prefix' entries: (key/value head, piece of the keys, row tile), pieces of `piece` tiles.  One piece where a head has one row
+// tile; with several, pieces as long as a CTA's run: neighbouring CTAs then read the same keys for different rows at the
+// same time, and L2 hands out what HBM was read for once (without pieces eight row tiles read a prefix of 134 MB seven
+// times from HBM).  A run is at least as long as all the prefix' tiles by all CTAs, so there are not more than 4/3 grid + hkv
+// rt_pre entries.
+struct Prefix {
+  int tiles, piece, pieces, entries;
+  __device__ void set(const List& list, int64_t own, int grid) {
+    tiles = piece = list.prefix_tiles();
+    pieces = entries = 0;
+    if (tiles == 0) return;
+    if (list.rt_pre > 1) {
+      const int64_t run = (own + (int64_t)list.hkv * list.rt_pre * tiles + grid - 1) / grid;
+      const int n = max(1, (int)((tiles + run / 2) / run));
+      piece = (tiles + n - 1) / n;  // (two or more: at least 3/4 of a run)
+    }
+    pieces = (tiles + piece - 1) / piece;
+    entries = list.hkv * pieces * list.rt_pre;
+  }
+  __device__ int64_t cost() const { return piece + kSegCost; }
+  __device__ int64_t total() const { return entries * cost(); }
+  __device__ int tiles_of(int x) const { return min(piece, tiles - x * piece); }
+};
 // CTA c of n takes [start(c), start(c + 1)) of a list.
-__device__ __forceinline__ int64_t run_start(int64_t total, int c, int n) { return total * c / n; }
-__device__ __forceinline__ int run_of(int64_t total, int64_t at, int n) { return (int)(((at + 1) * n - 1) / total); }
+// (A division of 64 bits takes a hundred instructions, of 32 bits a fifth of that.)
+__device__ __forceinline__ int64_t run_start(int64_t total, int c, int n) {
+  const int64_t x = total * c;
+  return x < INT32_MAX ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
+}
+__device__ __forceinline__ int run_of(int64_t total, int64_t at, int n) {
+  const int64_t x = (at + 1) * n - 1;
+  return x < INT32_MAX ? (int)((uint32_t)x / (uint32_t)total) : (int)(x / total);
+}
 __device__ __forceinline__ int runs_of(int64_t total, int grid) { return total < grid ? (int)total : grid; }
 
-// Partial results: for the prefix' segments, then the caches', [slots][D / 4][lanes] float4 and [slots][lanes] (m, l); then the
-// lists' offset of each sequence.  A lane is a row, or one of a row's copies.
+// Partial results: for the prefix' segments, then the caches', [slots][D / 4][lanes] float4 and [slots][lanes] (m, l), a lane for
+// each row; then the lists' offset of each sequence.
 struct Partials {
   float4 *pre_o, *own_o;
   float2 *pre_ml, *own_ml;
-  int64_t* offsets;  // [b + 1]: of each sequence's first entry, then the total
+  int64_t* offsets;  // [b + 2]: of each sequence's first entry, then the total, and the caches' part of it
   int pre_lanes, own_lanes;
 };
 
+int cache_grid() { return std::min(kMostCtas, device_sm_count()); }
 int row_copies(int d, int64_t rows) { return d == 256 || rows > 64 ? 1 : (rows > 32 ? 2 : 4); }
 
 struct Shape {  // of a launch
@@ -142,14 +180,14 @@ struct Shape {  // of a launch
     rt_pre = p > 0 ? (int)((all + BM - 1) / BM) : 0;
     r_own = row_copies(d, gn);
     r_pre = row_copies(d, all);
-    own_lanes = r_own * std::min(gn, BM);
-    pre_lanes = r_pre * (int)std::min<int64_t>(all, BM);
-    pre_slots = p > 0 ? (int64_t)hkv * rt_pre + grid : 0;
+    own_lanes = std::min(gn, BM);
+    pre_lanes = (int)std::min<int64_t>(all, BM);
+    pre_slots = p > 0 ? (int64_t)hkv * rt_pre + 3 * grid : 0;
     own_slots = (int64_t)b * hkv * rt_own + grid;
   }
   size_t bytes(int b, int d) const {
     const size_t lanes = (size_t)pre_slots * pre_lanes + (size_t)own_slots * own_lanes;
-    return lanes * ((size_t)d * 4 + 8) + ((size_t)b + 2) * 8 + 64;
+    return lanes * ((size_t)d * 4 + 8) + ((size_t)b + 2) * 8;
   }
   Partials carve(void* ws, int d) const {
     Partials w;
@@ -171,9 +209,11 @@ struct Shape {  // of a launch
 
 struct CacheParams {
   const void* q;
+  void* o;
+  float* lse;
   List list;
   Partials ws;
-  int h, gn;
+  int gn;
   int r_own, r_pre;  // copies of a row
   float scale_log2;
   unsigned long long* err;
@@ -278,6 +318,16 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
   const ErrCtx ctx{a.err, abort_flag};
 
   asm volatile("griddepcontrol.launch_dependents;");
+  if (warp == C::PRODUCER_WARP && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_k16);
+    tma_prefetch_desc(&tm_v16);
+    if (list.p > 0) {
+      tma_prefetch_desc(&tm_kp);
+      tma_prefetch_desc(&tm_vp);
+    }
+  }
   if (threadIdx.x == 0) {
     if ((smem_u32(smem) & 1023u) != 0) report_error(a.err, DERR_BAD_SMEM_ALIGN, 400);
     *abort_flag = (smem_u32(smem) & 1023u) != 0;
@@ -316,11 +366,14 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int64_t total = list.prefix_total();
+  int64_t own_all = 0;
 #pragma unroll
-  for (int w = 0; w < C::THREADS / 32; ++w) total += red[w];
+  for (int w = 0; w < C::THREADS / 32; ++w) own_all += red[w];
+  Prefix pre;
+  pre.set(list, own_all, gridDim.x);
+  const int64_t pre_total = pre.total(), total = pre_total + own_all;
   if (blockIdx.x == 0 && warp == C::DRAIN_WARP0) {
-    int64_t at = list.prefix_total();
+    int64_t at = pre_total;
     for (int s0 = 0; s0 < list.b; s0 += 32) {
       int64_t v = s0 + lane < list.b ? list.own_total(s0 + lane) : 0;
       const int64_t mine = v;
@@ -331,7 +384,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
       if (s0 + lane < list.b) a.ws.offsets[s0 + lane] = at + v - mine;
       at += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) a.ws.offsets[list.b] = total;
+    if (lane == 0) a.ws.offsets[list.b] = total, a.ws.offsets[list.b + 1] = own_all;
     __syncwarp();
   }
   const uint32_t tbase = *tmem_slot;
@@ -363,31 +416,27 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
     // ------------------------------------------------------------------ producer
     if (start_ok) {
       const int64_t u0 = run_start(total, blockIdx.x, runs), u1 = run_start(total, blockIdx.x + 1, runs);
-      const int64_t pre_total = list.prefix_total();
-      // the sequence that the run begins in (the whole warp), and its offset
+      // the sequence that the run begins in, or the first one behind the prefix (the whole warp), and its offset
       int b = 0;
       int64_t b_off = pre_total;
-      if (u1 > pre_total) {
-        const int64_t from = max(u0, pre_total);
-        for (int s0 = 0; s0 < list.b; s0 += 32) {
-          int64_t v = s0 + lane < list.b ? list.own_total(s0 + lane) : 0;
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += x;
-          }
-          const unsigned past = __ballot_sync(0xffffffffu, b_off + v > from);
-          if (past) {
-            const int f = __ffs(past) - 1;
-            b = s0 + f;
-            if (f > 0) b_off += __shfl_sync(0xffffffffu, v, f - 1);
-            break;
-          }
-          b_off += __shfl_sync(0xffffffffu, v, 31);
+      const int64_t from = max(u0, pre_total);
+      for (int s0 = 0; s0 < list.b && u1 > pre_total; s0 += 32) {
+        int64_t v = s0 + lane < list.b ? list.own_total(s0 + lane) : 0;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += x;
         }
+        const unsigned past = __ballot_sync(0xffffffffu, b_off + v > from);
+        if (past) {
+          const int f = __ffs(past) - 1;
+          b = s0 + f;
+          const int64_t before = __shfl_sync(0xffffffffu, v, f > 0 ? f - 1 : 0);
+          if (f > 0) b_off += before;
+          break;
+        }
+        b_off += __shfl_sync(0xffffffffu, v, 31);
       }
       if (lane == 0) {
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
         int n_segs = 0;
         uint32_t pos = 0;  // loads issued
         bool ok = true;
@@ -395,65 +444,66 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
           const int at = n_segs % kSegs;
           if (n_segs >= kSegs && !mbar_wait(seg_empty + at, (uint32_t)(n_segs / kSegs - 1) & 1, ctx, 411)) return false;
           volatile int* to = reinterpret_cast<volatile int*>(segs + at);
-          const int* from = reinterpret_cast<const int*>(&g);
+          const int* from_ = reinterpret_cast<const int*>(&g);
 #pragma unroll
-          for (int i = 0; i < (int)(sizeof(Seg) / 4); ++i) to[i] = from[i];
+          for (int i = 0; i < (int)(sizeof(Seg) / 4); ++i) to[i] = from_[i];
           mbar_arrive(seg_full + at);
           ++n_segs;
           return true;
         };
-        int64_t u = u0;
-        List::Keys keys = list.keys(b < list.b ? list.len_of(b) : 0);
-        while (ok && u < u1) {
-          // the entry at u: its offset, tiles and rows
-          Seg g;
-          int64_t off;
-          int tiles;
-          if (u < pre_total) {
-            const int64_t c = List::cost(list.prefix_tiles());
-            const int e = (int)(u / c);
-            off = e * c;
-            tiles = list.prefix_tiles();
-            g.prefix = 1;
-            g.kvh = e / list.rt_pre;
-            g.rt = e - g.kvh * list.rt_pre;
-            g.b = 0;
-            g.head = g.kvh;
-            g.rows = min(BM, list.b * a.gn - g.rt * BM);
-            g.ns = g.sk = g.lo = 0;
-            g.end = list.p;
-            g.slot = e + (int)blockIdx.x;
-          } else {
-            const int entries = list.hkv * list.rt_own;
-            while (b < list.b && u >= b_off + entries * List::cost(keys.tiles)) {
-              b_off += entries * List::cost(keys.tiles);
-              ++b;
-              keys = list.keys(b < list.b ? list.len_of(b) : 0);
-            }
-            if (b >= list.b) break;
-            const int64_t c = List::cost(keys.tiles);
-            const int e = (int)((u - b_off) / c);
-            off = b_off + e * c;
-            tiles = keys.tiles;
-            g.prefix = 0;
-            g.b = b;
-            g.kvh = e / list.rt_own;
-            g.rt = e - g.kvh * list.rt_own;
-            g.head = b * list.hkv + g.kvh;
-            g.rows = min(BM, a.gn - g.rt * BM);
-            g.ns = keys.ns;
-            g.sk = keys.sk;
-            g.lo = keys.lo;
-            g.end = keys.len;
-            g.slot = b * entries + e + (int)blockIdx.x;
-          }
+        // the entry at u0, then one after the other
+        Seg g;
+        int tiles, len_next = 0;
+        int64_t off;
+        List::Keys keys{};
+        auto begin_own = [&](int entry) {  // entry of sequence b
+          g.prefix = 0;
+          g.b = b;
+          g.kvh = entry / list.rt_own;
+          g.rt = entry - g.kvh * list.rt_own;
+          g.ns = keys.ns;
+          g.sk = keys.sk;
+          g.lo = keys.lo;
+          g.end = keys.len;
+          tiles = keys.tiles;
+        };
+        auto next_len = [&]() { len_next = b + 1 < list.b ? list.lens[b + 1] : 0; };
+        int piece = 0;  // of the prefix' keys
+        auto begin_pre = [&]() {
+          g.lo = piece * pre.piece * BN;
+          tiles = pre.tiles_of(piece);
+          g.end = min(list.p, g.lo + tiles * BN);
+        };
+        if (u0 < pre_total) {
+          const int c = (int)pre.cost();
+          const int e = u0 < INT32_MAX ? (int)((uint32_t)u0 / (uint32_t)c) : (int)(u0 / c);
+          off = (int64_t)e * c;
+          g.prefix = 1;
+          g.b = 0;
+          g.kvh = e / (pre.pieces * list.rt_pre);
+          piece = e / list.rt_pre - g.kvh * pre.pieces;
+          g.rt = e % list.rt_pre;
+          g.ns = g.sk = 0;
+          begin_pre();
+          if (u1 > pre_total) keys = list.keys(list.len_of(b));
+        } else {
+          keys = list.keys(list.len_of(b));
+          const int64_t c = List::cost(keys.tiles), in = u0 - b_off;
+          const int e = in < INT32_MAX ? (int)((uint32_t)in / (uint32_t)c) : (int)(in / c);
+          off = b_off + e * c;
+          begin_own(e);
+        }
+        next_len();
+        while (ok) {
+          g.head = g.prefix ? g.kvh : g.b * list.hkv + g.kvh;
+          g.rows = min(BM, (g.prefix ? list.b * a.gn : a.gn) - g.rt * BM);
+          g.slot = (g.prefix ? (g.kvh * pre.pieces + piece) * list.rt_pre : g.head * list.rt_own) + g.rt + (int)blockIdx.x;
           // its tiles in this run
-          g.t0 = (int)max((int64_t)0, u - off - kSegCost);
+          g.t0 = (int)max((int64_t)0, u0 - off - kSegCost);
           const int t1 = (int)min((int64_t)tiles, u1 - off - kSegCost);
           g.nt = t1 - g.t0;
-          u = min(u1, off + tiles + kSegCost);
-          if (g.nt <= 0) continue;
-          if (!(ok = publish(g))) break;
+          g.whole = list.p == 0 && g.nt == tiles;
+          if (g.nt > 0 && !(ok = publish(g))) break;
           for (int t = g.t0; ok && t < t1; ++t) {
             int n;
             const int base = tile_keys(g, t, &n);
@@ -481,7 +531,35 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
                                 base + x * kLoadRows, g.head);
               }
             }
+            // behind the run's first tile: the first rows of Q go before the flood of all CTAs' loads, in which they took 5 us.  (No
+            // other segment is published yet, so this phase of the barrier is the current or the last one.)
+            if (ok && pos == 2) ok = mbar_wait(q_full, 0, ctx, 414);
           }
+          // the next entry
+          off += g.prefix ? pre.cost() : tiles + kSegCost;
+          if (off >= u1) break;
+          if (++g.rt < (g.prefix ? list.rt_pre : list.rt_own)) continue;
+          g.rt = 0;
+          if (g.prefix) {
+            if (++piece == pre.pieces) {
+              piece = 0;
+              if (++g.kvh == list.hkv) {  // the sequences follow (b is the first one with something in its cache)
+                begin_own(0);
+                continue;
+              }
+            }
+            begin_pre();
+            continue;
+          }
+          if (++g.kvh < list.hkv) continue;
+          do {
+            ++b;
+            if (b >= list.b) break;
+            keys = list.keys(min(max(len_next, 0), list.capacity));
+            next_len();
+          } while (keys.tiles == 0);
+          if (b >= list.b) break;
+          begin_own(0);
         }
         Seg none{};
         if (ok) publish(none);
@@ -518,6 +596,10 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
         while (ok && g.rows > 0 && g_qk < g_pv + 2) {
           // (one Q buffer: the next segment's Q arrives when the last one's O is final)
           if (C::QBUFS == 1 && t == 0 && g_qk > g_pv) break;
+          // (with two it may be on its way still: the P V of what is there does not wait for it)
+          if (C::QBUFS == 2 && t == 0 && g_qk > g_pv &&
+              !__all_sync(0xffffffffu, mbar_test_wait(q_full + (sq & 1), (uint32_t)(sq >> 1) & 1)))
+            break;
           const uint32_t pos = 2 * g_qk, slot = pos % C::STAGES;
           const int qb = C::QBUFS == 2 ? (sq & 1) : 0;
           if (t == 0 && !(ok = wait(q_full + qb, (uint32_t)(sq / C::QBUFS) & 1, 420))) break;
@@ -553,10 +635,11 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
         const int first = i ? first_[1] : first_[0], last = i ? last_[1] : last_[0], n = i ? keys_[1] : keys_[0];
         const uint32_t pos = 2 * g_pv + 1, slot = pos % C::STAGES;
         if (!(ok = wait(kv_full + slot, (pos / C::STAGES) & 1, 422))) break;
-        if (n < BN) {
+        const int steps = (n + 15) / 16;  // of 16 keys
+        if (n < steps * 16) {
           // V rows behind the segment's keys (another sequence's, or what the place held before): zero, since 0 x NaN is NaN
           uint8_t* vt = smem + slot * C::TILE_BYTES;
-          for (int x = n * 8 + lane; x < BN * 8; x += 32)
+          for (int x = n * 8 + lane; x < steps * 128; x += 32)
 #pragma unroll
             for (int kb = 0; kb < C::KB; ++kb)
               *reinterpret_cast<uint4*>(vt + kb * (BN * 128) + x * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -574,7 +657,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            umma_ts(tbase + C::O_COL, tbase + p_col + kk * 8, bd[kk], idesc_pv, (first < 0 || kk > 0) ? 1u : 0u);
+            if (kk < steps) umma_ts(tbase + C::O_COL, tbase + p_col + kk * 8, bd[kk], idesc_pv, (first < 0 || kk > 0) ? 1u : 0u);
           umma_commit(pv_done);
           umma_commit(kv_empty + slot);
           if (last) umma_commit(o_full);
@@ -670,73 +753,145 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
                                    : ((int64_t)g.b * list.hkv + g.kvh) * a.gn + r;
       const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row * D);
       const uint32_t q_col = C::Q_COL + (C::QBUFS == 2 ? (s & 1) : 0) * (D / 2);
+      constexpr int BLOCKS = D == 64 ? 1 : 2;  // 64-column blocks whose loads are in flight together
 #pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t w[32];
+      for (int c = 0; c < D / 64; c += BLOCKS) {
+        uint32_t x[BLOCKS][32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 u = rit < g.rows ? from[c * 8 + i] : make_uint4(0u, 0u, 0u, 0u);
-          w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-        }
-        tmem_st32(tmem_addr(tbase, lane_base, q_col + c * 32), w);
+        for (int k = 0; k < BLOCKS; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 u = rit < g.rows ? from[(c + k) * 8 + i] : make_uint4(0u, 0u, 0u, 0u);
+            x[k][4 * i] = u.x, x[k][4 * i + 1] = u.y, x[k][4 * i + 2] = u.z, x[k][4 * i + 3] = u.w;
+          }
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) tmem_st32(tmem_addr(tbase, lane_base, q_col + (c + k) * 32), x[k]);
       }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(q_full + (C::QBUFS == 2 ? (s & 1) : 0));
     };
-    if (ok) {
-      Seg g = read_seg(0, ok);
-      if (g.rows > 0) load_q(g, 0);
-      for (int s = 0; ok && g.rows > 0; ++s) {
-        // (with two Q buffers the S that read this one are those of the segment before, whose O was final)
-        Seg next{};
-        if (C::QBUFS == 2) {
-          next = read_seg(s + 1, ok);
-          if (ok && next.rows > 0) load_q(next, s + 1);
-        }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(o_full, s & 1, ctx, 440));
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(stat_full + s % kSegs, (uint32_t)(s / kSegs) & 1, ctx, 441));
-        if (!ok) break;
-        tc_fence_after();
-        int cp, rit;
-        const int R = g.prefix ? a.r_pre : a.r_own;
-        lane_row(R, quarter, lane, &cp, &rit);
-        const float2 ml = stats[(s % kSegs) * BM + quarter * 32 + lane];
-        const int lanes = g.prefix ? a.ws.pre_lanes : a.ws.own_lanes;
-        const int to = cp * (lanes / R) + rit;
-        const bool mine = rit < g.rows;
-        const bool any = (quarter % (4 / R)) * 32 < g.rows;
-        float4* out = (g.prefix ? a.ws.pre_o : a.ws.own_o) + (int64_t)g.slot * (D / 4) * lanes + to;
-        constexpr int HALF = D == 256 ? 128 : D;  // columns held in registers at a time
+    // O of segment s out of TMEM; false when a wait ran out
+    auto store_o = [&](const Seg& g, int s) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(o_full, s & 1, ctx, 440));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(stat_full + s % kSegs, (uint32_t)(s / kSegs) & 1, ctx, 441));
+      if (!(ok = named_bar_and(kDrainBarrier, 128, ok))) return false;
+      tc_fence_after();
+      int cp, rit;
+      const int R = g.prefix ? a.r_pre : a.r_own;
+      lane_row(R, quarter, lane, &cp, &rit);
+      const float2* stat = stats + (s % kSegs) * BM;
+      float2 ml = stat[quarter * 32 + lane];
+      const int lanes = g.prefix ? a.ws.pre_lanes : a.ws.own_lanes;
+      const bool mine = rit < g.rows;
+      float4* out = (g.prefix ? a.ws.pre_o : a.ws.own_o) + (int64_t)g.slot * (D / 4) * lanes;
+      const int64_t row0 = ((int64_t)g.b * list.hkv + g.kvh) * a.gn + g.rt * BM;  // (whole) of O
+      uint16_t* final_o = static_cast<uint16_t*>(a.o) + row0 * D;
+      // the copies of a row joined: their common maximum and sum, this copy's weight
+      float f = 1.f;
+      float* weight = reinterpret_cast<float*>(smem + C::OFF_X) + BM * C::XROW;  // [copy][row]
+      if (R > 1) {
+        float2 c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = k < R ? stat[k * (BM / R) + rit] : make_float2(-INFINITY, 0.f);
+        const float M = fmaxf(fmaxf(c[0].x, c[1].x), fmaxf(c[2].x, c[3].x));
+        float l = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l += c[k].x == -INFINITY ? c[k].y : ex2(c[k].x - M) * c[k].y;  // (NaN scores: m = -inf, l = NaN)
+        f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
+        ml = make_float2(M, l);
+      }
+      if (g.whole && !(ml.y == 0.f)) f *= 1.f / ml.y;
+      float* xs = reinterpret_cast<float*>(smem + C::OFF_X);
+      const int copies = R * g.rows;  // rows of the exchange, which takes 128 of 32 columns: 128 / copies pieces of the rows at a time
+      const int pieces = R == 1 ? D / 32 : BM / copies;
 #pragma unroll 1
-        for (int h = 0; h < D / HALF; ++h) {
-          uint32_t r[HALF / 32][32];
-          if (any) {
+      for (int c = 0, at = 0; c < D / 32; ++c) {
+        if (R > 1 && at == 0) named_bar_sync(kDrainBarrier, 128);  // what was exchanged before has been read
+        uint32_t r[32];
+        tmem_ld32(tmem_addr(tbase, lane_base, C::O_COL + c * 32), r);
+        tmem_wait_ld();
+        reg_fence(r);
+        if (c == D / 32 - 1) {  // all of O is in registers or gone: the next segment may overwrite it
+          tc_fence_before();
+          mbar_arrive(o_empty);
+        }
+        if (R == 1) {
+          if (mine && g.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(final_o + rit * D + c * 32);
 #pragma unroll
-            for (int c = 0; c < HALF / 32; ++c) tmem_ld32(tmem_addr(tbase, lane_base, C::O_COL + h * HALF + c * 32), r[c]);
-            tmem_wait_ld();
+            for (int i = 0; i < 4; ++i) {
+              uint32_t pk[4];
 #pragma unroll
-            for (int c = 0; c < HALF / 32; ++c) reg_fence(r[c]);
+              for (int k = 0; k < 4; ++k)
+                pk[k] = pack2<BF16>(__uint_as_float(r[8 * i + 2 * k]) * f, __uint_as_float(r[8 * i + 2 * k + 1]) * f);
+              dst[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          } else if (mine) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              out[(c * 8 + i) * lanes + rit] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                                           __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
           }
-          if (h == D / HALF - 1) {  // O is in registers: the next segment may overwrite it
-            tc_fence_before();
-            mbar_arrive(o_empty);
-          }
+        } else if constexpr (D < 256) {
           if (mine) {
+            float4* to = reinterpret_cast<float4*>(xs + (at * copies + cp * g.rows + rit) * C::XROW);
 #pragma unroll
-            for (int c = 0; c < HALF / 4; ++c)
-              out[(int64_t)(h * (HALF / 4) + c) * lanes] =
-                  make_float4(__uint_as_float(r[c / 8][c % 8 * 4]), __uint_as_float(r[c / 8][c % 8 * 4 + 1]),
-                              __uint_as_float(r[c / 8][c % 8 * 4 + 2]), __uint_as_float(r[c / 8][c % 8 * 4 + 3]));
+            for (int i = 0; i < 8; ++i)
+              to[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]),
+                                  __uint_as_float(r[4 * i + 3]));
+            if (at == 0) weight[cp * g.rows + rit] = f;
           }
+          if (++at < pieces && c < D / 32 - 1) continue;
+          named_bar_sync(kDrainBarrier, 128);
+          const int first = c + 1 - at;
+#pragma unroll 1
+          for (int e = quarter * 32 + lane; e < g.rows * 8 * at; e += 128) {
+            const int i = e & 7, pr = e >> 3, piece = pr / g.rows, row = pr - piece * g.rows;
+            const float* from = xs + (piece * copies + row) * C::XROW + 4 * i;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k < R) {
+                const float fk = weight[k * g.rows + row];
+                const float4 x = *reinterpret_cast<const float4*>(from + k * g.rows * C::XROW);
+                if (fk != 0.f)  // (not a copy that saw nothing)
+                  sum.x = fmaf(fk, x.x, sum.x), sum.y = fmaf(fk, x.y, sum.y), sum.z = fmaf(fk, x.z, sum.z), sum.w = fmaf(fk, x.w, sum.w);
+              }
+            }
+            const int col = (first + piece) * 8 + i;
+            if (g.whole)
+              *reinterpret_cast<uint2*>(final_o + row * D + 4 * col) = make_uint2(pack2<BF16>(sum.x, sum.y), pack2<BF16>(sum.z, sum.w));
+            else
+              out[col * lanes + row] = sum;
+          }
+          at = 0;
         }
-        if (mine) (g.prefix ? a.ws.pre_ml : a.ws.own_ml)[(int64_t)g.slot * lanes + to] = ml;
-        if (a.counter && quarter == 0 && lane == 0) atomicAdd(a.counter, (unsigned long long)g.nt);
-        if (C::QBUFS == 1) {
-          next = read_seg(s + 1, ok);
-          if (ok && next.rows > 0) load_q(next, s + 1);
-        }
-        g = next;
+      }
+      if (mine && cp == 0) {
+        if (g.whole) a.lse[row0 + rit] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+        else (g.prefix ? a.ws.pre_ml : a.ws.own_ml)[(int64_t)g.slot * lanes + rit] = ml;
+      }
+      if (a.counter && quarter == 0 && lane == 0) atomicAdd(a.counter, (unsigned long long)g.nt);
+      return true;
+    };
+    // The four warps meet at named barriers, which no limit of time ends: whether there is a segment, and whether its O came,
+    // they decide together (a reducing barrier), and between that and their last barrier nothing waits for anything else.
+    // (What runs once a segment is kept short: its instructions come from L2 or memory, and unrolled over all columns they
+    // cost more than a short segment.)
+    Seg g{}, next{};  // the segment whose O is due, the one behind it
+    auto advance = [&](int s) {
+      next = read_seg(s, ok);
+      if (ok && next.rows > 0) load_q(next, s);
+    };
+    for (int s = -1; start_ok; ++s, g = next) {
+      if (s >= 0 && !named_bar_and(kDrainBarrier, 128, ok && g.rows > 0)) break;
+      if constexpr (C::QBUFS == 2) {  // the S that read this Q buffer are those of the segment before, whose O was final
+        advance(s + 1);
+        if (s >= 0 && !store_o(g, s)) break;
+      } else {
+        if (s >= 0 && !store_o(g, s)) break;
+        advance(s + 1);
       }
     }
   }
@@ -748,133 +903,186 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
   }
 }
 
-// Joins the segments of each row: O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s, L = (M + log2 of the latter) ln 2, in the list's
-// order.  A warp takes a row; a lane its columns, four at a time.
+// Joins the segments of rows that have several: O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s, L = (M + log2 of the latter) ln 2, in
+// the list's order; rows that see nothing get O = 0, L = -inf; rows with one segment are finished.  A block takes a row (or
+// several one after the other, where there are many): D / 4 threads a partial result, kFinishThreads / (D / 4) results side
+// by side, several loads of each in flight (a warp a row, one result after the other: 7 to 24 us where this takes 4 to 6).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kFinishThreads)
-    decode_cache_finish(const __grid_constant__ CacheParams a, void* __restrict__ out, float* __restrict__ lse, int64_t rows, int grid) {
+    decode_cache_finish(const __grid_constant__ CacheParams a, int grid, int rows, int rows_per_block) {
+  constexpr int CH = D / 4, WAYS = kFinishThreads / CH, AHEAD = 4;
+  __shared__ float4 sums[WAYS][CH];
+  __shared__ int slots[kMostSlots], head_n[3];
   const List& list = a.list;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = ((int64_t)blockIdx.x * kFinishThreads + threadIdx.x) >> 5;
-  const int64_t bh = row / a.gn;  // sequence and key/value head
-  const int w = (int)(row - bh * a.gn);
-  const int b = (int)(bh / list.hkv), kvh = (int)(bh - (int64_t)b * list.hkv);
-  const bool valid = row < rows;
-  const int tiles = valid ? list.keys(list.len_of(b)).tiles : 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!valid) return;
-  const int64_t total = a.ws.offsets[list.b];
-  const int runs = runs_of(total, grid);
-  // the segments of an entry: CTAs [c0, c0 + n) have one each, in slots from first + c0 on
-  struct Part {
-    const float4* o;
-    const float2* ml;
-    int n, lanes, copies, lane;
-  } part[2];
-  auto entry = [&](int64_t e, int64_t off, int t, const float4* o, const float2* ml, int lanes, int copies, int r) {
-    Part x;
-    const int c0 = run_of(total, off + kSegCost, runs), c1 = run_of(total, off + kSegCost + t - 1, runs);
-    x.n = c1 - c0 + 1;
-    x.lanes = lanes;
-    x.copies = copies;
-    x.lane = r;
-    x.o = o + (e + c0) * (D / 4) * lanes;
-    x.ml = ml + (e + c0) * lanes;
-    return x;
-  };
-  part[0].n = part[1].n = 0;
-  part[0].copies = part[1].copies = 1;
-  if (list.p > 0) {
-    const int64_t r = (int64_t)b * a.gn + w;
-    const int rt = (int)(r / BM);
-    const int64_t e = (int64_t)kvh * list.rt_pre + rt;
-    part[0] = entry(e, e * List::cost(list.prefix_tiles()), list.prefix_tiles(), a.ws.pre_o, a.ws.pre_ml, a.ws.pre_lanes, a.r_pre,
-                    (int)(r % BM));
+  const int lane = threadIdx.x & 31, col = threadIdx.x % CH, way = threadIdx.x / CH;
+  __shared__ int64_t part[2][kFinishThreads / 32];
+  bool waited = false;
+  int64_t total = 0, sums_before = 0;
+  Prefix pre{};
+  // The list of few sequences is looked at again here, before the wait for the kernel that wrote it down.
+  const bool alone = list.b <= kFewSequences;
+  const int b0 = (int)blockIdx.x * rows_per_block / a.gn / list.hkv;  // of the first row
+  if (alone) {
+    int64_t all = 0, before = 0;
+    for (int s = threadIdx.x; s < list.b; s += kFinishThreads) {
+      const int64_t x = list.own_total(s);
+      all += x;
+      if (s < b0) before += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (lane == 0) part[0][threadIdx.x >> 5] = all, part[1][threadIdx.x >> 5] = before;
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int k = 0; k < kFinishThreads / 32; ++k) all += part[0][k], before += part[1][k];
+    if (list.p > 0) pre.set(list, all, grid);
+    total = pre.total() + all;
+    sums_before = pre.total() + before;
   }
-  if (tiles > 0) {
-    const int64_t e = (int64_t)kvh * list.rt_own + w / BM;
-    part[1] = entry((int64_t)b * list.hkv * list.rt_own + e, a.ws.offsets[b] + e * List::cost(tiles), tiles, a.ws.own_o,
-                    a.ws.own_ml, a.ws.own_lanes, a.r_own, w % BM);
-  }
-  const int n0 = part[0].n * part[0].copies, n = n0 + part[1].n * part[1].copies;  // partial results
-  auto place = [&](int i, const float4** o, int* lanes) {
-    const Part& x = i < n0 ? part[0] : part[1];
-    if (i >= n0) i -= n0;
-    const int seg = i / x.copies, at = (i - seg * x.copies) * (x.lanes / x.copies) + x.lane;
-    *o = x.o + (int64_t)seg * (D / 4) * x.lanes + at;
-    *lanes = x.lanes;
-    return x.ml + (int64_t)seg * x.lanes + at;
-  };
-  constexpr int CH = D / 4;                          // float4 columns of a row
-  constexpr int PER = CH > 32 ? CH / 32 : 1;         // of a lane
-  constexpr int WAYS = CH < 32 ? 32 / CH : 1;        // partial results side by side (d = 64)
-  const int col = lane % (CH < 32 ? CH : 32), way = lane / (CH < 32 ? CH : 32);
-  float M = -INFINITY, l = 0.f;
-  float4 acc[PER];
+  int b_at = b0;  // sums_before is this sequence's offset
+  const int end = min(rows, ((int)blockIdx.x + 1) * rows_per_block);
+  for (int row = (int)blockIdx.x * rows_per_block; row < end; ++row) {
+    const int bh = row / a.gn;  // sequence and key/value head
+    const int w = row - bh * a.gn;
+    const int b = bh / list.hkv, kvh = bh - b * list.hkv;
+    const int tiles = list.keys(list.len_of(b)).tiles;
+    if (!waited && !alone) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+      total = a.ws.offsets[list.b];
+      if (list.p > 0) pre.set(list, a.ws.offsets[list.b + 1], grid);
+    }
+    for (; alone && b_at < b; ++b_at) sums_before += list.own_total(b_at);
+    const int64_t own_off = alone ? sums_before : a.ws.offsets[b];
+    const int runs = runs_of(total, grid);
+    // The segments of an entry: CTAs c0 to c1 have one each, in slots from the entry's number + c0 on.  Those of the prefix'
+    // pieces are listed first, in their order, by the first warp.
+    if (threadIdx.x < 32) {
+      int n = 0;
+      if (list.p > 0) {
+        const int rt = (b * a.gn + w) / BM;
+        for (int x0 = 0; x0 < pre.pieces; x0 += 32) {
+          const int x = x0 + lane, e = (kvh * pre.pieces + x) * list.rt_pre + rt;
+          int c0 = 0, mine = 0;
+          if (x < pre.pieces) {
+            const int64_t off = e * pre.cost() + kSegCost;
+            c0 = run_of(total, off, runs);
+            mine = run_of(total, off + pre.tiles_of(x) - 1, runs) - c0 + 1;
+          }
+          int end_ = mine;
 #pragma unroll
-  for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    // 32 results' statistics at once, then their O
-    const float4* o = nullptr;
-    int lanes = 0;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (i0 + lane < n) ml = *place(i0 + lane, &o, &lanes);
-    float mx = ml.x;
-    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    const float top = fmaxf(M, mx);
-    const float old = M == -INFINITY ? 0.f : ex2(M - top);
-    M = top;
-    // (a row of NaN scores has m = -inf and l = NaN)
-    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - top);
-    const bool there = ml.x != -INFINITY || ml.y != 0.f;
-    l *= old;
-    float add = there ? f * ml.y : 0.f;
-    for (int s = 16; s > 0; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
-    l += add;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k].x *= old, acc[k].y *= old, acc[k].z *= old, acc[k].w *= old;
-    const unsigned present = __ballot_sync(0xffffffffu, there);
-    const int m = min(32, n - i0);
-#pragma unroll 4
-    for (int i = 0; i < m; i += WAYS) {
-      const int mine = i + way;
-      const float fi = __shfl_sync(0xffffffffu, f, mine & 31);
-      if (mine < m && ((present >> mine) & 1)) {
-        place(i0 + mine, &o, &lanes);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          const float4 x = o[(int64_t)(col + 32 * k) * lanes];
-          acc[k].x = fmaf(fi, x.x, acc[k].x), acc[k].y = fmaf(fi, x.y, acc[k].y);
-          acc[k].z = fmaf(fi, x.z, acc[k].z), acc[k].w = fmaf(fi, x.w, acc[k].w);
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, end_, o);
+            if (lane >= o) end_ += y;
+          }
+          for (int k = 0; k < mine; ++k)
+            if (n + end_ - mine + k < kMostSlots) slots[n + end_ - mine + k] = e + c0 + k;
+          n += __shfl_sync(0xffffffffu, end_, 31);
         }
       }
+      if (lane == 0) {
+        head_n[0] = min(n, kMostSlots);
+        int own_n = 0, slot = 0;
+        if (tiles > 0) {
+          const int e = kvh * list.rt_own + w / BM;
+          const int64_t off = own_off + e * List::cost(tiles) + kSegCost;
+          const int c0 = run_of(total, off, runs);
+          own_n = run_of(total, off + tiles - 1, runs) - c0 + 1;
+          slot = b * list.hkv * list.rt_own + e + c0;
+        }
+        head_n[1] = own_n;
+        head_n[2] = slot;
+      }
     }
-  }
-  if constexpr (WAYS > 1) {
-    acc[0].x += __shfl_xor_sync(0xffffffffu, acc[0].x, 16), acc[0].y += __shfl_xor_sync(0xffffffffu, acc[0].y, 16);
-    acc[0].z += __shfl_xor_sync(0xffffffffu, acc[0].z, 16), acc[0].w += __shfl_xor_sync(0xffffffffu, acc[0].w, 16);
-  }
-  static_assert(WAYS <= 2, "two results side by side");
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // (nothing visible: O = 0)
-  uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + row * D);
-  if (way == 0) {
+    __syncthreads();
+    if (!waited) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+    }
+    const int n_pre = head_n[0], n = n_pre + head_n[1];  // partial results
+    const int own_slot = head_n[2];
+    const bool finished = n == 1 && list.p == 0;
+    auto load = [&](int i, float4* x, float2* ml) {
+      const bool own = i >= n_pre;
+      const int64_t slot = own ? own_slot + i - n_pre : slots[i];
+      const int lanes = own ? a.ws.own_lanes : a.ws.pre_lanes, at = own ? w % BM : (b * a.gn + w) % BM;
+      if (x) *x = (own ? a.ws.own_o : a.ws.pre_o)[(slot * CH + col) * lanes + at];
+      *ml = (own ? a.ws.own_ml : a.ws.pre_ml)[slot * lanes + at];
+    };
+    if (finished) {
+      __syncthreads();
+      continue;
+    }
+    // this thread's results are way, way + WAYS, ...: the first ones' O on the way while every warp takes the statistics of all
+    float4 x[AHEAD];
+    float2 xm[AHEAD];
 #pragma unroll
-    for (int k = 0; k < PER; ++k)
-      dst[col + 32 * k] = make_uint2(pack2<BF16>(acc[k].x * inv, acc[k].y * inv), pack2<BF16>(acc[k].z * inv, acc[k].w * inv));
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = way + j * WAYS;
+      xm[j] = make_float2(-INFINITY, 0.f);
+      if (i < n) load(i, &x[j], &xm[j]);
+    }
+    float M = -INFINITY, l = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < n) load(i0 + lane, nullptr, &ml);
+      float top = fmaxf(M, ml.x);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      l = M == -INFINITY ? l : l * ex2(M - top);
+      M = top;
+      // (a row of NaN scores has m = -inf and l = NaN)
+      float add = ml.x == -INFINITY ? ml.y : ex2(ml.x - top) * ml.y;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
+      l += add;
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = way; i0 < n; i0 += AHEAD * WAYS) {
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        // what saw nothing (m = -inf, l = 0) is left out, whatever its O holds
+        const bool there = xm[j].x != -INFINITY || !(xm[j].y == 0.f);
+        const float f = xm[j].x == -INFINITY ? 1.f : ex2(xm[j].x - M);
+        if (there)
+          acc.x = fmaf(f, x[j].x, acc.x), acc.y = fmaf(f, x[j].y, acc.y), acc.z = fmaf(f, x[j].z, acc.z), acc.w = fmaf(f, x[j].w, acc.w);
+        const int i = i0 + (j + AHEAD) * WAYS;
+        xm[j] = make_float2(-INFINITY, 0.f);
+        if (i < n) load(i, &x[j], &xm[j]);
+      }
+    }
+    sums[way][col] = acc;
+    __syncthreads();
+    if (way == 0) {
+#pragma unroll
+      for (int k = 1; k < WAYS; ++k) {
+        const float4 y = sums[k][col];
+        acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // (nothing visible: O = 0)
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (int64_t)row * D)[col] =
+          make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+      if (col == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    }
+    __syncthreads();  // (the next row's sums)
   }
-  if (lane == 0) lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
 template <int D, bool BF16>
 cudaError_t launch_d(const CacheDecodeArgs& a) {
   using C = CacheCfg<D>;
-  const int grid = device_sm_count();
+  const int grid = cache_grid();
   const Shape shape(a.b, a.h, a.hkv, a.nq, a.p, D, grid);
   CacheParams p{};
   p.q = a.q;
+  p.o = a.o;
+  p.lse = a.lse;
   p.list = List{a.lens, a.b, a.hkv, a.nq, a.capacity, a.p, C::BN, shape.rt_own, shape.rt_pre, a.window, a.window > 0 ? a.sinks : 0};
   p.ws = shape.carve(a.ws, D);
-  p.h = a.h;
   p.gn = shape.gn;
   p.r_own = shape.r_own;
   p.r_pre = shape.r_pre;
@@ -901,9 +1109,10 @@ cudaError_t launch_d(const CacheDecodeArgs& a) {
   kern<<<grid, C::THREADS, C::SMEM, a.stream>>>(p, tk, tv, tk16, tv16, tkp, tvp, tkp16, tvp16);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the runs are still going (it waits for them before it reads what they write)
-  const int64_t rows = (int64_t)a.b * a.h * a.nq;
+  // (several rows a block only where single ones would be many more blocks than the GPU holds)
+  const int rows = a.b * a.h * a.nq, per_block = std::max(1, std::min(16, rows / (grid * 16)));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((rows * 32 + kFinishThreads - 1) / kFinishThreads));
+  cfg.gridDim = dim3((unsigned)((rows + per_block - 1) / per_block));
   cfg.blockDim = dim3(kFinishThreads);
   cfg.stream = a.stream;
   cudaLaunchAttribute attr{};
@@ -911,13 +1120,13 @@ cudaError_t launch_d(const CacheDecodeArgs& a) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_cache_finish<D, BF16>, p, a.o, a.lse, rows, grid);
+  return cudaLaunchKernelEx(&cfg, decode_cache_finish<D, BF16>, p, grid, rows, per_block);
 }
 
 }  // namespace
 
 size_t decode_cache_workspace_bytes(int b, int h, int hkv, int nq, int p, int d) {
-  return Shape(b, h, hkv, nq, p, d, device_sm_count()).bytes(b, d);
+  return Shape(b, h, hkv, nq, p, d, cache_grid()).bytes(b, d);
 }
 
 cudaError_t launch_decode_cache(const CacheDecodeArgs& a) {
