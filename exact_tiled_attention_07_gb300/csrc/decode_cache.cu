@@ -531,9 +531,6 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
                                 base + x * kLoadRows, g.head);
               }
             }
-            // behind the run's first tile: the first rows of Q go before the flood of all CTAs' loads, in which they took 5 us.  (No
-            // other segment is published yet, so this phase of the barrier is the current or the last one.)
-            if (ok && pos == 2) ok = mbar_wait(q_full, 0, ctx, 414);
           }
           // the next entry
           off += g.prefix ? pre.cost() : tiles + kSegCost;
