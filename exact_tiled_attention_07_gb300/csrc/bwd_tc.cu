@@ -844,6 +844,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
           // faster; with one chunk (d = 128) the preload measured 1.4 % slower).
           constexpr bool kPreload = NCH > 1;
           uint32_t pk[NCH * 16];
+          // (window) P as it was before it was rounded, for dS: dK and dQ are off by 0.0024 of their rms instead of 0.0030 (bf16; 0.0017
+          // is their own rounding), and the kernel takes the same time (650 us; d = 64: 2 % more)
+          constexpr bool kKeepP = WINDOW;
+          float pf[kKeepP ? NCH * 32 : 1];
 #pragma unroll
           for (int cl = 0; cl < NCH; ++cl) {
             const int c = c0 + cl;
@@ -872,6 +876,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                     const int qc = c * 32 + t + u;
                     e[u] = (key_ok && qc >= mask_below && qc < mask_above) ? e[u] : 0.f;
                   }
+                }
+                if constexpr (kKeepP) {
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) pf[cl * 32 + t + u] = e[u];
                 }
                 pk[cl * 16 + t / 2] = pack2<BF16>(e[0], e[1]);
                 pk[cl * 16 + t / 2 + 1] = pack2<BF16>(e[2], e[3]);
@@ -913,11 +921,15 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
               for (int t = 0; t < 16; t += 2) {
                 // dS = P o (dP - D), two queries per paired subtract and multiply
                 const float4 d4 = kPreload ? dc[t / 2] : *reinterpret_cast<const float4*>(dvec + c * 32 + 2 * t);
-                const float2 ds01 = fmul2(unpack2<BF16>(pk[cl * 16 + t]),
+                const float2 p01 = kKeepP ? make_float2(pf[kKeepP ? cl * 32 + 2 * t : 0], pf[kKeepP ? cl * 32 + 2 * t + 1 : 0])
+                                          : unpack2<BF16>(pk[cl * 16 + t]);
+                const float2 p23 = kKeepP ? make_float2(pf[kKeepP ? cl * 32 + 2 * t + 2 : 0], pf[kKeepP ? cl * 32 + 2 * t + 3 : 0])
+                                          : unpack2<BF16>(pk[cl * 16 + t + 1]);
+                const float2 ds01 = fmul2(p01,
                                           fsub2(make_float2(__uint_as_float(r[2 * t]), __uint_as_float(r[2 * t + 1])),
                                                 make_float2(d4.x, d4.y)));
                 const float2 ds23 =
-                    fmul2(unpack2<BF16>(pk[cl * 16 + t + 1]),
+                    fmul2(p23,
                           fsub2(make_float2(__uint_as_float(r[2 * t + 2]), __uint_as_float(r[2 * t + 3])),
                                 make_float2(d4.z, d4.w)));
                 dsk[t] = pack2<BF16>(ds01.x, ds01.y);

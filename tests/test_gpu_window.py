@@ -2,8 +2,8 @@
 
 Tolerances (e = EPS, half a step of the 16-bit type, relative).  Scores are fp32 sums of d products, L and the exponentials fp32:
 together ds = (d / 16 + 8) 2^-23 |q| |k| scale + 2^-20 of a score, so a probability is off by (2 ds) p before it is rounded (e p).
-O: |O| e + e sum p |v| + 2 ds max |v|.  Gradients: dV sums rounded p times dO; dS = p (dP - D) is rounded once more, and D = sum
-dO O takes the rounded O, so D is off by dD = sum |dO| |dO's O error|; dS by (2 e + 2 ds) |dS| + p (dD + (d / 16 + 8) 2^-23 |dO| |v|);
+O: |O| e + e sum p |v| + 2 ds max |v|.  Gradients: dV sums rounded p times dO; dS = p (dP - D) takes p unrounded and is rounded itself, and D = sum
+dO O takes the rounded O, so D is off by dD = sum |dO| |dO's O error|; dS by (e + 2 ds) |dS| + p (dD + (d / 16 + 8) 2^-23 |dO| |v|);
 dQ and dK sum dS times k and q; each is rounded once at the end (e).
 """
 
@@ -55,7 +55,7 @@ def reference(q, k, v, window, sinks, scale, do=None):
     g = p * (dp - big)
     big_tol = (do.abs() * o_tol).sum(-1, keepdim=True)
     dp_tol = (d / 16 + 8) * 2.0 ** -23 * do.norm(dim=-1, keepdim=True) * v.norm(dim=-1).max()
-    g_tol = (2 * e + 2 * ds) * g.abs() + p * (big_tol + dp_tol)
+    g_tol = (e + 2 * ds) * g.abs() + p * (big_tol + dp_tol)
     dq, dk, dv = scale * (g @ k), scale * (g.transpose(-1, -2) @ q).sum(0), (p.transpose(-1, -2) @ do).sum(0)
     out["dq"] = dq, e * dq.abs() + scale * (g_tol @ k.abs()) + 2.0 ** -24
     out["dk"] = dk, e * dk.abs() + scale * (g_tol.transpose(-1, -2) @ q.abs()).sum(0) + 2.0 ** -24
@@ -146,7 +146,7 @@ def test_same_as_causal_and_as_the_masked_window(fa, d):
     got = [torch.empty_like(t) for t in (q, k, v)]
     ws = torch.empty(fa.fa_bwd_workspace_size(2, 4, 900, d), dtype=torch.uint8, device="cuda")
     fa.fa_bwd_window(q, k, v, o, do, lse, *got, ws, d ** -0.5, 200, 0)
-    assert torch.equal(ref[1], got[1]) and torch.equal(ref[2], got[2])
+    assert torch.equal(ref[2], got[2])  # (dK: the masked kernel's dS takes the rounded probabilities)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
