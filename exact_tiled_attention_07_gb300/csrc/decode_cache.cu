@@ -79,6 +79,11 @@ struct CacheCfg {
   static_assert(SMEM <= 232448 && OFF_SEG % 8 == 0 && OFF_STAT % 8 == 0 && OFF_RED % 8 == 0, "shared memory");
 };
 
+// x / y of numbers that are not negative: a division of 64 bits takes a hundred instructions, of 32 bits a fifth of that.
+__device__ __forceinline__ int64_t div(int64_t x, int64_t y) {
+  return (x | y) >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 // What lies of an entry in a CTA's run.
 struct Seg {
   int rows;     // of the entry's 128 (0: no more segments)
@@ -96,15 +101,16 @@ static_assert(sizeof(Seg) <= 64, "Seg");
 // The list of tiles.  Offsets count tiles and kSegCost for each entry.
 struct List {
   const int32_t* lens;
-  int b, hkv, nq, capacity, p, bn;
+  int b, hkv, nq, capacity, p, log_bn;  // (log2 of a tile's keys: divisions by it are shifts)
   int rt_own, rt_pre;  // row tiles of a sequence's head, of the prefix' head
   int window, sinks;
 
+  __device__ int tiles_of(int keys) const { return (int)(((unsigned)keys + (1u << log_bn) - 1) >> log_bn); }
   // keys of a sequence: sinks [0, sk), the rest [lo, len)
   struct Keys {
     int len, lo, sk, ns, tiles;
   };
-  __host__ __device__ Keys keys(int len) const {
+  __device__ Keys keys(int len) const {
     Keys k;
     k.len = len;
     k.lo = 0;
@@ -113,13 +119,13 @@ struct List {
       k.lo = lo > 0 ? (int)lo : 0;
     }
     k.sk = sinks < k.lo ? sinks : k.lo;
-    k.ns = (k.sk + bn - 1) / bn;
-    k.tiles = k.ns + (int)(((int64_t)len - k.lo + bn - 1) / bn);
+    k.ns = tiles_of(k.sk);
+    k.tiles = k.ns + tiles_of(len - k.lo);
     return k;
   }
   __device__ int len_of(int s) const { return min(max(lens[s], 0), capacity); }
-  __host__ __device__ static int64_t cost(int tiles) { return tiles > 0 ? tiles + kSegCost : 0; }
-  __host__ __device__ int prefix_tiles() const { return (int)(((int64_t)p + bn - 1) / bn); }
+  __device__ static int64_t cost(int tiles) { return tiles > 0 ? tiles + kSegCost : 0; }
+  __device__ int prefix_tiles() const { return tiles_of(p); }
   __device__ int64_t own_total(int s) const { return (int64_t)hkv * rt_own * cost(keys(len_of(s)).tiles); }
 };
 
@@ -135,8 +141,8 @@ struct Prefix {
     pieces = entries = 0;
     if (tiles == 0) return;
     if (list.rt_pre > 1) {
-      const int64_t run = (own + (int64_t)list.hkv * list.rt_pre * tiles + grid - 1) / grid;
-      const int n = max(1, (int)((tiles + run / 2) / run));
+      const int64_t run = div(own + (int64_t)list.hkv * list.rt_pre * tiles + grid - 1, grid);
+      const int n = max(1, (int)div(tiles + run / 2, run));
       piece = (tiles + n - 1) / n;  // (two or more: at least 3/4 of a run)
     }
     pieces = (tiles + piece - 1) / piece;
@@ -147,15 +153,8 @@ struct Prefix {
   __device__ int tiles_of(int x) const { return min(piece, tiles - x * piece); }
 };
 // CTA c of n takes [start(c), start(c + 1)) of a list.
-// (A division of 64 bits takes a hundred instructions, of 32 bits a fifth of that.)
-__device__ __forceinline__ int64_t run_start(int64_t total, int c, int n) {
-  const int64_t x = total * c;
-  return x < INT32_MAX ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
-}
-__device__ __forceinline__ int run_of(int64_t total, int64_t at, int n) {
-  const int64_t x = (at + 1) * n - 1;
-  return x < INT32_MAX ? (int)((uint32_t)x / (uint32_t)total) : (int)(x / total);
-}
+__device__ __forceinline__ int64_t run_start(int64_t total, int c, int n) { return div(total * c, n); }
+__device__ __forceinline__ int run_of(int64_t total, int64_t at, int n) { return (int)div((at + 1) * n - 1, total); }
 __device__ __forceinline__ int runs_of(int64_t total, int grid) { return total < grid ? (int)total : grid; }
 
 // Partial results: for the prefix' segments, then the caches', [slots][D / 4][lanes] float4 and [slots][lanes] (m, l), a lane for
@@ -476,7 +475,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
         };
         if (u0 < pre_total) {
           const int c = (int)pre.cost();
-          const int e = u0 < INT32_MAX ? (int)((uint32_t)u0 / (uint32_t)c) : (int)(u0 / c);
+          const int e = (int)div(u0, c);
           off = (int64_t)e * c;
           g.prefix = 1;
           g.b = 0;
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
         } else {
           keys = list.keys(list.len_of(b));
           const int64_t c = List::cost(keys.tiles), in = u0 - b_off;
-          const int e = in < INT32_MAX ? (int)((uint32_t)in / (uint32_t)c) : (int)(in / c);
+          const int e = (int)div(in, c);
           off = b_off + e * c;
           begin_own(e);
         }
@@ -1078,7 +1077,7 @@ cudaError_t launch_d(const CacheDecodeArgs& a) {
   p.q = a.q;
   p.o = a.o;
   p.lse = a.lse;
-  p.list = List{a.lens, a.b, a.hkv, a.nq, a.capacity, a.p, C::BN, shape.rt_own, shape.rt_pre, a.window, a.window > 0 ? a.sinks : 0};
+  p.list = List{a.lens, a.b, a.hkv, a.nq, a.capacity, a.p, D == 256 ? 6 : 7, shape.rt_own, shape.rt_pre, a.window, a.window > 0 ? a.sinks : 0};
   p.ws = shape.carve(a.ws, D);
   p.gn = shape.gn;
   p.r_own = shape.r_own;
