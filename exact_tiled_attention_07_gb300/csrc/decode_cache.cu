@@ -14,9 +14,10 @@
 // equal run.  What lies of an entry in one run is a segment.  A window's tiles begin at its first key, not at a
 // multiple of the tile; the sinks in front of it have tiles of their own; a tile's loads end behind its last key (in steps
 // of 16 rows).
-// The joining of segments (O and row statistics of each, unnormalised, in the workspace) is a second launch,
-// decode_cache_finish.  Slots need no bookkeeping: along the list each new segment has either the next entry or the next CTA, so
-// entry + CTA numbers them.
+// An entry that lies inside one run, and has no prefix, is finished there; the segments of the others (O and row statistics of
+// each, unnormalised, in the workspace) are joined by a second launch, decode_cache_finish, which starts under the first one.
+// Slots need no bookkeeping: along the list each new segment has either the next entry or the next CTA, so entry + CTA
+// numbers them.
 //
 // A CTA is a chain of warps that run ahead of one another across segments:
 //   producer  walks the list, publishes segments in a ring, loads K and V tiles into a ring that takes the shared memory;
@@ -24,8 +25,15 @@
 //   softmax   (4 warps, a thread a row) as in the forward kernel: exp2, lazy rescaling by 2^8.  With 32 rows or fewer
 //             the rows stand in all four lane quarters and each takes a quarter of the tile's columns, as if they were
 //             other pieces of the keys (two halves for up to 64 rows);
-//   drain     (4 warps) the next segment's Q into TMEM, a finished segment's O out of it, so that the softmax goes on
-//             with the next segment's scores meanwhile.
+//   drain     (4 warps) the next segment's Q into TMEM, a finished segment's O out of it (copies of a row joined), so that
+//             the softmax goes on with the next segment's scores meanwhile.
+// Measured (one GB300, d = 128, 4 rows a head): 32 x 8 heads of 32,768 slots (4.3 GB) 597 us, 7.2 TB/s, above the measured copy
+// rate; 64 x 8 of 2,048 slots 97 us (5.5 TB/s); d = 64 and 256 6.8 and 7.1 TB/s on 2.1 and 4.3 GB.  Around that: 5 us until the first
+// scores, of which 1.5 are index arithmetic and the rest latencies (launch, lengths, Q, first keys), one behind the other;
+// 2.5 to 3 us for a segment of one tile (the drain's work on it: 150 us for 512 x 8 heads of 100 slots); 0.9 us for a tile of
+// the prefix with 128 rows, one softmax warp a scheduler, twice the matrix instructions' time.  Steps (16 sequences with a
+// window of 4,096; 64 behind a prefix of 32,768): segments' copies joined by the second launch 60, 142 us; joined here, index
+// arithmetic in 32 bits, the next segment's Q not waited for while a P V is due 50, 146; the prefix in pieces 50, 127.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -44,7 +52,9 @@ constexpr int BM = 128;  // rows of a tile (TMEM lanes)
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kLoadRows = 16;   // rows of the loads that end a tile early
-constexpr int kSegCost = 2;     // what a segment's start and end cost, in tiles
+// What a segment's start and end cost, in tiles.  Counted as 2, 3, 4, 6: 12 sequences of up to 2,047 slots behind 20,001 shared
+// tokens 48, 44, 42, 44 us; 64 of up to 3,943 behind 32,768 130, 130, 134, 142; without a prefix the same within 2 %.
+constexpr int kSegCost = 3;
 constexpr int kSegs = 4;        // published segments, and row statistics, in flight
 constexpr int kFinishThreads = 128;
 constexpr int kMostSlots = 1024;  // segments that a row has in the prefix, at most (pieces + CTAs)
@@ -685,7 +695,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
       if (!g.prefix) {
         hi = g.end - list.nq + (g.rt * BM + rit) % list.nq + 1;
         if (list.window > 0) {
-          lo = max(0, hi - list.window);
+          lo = hi > list.window ? hi - list.window : 0;
           sinks = list.sinks;
         }
       }

@@ -248,3 +248,33 @@ def test_refusals(fa):
         fa.attention_decode_window(q, k, v, lens, 0, 4)
     empty = fa.attention_decode_window(q[:, :, :0].contiguous(), k, v, lens)
     assert empty[0].shape == (1, 4, 0, 64)
+
+
+@pytest.mark.parametrize("P", [None, 300])
+def test_more_sequences_than_the_second_launch_looks_through(fa, P):
+    """600 sequences, several rows a block of the second launch, 38 tiles of rows behind the prefix."""
+    run(fa, [(i * 37) % 70 for i in range(600)], 16, 2, 1, 64, "fp16", 70, P=P)
+
+
+def test_prefix_in_pieces(fa):
+    """Several tiles of rows: the prefix is cut into pieces as long as a run, here of 26 tiles and of one."""
+    run(fa, [50] * 64, 32, 8, 1, 128, "bf16", 50, P=32768)
+    run(fa, [0] * 130, 8, 4, 2, 64, "fp16", 64, P=1300)
+    run(fa, [1, 2000] * 40, 8, 2, 1, 256, "bf16", 2000, P=777)
+
+
+def test_rows_longer_than_their_sequence_under_the_largest_window(fa):
+    run(fa, [1, 2, 0, 5], 2, 1, 9, 128, "bf16", 8, 2 ** 31 - 1, 2 ** 31 - 1)
+
+
+def test_another_workspace_and_outputs_keep_their_neighbours(fa):
+    q, k, v, lens, prefix = make([300, 7], 4, 2, 1, 128, "bf16", 300, P=200)
+    B, H, Nq, d = q.shape
+    n = fa.fa_decode_prefix_workspace_size(B, H, 2, Nq, 200, 300, d)
+    ws = torch.full((n + 512,), 3, dtype=torch.uint8, device="cuda")
+    o = torch.full((B + 2, H, Nq, d), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((B + 2, H, Nq), 9.0, device="cuda")
+    fa.fa_decode_prefix(q, *prefix, k, v, lens, o[1:3], lse[1:3], d ** -0.5, ws[256:256 + n])
+    check(q, k, v, lens, o[1:3], lse[1:3], d ** -0.5, prefix=prefix)
+    assert (o[0] == 7).all() and (o[3] == 7).all() and (lse[0] == 9).all() and (lse[3] == 9).all()
+    assert (ws[:256] == 3).all() and (ws[256 + n:] == 3).all()
