@@ -463,27 +463,41 @@ def fa_bwd_masked(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, causal, windo
                                         int(window), mp, mh, _dt(Q), _stream(stream)))
 
 
+def _window_shape(Q, K, V, q_like=(), kv_like=(), rows=(), more=()):
+    """(B, H, Hkv, N, d) of a call with a window and sinks, after checking its tensors: q_like shaped as Q, kv_like as K, rows fp32
+    vectors of a number a query."""
+    qs, ks, dt = Q.shape, K.shape, Q.dtype
+    if len(qs) != 4 or len(ks) != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, H, N, d = qs
+    if ks[0] != B or ks[2:] != qs[2:] or ks[1] < 1 or H % ks[1]:
+        raise ValueError("K must be [B, Hkv, N, d] with H a multiple of Hkv")
+    for t in q_like:
+        if t.shape != qs or t.dtype != dt:
+            raise ValueError("Q, O, dO and dQ must share shape and dtype")
+    for t in (K, V, *kv_like):
+        if t.shape != ks or t.dtype != dt:
+            raise ValueError("K, V, dK and dV must share shape, and dtype with Q")
+    for t in rows:
+        _rows(t, B * H * N)
+    _ready(Q, K, V, *q_like, *kv_like, *rows, *more)
+    return B, H, ks[1], N, d
+
+
 def fa_fwd_window(Q, K, V, O, L, scale, window, sinks=0, stream=None):
     """Causal forward with a sliding window and the first `sinks` keys always visible."""
-    B, H, N, d = _shape4(Q)
-    _on_device(Q, K, V, O, L)
-    Hkv = _kv_heads(Q, K, V)
-    _same(Q, O)
-    _rows(L, B * H * N)
-    _check(load_library().fa_fwd_window(_p(Q), _p(K), _p(V), _p(O), _p(L), B, H, Hkv, N, d, float(scale), int(window),
-                                        int(sinks), _dt(Q), _stream(stream)))
+    shape = _window_shape(Q, K, V, (O,), (), (L,))
+    _check(load_library().fa_fwd_window(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), *shape,
+                                        float(scale), int(window), int(sinks), _dt(Q), _current(stream)))
 
 
 def fa_bwd_window(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, window, sinks=0, stream=None):
     """Backward of fa_fwd_window."""
-    B, H, N, d = _shape4(Q)
-    _on_device(Q, K, V, O, dO, L, dQ, dK, dV, workspace)
-    Hkv = _kv_heads(Q, K, V, dK, dV)
-    _same(Q, O, dO, dQ)
-    _rows(L, B * H * N)
-    _check(load_library().fa_bwd_window(_p(Q), _p(K), _p(V), _p(O), _p(dO), _p(L), _p(dQ), _p(dK), _p(dV), _p(workspace),
-                                        workspace.numel() * workspace.element_size(), B, H, Hkv, N, d, float(scale),
-                                        int(window), int(sinks), _dt(Q), _stream(stream)))
+    shape = _window_shape(Q, K, V, (O, dO, dQ), (dK, dV), (L,), (workspace,))
+    _check(load_library().fa_bwd_window(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), L.data_ptr(),
+                                        dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), *shape, float(scale), int(window),
+                                        int(sinks), _dt(Q), _current(stream)))
 
 
 def _packed(t, what):
@@ -863,14 +877,21 @@ def _sinks_allowed(causal, window, sinks, block_mask=None):
 def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, block_mask=None, sinks=0):
     """O, L = fa_fwd(q, k, v) (fa_fwd_gqa when k, v have fewer heads than q; fa_fwd_masked with a
     window or a block mask; fa_fwd_window with a window, causal, and sinks); outputs on q's device."""
+    if _sinks_allowed(causal, window, sinks, block_mask):
+        shape = _window_shape(q, k, v)
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        _check(load_library().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), *shape,
+                                            shape[4] ** -0.5 if scale is None else float(scale), int(window), int(sinks),
+                                            _dt(q), _current(stream)))
+        _used_on(stream, o, lse)
+        return o, lse
     B, H, N, d = _shape4(q)
     _warn_cuda_core("fwd", q, d)
     scale = d ** -0.5 if scale is None else scale
     o = torch.empty_like(q)
     lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    if _sinks_allowed(causal, window, sinks, block_mask):
-        fa_fwd_window(q, k, v, o, lse, scale, window, sinks, stream)
-    elif window or block_mask is not None:
+    if window or block_mask is not None:
         fa_fwd_masked(q, k, v, o, lse, scale, causal, window, block_mask, stream)
     elif k.shape[1] != H:
         fa_fwd_gqa(q, k, v, o, lse, scale, causal, stream)
@@ -883,6 +904,22 @@ def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=
                        block_mask=None, sinks=0):
     """dQ, dK, dV = fa_bwd(...) (fa_bwd_masked with a window or a block mask; fa_bwd_window with a window
     and sinks); outputs (and workspace, unless given) allocated with torch."""
+    if _sinks_allowed(causal, window, sinks, block_mask):
+        lib, dt, dev = load_library(), q.dtype, q.device
+        B, H, Hkv, N, d = _window_shape(q, k, v, (o, do), (), (lse,), (workspace,))
+        dq = torch.empty(q.shape, dtype=dt, device=dev)
+        dk, dv = torch.empty(k.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(lib.fa_bwd_workspace_size(B, H, N, d), 16), dtype=torch.uint8, device=dev)
+            _used_on(stream, ws)
+        _check(lib.fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+                                 dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
+                                 ws.numel() * ws.element_size(), B, H, Hkv, N, d,
+                                 d ** -0.5 if scale is None else float(scale), int(window), int(sinks), _dt(q),
+                                 _current(stream)))
+        _used_on(stream, dq, dk, dv)
+        return dq, dk, dv
     B, H, N, d = _shape4(q)
     _warn_cuda_core("bwd", q, d)
     scale = d ** -0.5 if scale is None else scale
@@ -890,9 +927,7 @@ def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=
     if workspace is None:
         nbytes = fa_bwd_workspace_size(B, H, N, d)
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    if _sinks_allowed(causal, window, sinks, block_mask):
-        fa_bwd_window(q, k, v, o, do, lse, dq, dk, dv, workspace, scale, window, sinks, stream)
-    elif window or block_mask is not None:
+    if window or block_mask is not None:
         fa_bwd_masked(q, k, v, o, do, lse, dq, dk, dv, workspace, scale, causal, window, block_mask, stream)
     elif k.shape[1] != H:
         fa_bwd_gqa(q, k, v, o, do, lse, dq, dk, dv, workspace, scale, causal, stream)
@@ -1021,14 +1056,21 @@ def qk_norm_rope_backward(dqo, dko, q, k, q_weight, k_weight, table, positions=N
     else:
         dt, dev = q.dtype, q.device
         dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
-    dwq = None if q_weight is None else torch.empty_like(q_weight)
-    dwk = None if k_weight is None else torch.empty_like(k_weight)
-    if dqo.dim() == 4 and dko.dim() == 4:
-        dqo, dko = dqo.transpose(1, 2), dko.transpose(1, 2)
-    sizes = _norm_rope_sizes(q, k, q_weight, k_weight, table, positions, eps, interleaved, (dqo, dko, dq, dk))
+    dwq = None if q_weight is None else torch.empty(q_weight.shape, dtype=q_weight.dtype, device=q.device)
+    dwk = None if k_weight is None else torch.empty(k_weight.shape, dtype=k_weight.dtype, device=q.device)
+    if dqo.dim() == 4 and dko.dim() == 4:  # [B, heads, N, d]
+        sizes = _norm_rope_sizes(q, k, q_weight, k_weight, table, positions, eps, interleaved, (dq, dk))
+        B, N, H, Hkv, d = sizes[:5]
+        if (dqo.shape, dko.shape) != ((B, H, N, d), (B, Hkv, N, d)) or not (dqo.dtype == dko.dtype == q.dtype):
+            raise ValueError("the gradients must be [B, H, N, d] and [B, Hkv, N, d] of the rows' dtype")
+        _ready(q_weight, strided=(q, dqo, dko))
+        (b0, h0, t0), (b1, h1, t1) = _token_rows(dqo), _token_rows(dko)
+        outer = (b0, t0, h0, b1, t1, h1)
+    else:
+        sizes = _norm_rope_sizes(q, k, q_weight, k_weight, table, positions, eps, interleaved, (dqo, dko, dq, dk))
+        outer = (*_token_rows(dqo), *_token_rows(dko))
     _norm_rope_bwd(dqo, dko, q, k, q_weight, k_weight, table, positions, dq, dk, dwq, dwk, None,
-                   (*_token_rows(dqo), *_token_rows(dko), *_token_rows(q), *_token_rows(k), *_token_rows(dq),
-                    *_token_rows(dk)), sizes, stream)
+                   (*outer, *_token_rows(q), *_token_rows(k), *_token_rows(dq), *_token_rows(dk)), sizes, stream)
     _used_on(stream, dwq, dwk, *(() if out is not None else (dq, dk)))
     return dq, dk, dwq, dwk
 
