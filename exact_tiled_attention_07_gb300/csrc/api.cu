@@ -199,24 +199,29 @@ struct RowTensor {
   int heads;
 };
 
-// Rows of an output lie apart: from the smallest stride up, a dimension's rows end before the next one's first step.
-fa_status check_rows_apart(const RowTensor& t, int B, int N, int d, const char* what) {
+// Whether rows lie apart: from the smallest stride up, a dimension's rows end before the next one's first step.
+bool rows_apart(const NormRopeStrides& st, int64_t heads, int B, int N, int d) {
   struct Dim {
-    int64_t stride;
-    int n;
-  } dims[3] = {{t.st.batch, B}, {t.st.token, N}, {t.st.head, t.heads}};
+    int64_t stride, n;
+  } dims[3] = {{st.batch, B}, {st.token, N}, {st.head, heads}};
   std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
   double extent = d;
   for (const Dim& x : dims) {
     if (x.n <= 1) continue;
-    if ((double)x.stride < extent)
-      return fail(FA_ERR_INVALID_ARG, "%s: rows of %s overlap (a stride of %lld elements)", what, t.name, (long long)x.stride);
+    if ((double)x.stride < extent) return false;
     extent += (double)(x.n - 1) * (double)x.stride;
   }
+  return true;
+}
+fa_status check_rows_apart(const RowTensor& t, int B, int N, int d, const char* what) {
+  if (!rows_apart(t.st, t.heads, B, N, d))
+    return fail(FA_ERR_INVALID_ARG, "%s: rows of %s overlap (strides of %lld, %lld and %lld elements)", what, t.name,
+                (long long)t.st.batch, (long long)t.st.token, (long long)t.st.head);
   return FA_OK;
 }
 
-// An output and another tensor (of one element size) that do not meet: apart in memory, or side by side inside a token.
+// An output and another tensor (of one element size) do not meet if they lie apart in memory, are heads of one tensor, or
+// lie side by side inside a token.
 bool rows_meet(const RowTensor& a, const RowTensor& b, int B, int N, int d, int eb) {
   auto bytes = [&](const RowTensor& t) {
     return (size_t)((B - 1) * t.st.batch + (N - 1) * t.st.token + (t.heads - 1) * t.st.head + d) * eb;
@@ -228,6 +233,9 @@ bool rows_meet(const RowTensor& a, const RowTensor& b, int B, int N, int d, int 
   const int64_t off = (int64_t)((reinterpret_cast<uintptr_t>(hi.p) - reinterpret_cast<uintptr_t>(lo.p)) / eb);
   const int64_t lo_end = (lo.heads - 1) * lo.st.head + d, hi_end = off + (hi.heads - 1) * hi.st.head + d;
   if (off < lo_end) return true;
+  if (a.st.head == b.st.head && a.st.head > 0 && off % a.st.head == 0 && off / a.st.head >= lo.heads &&
+      rows_apart(lo.st, off / a.st.head + hi.heads, B, N, d))
+    return false;
   // the smaller step of the token and the batch dimension repeats the pattern; the larger one has to leave room for it
   int64_t small = INT64_MAX, large = INT64_MAX;
   int n_small = 1;
@@ -1066,7 +1074,8 @@ fa_status fa_qk_norm_rope_bwd(const void* dQo, const void* dKo, const void* Q, c
   if (st != FA_OK) return st;
   const bool rows = (int64_t)B * N > 0 && H + Hkv > 0;
   if (!rows && !dwq && !dwk) return FA_OK;
-  if (dwq && dwq == dwk) return fail(FA_ERR_INVALID_ARG, "fa_qk_norm_rope_bwd: dwq is dwk");
+  const size_t nw = (size_t)d * (weight_dtype == FA_FP32 ? 4 : 2);
+  if (dwq && dwk && overlap({dwq, nw}, {dwk, nw})) return fail(FA_ERR_INVALID_ARG, "fa_qk_norm_rope_bwd: dwq overlaps dwk");
   if ((st = check_ptrs({workspace}, "fa_qk_norm_rope_bwd")) != FA_OK) return st;
   DeviceSyms syms;
   if ((st = device_syms(&syms)) != FA_OK) return st;

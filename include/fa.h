@@ -450,7 +450,8 @@ FA_API fa_status fa_decode_prefix(const void* Q, const void* KP, const void* VP,
  *   Q, K      [B][N][H][d] and [B][N][Hkv][d] dtype (bf16, fp16 or fp32), rows of d contiguous elements; either may have no
  *             heads (its pointers are then not looked at)
  *   Qo, Ko    out: the same, normed and rotated: y = x w / sqrt(mean(x^2) + eps) over the row's d elements, then each of
- *             the rotary / 2 pairs of channels (a, b) becomes (a cos - b sin, b cos + a sin). In 32 bits, rounded once.
+ *             the rotary / 2 pairs of channels (a, b) becomes (a cos - b sin, b cos + a sin). In 32 bits, rounded once. (A row
+ *             of zeros is NaN with eps = 0. What is not finite in a row stays in it and, backward, in dwq or dwk.)
  *   wq, wk    [d] weight_dtype (fp32 or dtype), or NULL: ones
  *   table     [table_len][rotary] fp32: cos of the rotary / 2 pairs' angles at a position, then their sin
  *   positions device int32 [B][N], or NULL: token n of every sequence is at position n (then N <= table_len). A position
@@ -461,8 +462,8 @@ FA_API fa_status fa_decode_prefix(const void* Q, const void* KP, const void* VP,
  *             dQo, dKo, Q, K, dQ, dK): multiples of 16 bytes; rows of outputs lie apart. So Q and K may be slices of
  *             one fused projection, packed sequences are one batch, and Qo may be [B][H][N][d] as fa_fwd takes it.
  * Outputs overlap no input and no other output, but for an output that is the input of its own kind (Qo = Q; backward: dQ =
- * dQo or dQ = Q, and so on) with the same strides, and for tensors that share their token and batch strides and lie side by side
- * inside a token.
+ * dQo or dQ = Q, and so on) with the same strides, for heads of one tensor, and for tensors that share their token and batch
+ * strides and lie side by side inside a token.
  * Backward: dQ, dK (gradients of Q and K from dQo and dKo) and dwq, dwk ([d] weight_dtype; NULL: not wanted), which are sums over
  * all tokens and heads, in 32 bits in an order that does not depend on timing. Two launches; the workspace takes
  * fa_qk_norm_rope_bwd_workspace_size(d) bytes, its contents on entry do not matter. No tokens: dwq and dwk are 0.

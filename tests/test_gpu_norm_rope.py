@@ -226,6 +226,15 @@ def test_in_place_and_into_one_buffer(fa):
     assert torch.equal(c.q, qo) and torch.equal(c.k, ko) and torch.equal(c.qkv[:, 6:], v)
 
 
+def test_results_are_heads_of_one_tensor(fa):
+    c = Case(fa, 20, 4, 2, 64, 64, "bf16", "bf16", False, 13, positions=False, packed=False, B=3)
+    qo, ko = fa.qk_norm_rope(c.q, c.k, c.wq, c.wk, c.table, eps=E)
+    both = torch.full((3, 8, 20, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    fa.fa_qk_norm_rope(c.q, c.k, c.wq, c.wk, c.table, both[:, 1:5].transpose(1, 2), both[:, 6:].transpose(1, 2), eps=E)
+    assert torch.equal(both[:, 1:5], qo) and torch.equal(both[:, 6:], ko)
+    assert (both[:, 0] == 3.0).all() and (both[:, 5] == 3.0).all()
+
+
 def test_another_stream_and_a_replayed_graph(fa):
     c = Case(fa, 64, 4, 2, 128, 128, "bf16", "fp32", True, 14)
     args = (c.wq, c.wk, c.table, c.pos, E, True)

@@ -109,6 +109,11 @@ def test_norm_overlaps(lib):
     ptrs = P[:13]
     ptrs[11] = ptrs[10]
     assert norm(lib, ptrs, n=6) == INVALID and "dwq" in message(lib)
+    ptrs[11] = ptrs[10] + 64 * 4 - 16
+    assert norm(lib, ptrs, n=6) == INVALID and "dwq" in message(lib)
+    # heads of one tensor [B][heads][N][d]: not one head too close
+    outer = [(10 * 64 * 8, 64, 640)] * 2
+    assert norm(lib, [*P[:2], P[8], P[8] + 3 * 640 * 2, *P[4:8]], strides(2, 10, 4, 2, 64) + outer) == INVALID
     assert norm(lib, P[:12] + [None], n=6) == INVALID and "null" in message(lib)
     need = lib.fa_qk_norm_rope_bwd_workspace_size(64)
     assert need > 0 and lib.fa_qk_norm_rope_bwd_workspace_size(60) == 0 and lib.fa_qk_norm_rope_bwd_workspace_size(512) == 0
