@@ -823,6 +823,20 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     int oq = 0;  // items with a result: O phases
     uint32_t stg_uses = 0;  // TMA stores from this warpgroup's staging box (all items)
     bool ok = start_ok;
+    // this thread's row of O in TMEM times f
+    auto rescale_o = [&](uint32_t col, uint32_t lanes, float f) {
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        const uint32_t ta = tmem_addr(tbase, lanes, col + c * 32);
+        tmem_ld32(ta, r);
+        tmem_wait_ld();
+        reg_fence(r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+        tmem_st32(ta, r);
+      }
+    };
     for (int r = 0, item = next_item(0, ok); ok && item >= 0; item = next_item(++r, ok)) {
       const Item w = item_at(item);
       const int head = w.head;
@@ -870,6 +884,73 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(sbar, sparity, ctx, 30 + q));
         if (!ok) break;
         tc_fence_after();
+        [[maybe_unused]] int seen = BN;  // (window) columns of a tile that lies in front of all rows' windows: the sinks in it
+        if constexpr (WINDOW) {
+          if (w.qrow0 + q * BM - window + 1 >= (tile_at(w, j) + 1) * BN) seen = max(0, min(BN, sinks - tile_at(w, j) * BN));
+        }
+        if constexpr (WINDOW) {
+          if (seen <= 32) {
+            // A tile of a few sinks, or of none (the second query tile's first): 32 columns instead of 128 and zeros for the others,
+            // where loading, masking and exponentials of a whole row cost the softmax 1.9 tiles.
+            float s[32];
+            uint32_t sr[32];
+            tmem_ld32(tmem_addr(tbase, lane_base, s_col), sr);
+            tmem_wait_ld();
+            reg_fence(sr);
+            if constexpr (C::SEP_P) {
+              tc_fence_before();
+              mbar_arrive(B.s_free + q);
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] = c < seen ? __uint_as_float(sr[c]) : -INFINITY;
+            const float m_blk = row_max3(s) * st;
+            float alpha = 1.f;
+            bool rescale = false;
+            if (m == -INFINITY) {
+              m = m_blk;
+              alpha = 0.f;
+            } else if (m_blk > m + kRescaleThreshold) {
+              alpha = ex2(m - m_blk);
+              m = m_blk;
+              rescale = true;
+            }
+            const float neg_m = m == -INFINITY ? 0.f : -m;
+            if constexpr (C::SEP_P) {
+              if (t > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(B.pv_q + q, (t - 1) & 1, ctx, 36 + q));
+                if (!ok) break;
+                tc_fence_after();
+              }
+            }
+            const uint32_t p_col = C::SEP_P ? (q ? C::P_COL1 : C::P_COL0) : s_col;
+            float2 part = make_float2(0.f, 0.f);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = ffma2(make_float2(s[2 * i], s[2 * i + 1]), st, neg_m);
+              const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+              part = fadd2(part, pp);
+              pk[i] = pack2<BF16>(pp.x, pp.y);
+            }
+            tmem_st16(tmem_addr(tbase, lane_base, p_col), pk);
+            const uint32_t zero[16] = {};
+#pragma unroll
+            for (int h = 1; h < BN / 32; ++h) tmem_st16(tmem_addr(tbase, lane_base, p_col + h * 16), zero);
+            l = l * alpha + part.x + part.y;
+            if (__any_sync(0xffffffffu, rescale)) {
+              if constexpr (C::NQ == 1) {
+                ok = __all_sync(0xffffffffu, mbar_wait(B.pv_done, (t - 1) & 1, ctx, 34));
+                if (!ok) break;
+                tc_fence_after();
+              }
+              rescale_o(o_col, lane_base, rescale ? alpha : 1.f);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(B.p_full + (C::NQ == 2 ? q : (t & 1)));
+            continue;
+          }
+        }
         // whole S row: all TMEM loads in flight before one wait
         uint32_t sr[BN / 32][32];
 #pragma unroll
@@ -898,13 +979,26 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
           }
           if (!((jflag[j] >> q) & 1)) hi = lo = 0;
         }
-        if constexpr (WINDOW) lo = row - window + 1 - jt * BN;
-        if (WINDOW && lo > 0 && sinks > jt * BN) {
-          // a tile of sinks (keys below `sinks` stay visible) behind which a window begins or that it has left
-          const int top = sinks - jt * BN;
+        if constexpr (WINDOW) {
+          lo = row - window + 1 - jt * BN;
+          if (lo > 0) {
+            // keys in front of the window, but for the sinks (which stay visible)
+            const int top = max(0, sinks - jt * BN);
+            if (top == 0) {
 #pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c >= hi || (c >= top && c < lo)) s[c] = -INFINITY;
+              for (int c = 0; c < BN; ++c)
+                if (c < lo) s[c] = -INFINITY;
+            } else {
+#pragma unroll
+              for (int c = 0; c < BN; ++c)
+                if (c >= top && c < lo) s[c] = -INFINITY;
+            }
+          }
+          if (hi < BN) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if (c >= hi) s[c] = -INFINITY;
+          }
         } else if (lo > 0 || hi < BN) {
 #pragma unroll
           for (int c = 0; c < BN; ++c)
@@ -977,18 +1071,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
             if (!ok) break;
             tc_fence_after();
           }
-          const float a = rescale ? alpha : 1.f;
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t r[32];
-            const uint32_t ta = tmem_addr(tbase, lane_base, o_col + c * 32);
-            tmem_ld32(ta, r);
-            tmem_wait_ld();
-            reg_fence(r);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * a);
-            tmem_st32(ta, r);
-          }
+          rescale_o(o_col, lane_base, rescale ? alpha : 1.f);
         }
         tmem_wait_st();
         tc_fence_before();
