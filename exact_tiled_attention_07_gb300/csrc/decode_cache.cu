@@ -364,6 +364,17 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  // the first 32 sequences' part of the list, summed up to each of them, for the producer's search
+  int64_t first32 = 0;
+  auto sum_up = [&](int64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    return v;
+  };
+  if (warp == C::PRODUCER_WARP) first32 = sum_up(lane < list.b ? list.own_total(lane) : 0);
   // the list's length: every thread adds up some sequences; CTA 0 leaves each one's offset for the finishing launch
   int64_t sum = 0;
   for (int s = threadIdx.x; s < list.b; s += C::THREADS) {
@@ -384,12 +395,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
   if (blockIdx.x == 0 && warp == C::DRAIN_WARP0) {
     int64_t at = pre_total;
     for (int s0 = 0; s0 < list.b; s0 += 32) {
-      int64_t v = s0 + lane < list.b ? list.own_total(s0 + lane) : 0;
-      const int64_t mine = v;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
+      const int64_t mine = s0 + lane < list.b ? list.own_total(s0 + lane) : 0, v = sum_up(mine);
       if (s0 + lane < list.b) a.ws.offsets[s0 + lane] = at + v - mine;
       at += __shfl_sync(0xffffffffu, v, 31);
     }
@@ -430,11 +436,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
       int64_t b_off = pre_total;
       const int64_t from = max(u0, pre_total);
       for (int s0 = 0; s0 < list.b && u1 > pre_total; s0 += 32) {
-        int64_t v = s0 + lane < list.b ? list.own_total(s0 + lane) : 0;
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += x;
-        }
+        const int64_t v = s0 == 0 ? first32 : sum_up(s0 + lane < list.b ? list.own_total(s0 + lane) : 0);
         const unsigned past = __ballot_sync(0xffffffffu, b_off + v > from);
         if (past) {
           const int f = __ffs(past) - 1;
