@@ -57,7 +57,8 @@ constexpr int kLoadRows = 16;   // rows of the loads that end a tile early
 constexpr int kSegCost = 3;
 constexpr int kSegs = 4;        // published segments, and row statistics, in flight
 constexpr int kFinishThreads = 128;
-constexpr int kMostSlots = 1024;  // segments that a row has in the prefix, at most (pieces + CTAs)
+constexpr int kListed = 64;  // slots of partial results that a warp lists at a time (a multiple of 32)
+constexpr int kAhead = 8;    // partial results whose loads a warp has in flight
 constexpr int kMostCtas = 512;
 constexpr int kFewSequences = 512;
 constexpr int kDrainBarrier = 1;  // named barrier of the four drain warps
@@ -912,172 +913,194 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
 }
 
 // Joins the segments of rows that have several: O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s, L = (M + log2 of the latter) ln 2, in
-// the list's order; rows that see nothing get O = 0, L = -inf; rows with one segment are finished.  A block takes a row (or
-// several one after the other, where there are many): D / 4 threads a partial result, kFinishThreads / (D / 4) results side
-// by side, several loads of each in flight (a warp a row, one result after the other: 7 to 24 us where this takes 4 to 6).
+// the list's order; rows that see nothing get O = 0, L = -inf; rows with one segment are finished.  A warp takes a row (or
+// several one after the other, where there are many): a lane four columns (at d = 64 half a warp every second partial
+// result, at d = 256 a lane eight columns), kAhead partial results in flight.  A block is small enough to stand beside one of the first
+// launch's CTAs, so that what can be known without its results is done when that one ends.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kFinishThreads)
-    decode_cache_finish(const __grid_constant__ CacheParams a, int grid, int rows, int rows_per_block) {
-  constexpr int CH = D / 4, WAYS = kFinishThreads / CH, AHEAD = 4;
-  __shared__ float4 sums[WAYS][CH];
-  __shared__ int slots[kMostSlots], head_n[3];
+    decode_cache_finish(const __grid_constant__ CacheParams a, int grid, int rows, int rows_per_warp) {
+  constexpr int WARPS = kFinishThreads / 32, CH = D / 4;
+  constexpr int WAYS = CH < 32 ? 32 / CH : 1, PER = CH > 32 ? CH / 32 : 1;  // results side by side, float4 columns of a lane
+  constexpr int AHEAD = kAhead / PER;
+  __shared__ int64_t part[2][WARPS];
+  __shared__ int slot_list[WARPS][kListed];
   const List& list = a.list;
-  const int lane = threadIdx.x & 31, col = threadIdx.x % CH, way = threadIdx.x / CH;
-  __shared__ int64_t part[2][kFinishThreads / 32];
-  bool waited = false;
-  int64_t total = 0, sums_before = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = lane % (CH < 32 ? CH : 32), way = lane / (CH < 32 ? CH : 32);
+  int* slots = slot_list[warp];
+  const int first = ((int)blockIdx.x * WARPS + warp) * rows_per_warp, end = min(rows, first + rows_per_warp);
+  const int b_block = (int)blockIdx.x * WARPS * rows_per_warp / a.gn / list.hkv;  // sequence of the block's first row
+  int64_t total = 0, own_off = 0;
   Prefix pre{};
   // The list of few sequences is looked at again here, before the wait for the kernel that wrote it down.
   const bool alone = list.b <= kFewSequences;
-  const int b0 = (int)blockIdx.x * rows_per_block / a.gn / list.hkv;  // of the first row
   if (alone) {
     int64_t all = 0, before = 0;
     for (int s = threadIdx.x; s < list.b; s += kFinishThreads) {
       const int64_t x = list.own_total(s);
       all += x;
-      if (s < b0) before += x;
+      if (s < b_block) before += x;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       all += __shfl_xor_sync(0xffffffffu, all, o);
       before += __shfl_xor_sync(0xffffffffu, before, o);
     }
-    if (lane == 0) part[0][threadIdx.x >> 5] = all, part[1][threadIdx.x >> 5] = before;
+    if (lane == 0) part[0][warp] = all, part[1][warp] = before;
     __syncthreads();
     all = before = 0;
 #pragma unroll
-    for (int k = 0; k < kFinishThreads / 32; ++k) all += part[0][k], before += part[1][k];
+    for (int k = 0; k < WARPS; ++k) all += part[0][k], before += part[1][k];
     if (list.p > 0) pre.set(list, all, grid);
     total = pre.total() + all;
-    sums_before = pre.total() + before;
+    own_off = pre.total() + before;
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    total = a.ws.offsets[list.b];
+    if (list.p > 0) pre.set(list, a.ws.offsets[list.b + 1], grid);
   }
-  int b_at = b0;  // sums_before is this sequence's offset
-  const int end = min(rows, ((int)blockIdx.x + 1) * rows_per_block);
-  for (int row = (int)blockIdx.x * rows_per_block; row < end; ++row) {
+  const int runs = runs_of(total, grid);
+  bool waited = !alone;
+  int b_at = b_block;  // (alone) own_off is this sequence's offset
+  for (int row = first; row < end; ++row) {
     const int bh = row / a.gn;  // sequence and key/value head
     const int w = row - bh * a.gn;
     const int b = bh / list.hkv, kvh = bh - b * list.hkv;
-    const int tiles = list.keys(list.len_of(b)).tiles;
-    if (!waited && !alone) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      waited = true;
-      total = a.ws.offsets[list.b];
-      if (list.p > 0) pre.set(list, a.ws.offsets[list.b + 1], grid);
+    if (alone) {
+      for (; b_at < b; ++b_at) own_off += list.own_total(b_at);
+    } else {
+      own_off = a.ws.offsets[b];
     }
-    for (; alone && b_at < b; ++b_at) sums_before += list.own_total(b_at);
-    const int64_t own_off = alone ? sums_before : a.ws.offsets[b];
-    const int runs = runs_of(total, grid);
-    // The segments of an entry: CTAs c0 to c1 have one each, in slots from the entry's number + c0 on.  Those of the prefix'
-    // pieces are listed first, in their order, by the first warp.
-    if (threadIdx.x < 32) {
+    // The segments of an entry: CTAs c0 to c1 have one each, in slots from the entry's number + c0 on; those of the prefix'
+    // pieces come first, in their order.
+    const int rt = (b * a.gn + w) / BM;
+    int n_pre = 0;
+    auto list_slots = [&](int base) {  // slots of the prefix' partial results base .. base + kListed - 1; how many there are in all
       int n = 0;
-      if (list.p > 0) {
-        const int rt = (b * a.gn + w) / BM;
-        for (int x0 = 0; x0 < pre.pieces; x0 += 32) {
-          const int x = x0 + lane, e = (kvh * pre.pieces + x) * list.rt_pre + rt;
-          int c0 = 0, mine = 0;
-          if (x < pre.pieces) {
-            const int64_t off = e * pre.cost() + kSegCost;
-            c0 = run_of(total, off, runs);
-            mine = run_of(total, off + pre.tiles_of(x) - 1, runs) - c0 + 1;
-          }
-          int end_ = mine;
+      for (int x0 = 0; x0 < pre.pieces; x0 += 32) {
+        const int x = x0 + lane, e = (kvh * pre.pieces + x) * list.rt_pre + rt;
+        int c0 = 0, mine = 0;
+        if (x < pre.pieces) {
+          const int64_t off = e * pre.cost() + kSegCost;
+          c0 = run_of(total, off, runs);
+          mine = run_of(total, off + pre.tiles_of(x) - 1, runs) - c0 + 1;
+        }
+        int upto = mine;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, end_, o);
-            if (lane >= o) end_ += y;
-          }
-          for (int k = 0; k < mine; ++k)
-            if (n + end_ - mine + k < kMostSlots) slots[n + end_ - mine + k] = e + c0 + k;
-          n += __shfl_sync(0xffffffffu, end_, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
         }
-      }
-      if (lane == 0) {
-        head_n[0] = min(n, kMostSlots);
-        int own_n = 0, slot = 0;
-        if (tiles > 0) {
-          const int e = kvh * list.rt_own + w / BM;
-          const int64_t off = own_off + e * List::cost(tiles) + kSegCost;
-          const int c0 = run_of(total, off, runs);
-          own_n = run_of(total, off + tiles - 1, runs) - c0 + 1;
-          slot = b * list.hkv * list.rt_own + e + c0;
+        for (int k = 0; k < mine; ++k) {
+          const int i = n + upto - mine + k - base;
+          if (i >= 0 && i < kListed) slots[i] = e + c0 + k;
         }
-        head_n[1] = own_n;
-        head_n[2] = slot;
+        n += __shfl_sync(0xffffffffu, upto, 31);
       }
+      __syncwarp();
+      return n;
+    };
+    if (list.p > 0) n_pre = list_slots(0);
+    int own_n = 0, own_slot = 0;
+    const int tiles = list.keys(list.len_of(b)).tiles;
+    if (tiles > 0) {
+      const int e = kvh * list.rt_own + w / BM;
+      const int64_t off = own_off + e * List::cost(tiles) + kSegCost;
+      const int c0 = run_of(total, off, runs);
+      own_n = run_of(total, off + tiles - 1, runs) - c0 + 1;
+      own_slot = b * list.hkv * list.rt_own + e + c0;
     }
-    __syncthreads();
     if (!waited) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
       waited = true;
     }
-    const int n_pre = head_n[0], n = n_pre + head_n[1];  // partial results
-    const int own_slot = head_n[2];
-    const bool finished = n == 1 && list.p == 0;
-    auto load = [&](int i, float4* x, float2* ml) {
-      const bool own = i >= n_pre;
-      const int64_t slot = own ? own_slot + i - n_pre : slots[i];
-      const int lanes = own ? a.ws.own_lanes : a.ws.pre_lanes, at = own ? w % BM : (b * a.gn + w) % BM;
-      if (x) *x = (own ? a.ws.own_o : a.ws.pre_o)[(slot * CH + col) * lanes + at];
-      *ml = (own ? a.ws.own_ml : a.ws.pre_ml)[slot * lanes + at];
-    };
-    if (finished) {
-      __syncthreads();
-      continue;
-    }
-    // this thread's results are way, way + WAYS, ...: the first ones' O on the way while every warp takes the statistics of all
-    float4 x[AHEAD];
-    float2 xm[AHEAD];
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      const int i = way + j * WAYS;
-      xm[j] = make_float2(-INFINITY, 0.f);
-      if (i < n) load(i, &x[j], &xm[j]);
-    }
+    const int n = n_pre + own_n;  // partial results
+    if (n == 1 && list.p == 0) continue;
+    const int pre_at = (b * a.gn + w) % BM, own_at = w % BM;
     float M = -INFINITY, l = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
+    float4 acc[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = 0; base < n; base += 32) {
+      // (the list holds kListed slots of the prefix)
+      if (base > 0 && base % kListed == 0 && base < n_pre) {
+        __syncwarp();
+        list_slots(base);
+      }
+      const int m = min(32, n - base);
+      auto o_at = [&](int i) {  // O of result base + i, this lane's first column
+        i += base;
+        const bool own = i >= n_pre;
+        const int64_t slot = own ? own_slot + i - n_pre : slots[i % kListed];
+        const int lanes = own ? a.ws.own_lanes : a.ws.pre_lanes;
+        return (own ? a.ws.own_o : a.ws.pre_o) + (slot * CH + col) * lanes + (own ? own_at : pre_at);
+      };
+      // the first results' O on the way while the statistics of all come
+      float4 x[AHEAD][PER];
+      auto load = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          const int i = i0 + j * WAYS + way;
+          if (i < m) {
+            const float4* o = o_at(i);
+            const int lanes = base + i >= n_pre ? a.ws.own_lanes : a.ws.pre_lanes;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) x[j][k] = o[(int64_t)32 * k * lanes];
+          }
+        }
+      };
+      load(0);
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (i0 + lane < n) load(i0 + lane, nullptr, &ml);
+      if (lane < m) {
+        const int i = base + lane;
+        const bool own = i >= n_pre;
+        const int64_t slot = own ? own_slot + i - n_pre : slots[i % kListed];
+        ml = own ? a.ws.own_ml[slot * a.ws.own_lanes + own_at] : a.ws.pre_ml[slot * a.ws.pre_lanes + pre_at];
+      }
       float top = fmaxf(M, ml.x);
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-      l = M == -INFINITY ? l : l * ex2(M - top);
+      const float old = M == -INFINITY ? 1.f : ex2(M - top);  // (nothing yet: sums of 0, or of NaN)
       M = top;
-      // (a row of NaN scores has m = -inf and l = NaN)
-      float add = ml.x == -INFINITY ? ml.y : ex2(ml.x - top) * ml.y;
+      // what saw nothing (m = -inf, l = 0) is left out, whatever its O holds; a row of NaN scores has m = -inf and l = NaN
+      const unsigned there = __ballot_sync(0xffffffffu, ml.x != -INFINITY || !(ml.y == 0.f));
+      const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - top);
+      float add = f * ml.y;
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
-      l += add;
-    }
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = way; i0 < n; i0 += AHEAD * WAYS) {
+      l = l * old + add;
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        // what saw nothing (m = -inf, l = 0) is left out, whatever its O holds
-        const bool there = xm[j].x != -INFINITY || !(xm[j].y == 0.f);
-        const float f = xm[j].x == -INFINITY ? 1.f : ex2(xm[j].x - M);
-        if (there)
-          acc.x = fmaf(f, x[j].x, acc.x), acc.y = fmaf(f, x[j].y, acc.y), acc.z = fmaf(f, x[j].z, acc.z), acc.w = fmaf(f, x[j].w, acc.w);
-        const int i = i0 + (j + AHEAD) * WAYS;
-        xm[j] = make_float2(-INFINITY, 0.f);
-        if (i < n) load(i, &x[j], &xm[j]);
+      for (int k = 0; k < PER; ++k) acc[k].x *= old, acc[k].y *= old, acc[k].z *= old, acc[k].w *= old;
+      for (int i0 = 0; i0 < m; i0 += AHEAD * WAYS) {
+        if (i0 > 0) load(i0);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          const int i = i0 + j * WAYS + way;
+          const float fi = __shfl_sync(0xffffffffu, f, i & 31);
+          if (i < m && ((there >> i) & 1)) {
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+              acc[k].x = fmaf(fi, x[j][k].x, acc[k].x), acc[k].y = fmaf(fi, x[j][k].y, acc[k].y),
+              acc[k].z = fmaf(fi, x[j][k].z, acc[k].z), acc[k].w = fmaf(fi, x[j][k].w, acc[k].w);
+          }
+        }
       }
     }
-    sums[way][col] = acc;
-    __syncthreads();
+    if constexpr (WAYS == 2) {
+      acc[0].x += __shfl_xor_sync(0xffffffffu, acc[0].x, 16), acc[0].y += __shfl_xor_sync(0xffffffffu, acc[0].y, 16);
+      acc[0].z += __shfl_xor_sync(0xffffffffu, acc[0].z, 16), acc[0].w += __shfl_xor_sync(0xffffffffu, acc[0].w, 16);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // (nothing visible: O = 0)
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (int64_t)row * D);
     if (way == 0) {
 #pragma unroll
-      for (int k = 1; k < WAYS; ++k) {
-        const float4 y = sums[k][col];
-        acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // (nothing visible: O = 0)
-      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (int64_t)row * D)[col] =
-          make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-      if (col == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+      for (int k = 0; k < PER; ++k)
+        dst[col + 32 * k] = make_uint2(pack2<BF16>(acc[k].x * inv, acc[k].y * inv), pack2<BF16>(acc[k].z * inv, acc[k].w * inv));
     }
-    __syncthreads();  // (the next row's sums)
+    if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    __syncwarp();  // (the next row's slots)
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D, bool BF16>
@@ -1117,8 +1140,9 @@ cudaError_t launch_d(const CacheDecodeArgs& a) {
   kern<<<grid, C::THREADS, C::SMEM, a.stream>>>(p, tk, tv, tk16, tv16, tkp, tvp, tkp16, tvp16);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the runs are still going (it waits for them before it reads what they write)
-  // (several rows a block only where single ones would be many more blocks than the GPU holds)
-  const int rows = a.b * a.h * a.nq, per_block = std::max(1, std::min(16, rows / (grid * 16)));
+  // (several rows a warp only where single ones would be many more warps than the GPU holds)
+  const int rows = a.b * a.h * a.nq, per_warp = std::max(1, std::min(16, rows / (grid * 64)));
+  const int per_block = per_warp * (kFinishThreads / 32);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((rows + per_block - 1) / per_block));
   cfg.blockDim = dim3(kFinishThreads);
@@ -1128,7 +1152,7 @@ cudaError_t launch_d(const CacheDecodeArgs& a) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_cache_finish<D, BF16>, p, grid, rows, per_block);
+  return cudaLaunchKernelEx(&cfg, decode_cache_finish<D, BF16>, p, grid, rows, per_warp);
 }
 
 }  // namespace
