@@ -822,6 +822,10 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 1)
         tmem_ld32(tmem_addr(tbase, lane_base, C::O_COL + c * 32), r);
         tmem_wait_ld();
         reg_fence(r);
+        if (R == 1 && g.whole && ml.y == 0.f) {  // a row that sees nothing: 0, also where V is not finite (0 x NaN)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
         if (c == D / 32 - 1) {  // all of O is in registers or gone: the next segment may overwrite it
           tc_fence_before();
           mbar_arrive(o_empty);

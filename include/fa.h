@@ -245,9 +245,10 @@ FA_API fa_status fa_bwd_masked(const void* Q, const void* K, const void* V, cons
  * Causal attention with a sliding window and a few first keys (sinks) that stay visible: query i sees key j when j <= i
  * and (i - j < window or j < sinks). Layouts, grouped heads, workspace and errors as fa_fwd_gqa / fa_bwd_gqa; window >= 1,
  * sinks >= 0 (either may exceed N: a window of N or more is causal attention). bf16 and fp16 with d in {64, 128, 256}; others
- * return FA_ERR_UNSUPPORTED. Key tiles outside the window and the sinks are neither loaded nor multiplied. (Inside a 128-row tile
- * that is visible in part, a hidden key's weight is an exact zero, as in fa_fwd: a V row that is not finite reaches the
- * queries whose 128-row tiles meet its tile.) One launch forward, the three of fa_bwd backward.
+ * return FA_ERR_UNSUPPORTED. Key tiles outside the window and the sinks are neither loaded nor multiplied. (Inside a tile
+ * of 128 keys that is visible in part, a hidden key's weight is an exact zero, as in fa_fwd: a V row that is not finite reaches
+ * every query of a block of 256, at d = 256 of 128, in which some query sees a key of its tile.) One launch forward, the
+ * three of fa_bwd backward.
  */
 FA_API fa_status fa_fwd_window(const void* Q, const void* K, const void* V, void* O, float* L, int B, int H, int Hkv,
                                int N, int d, float scale, int window, int sinks, fa_dtype dtype, void* stream);

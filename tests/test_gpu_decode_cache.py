@@ -278,3 +278,14 @@ def test_another_workspace_and_outputs_keep_their_neighbours(fa):
     check(q, k, v, lens, o[1:3], lse[1:3], d ** -0.5, prefix=prefix)
     assert (o[0] == 7).all() and (o[3] == 7).all() and (lse[0] == 9).all() and (lse[3] == 9).all()
     assert (ws[:256] == 3).all() and (ws[256 + n:] == 3).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [2, 32])
+def test_rows_that_see_nothing_are_zero_whatever_the_values_are(fa, d, H):
+    """Rows in front of the sequence's first token, with values that are not finite in slots that later rows see."""
+    q, k, v, lens, _ = make([3, 9], H, 2, 9, d, "bf16", 16)
+    v[0, :, 1], v[0, :, 2] = math.inf, math.nan
+    o, lse = fa.attention_decode_window(q, k, v, lens)
+    assert (o[0, :, :6] == 0).all() and (lse[0, :, :6] == -math.inf).all() and lse[0, :, 6:].isfinite().all()
+    check(q[1:], k[1:], v[1:], lens[1:], o[1:], lse[1:], d ** -0.5)
