@@ -866,17 +866,19 @@ def _warn_cuda_core(pass_, t, d):
 
 
 def _sinks_allowed(causal, window, sinks, block_mask=None):
-    """Whether a call is one of a window with sinks (fa_fwd_window and its kind)."""
+    """Whether a call is one of a window with sinks (fa_fwd_window and its kind): sinks given, 0 as well where it is such a window."""
+    good = causal and window >= 1 and block_mask is None
     if not sinks:
-        return False
-    if not causal or window < 1 or block_mask is not None:
+        return sinks is not None and good
+    if not good:
         raise ValueError("sinks go with causal attention and a window, without a block mask")
     return True
 
 
-def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, block_mask=None, sinks=0):
+def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, block_mask=None, sinks=None):
     """O, L = fa_fwd(q, k, v) (fa_fwd_gqa when k, v have fewer heads than q; fa_fwd_masked with a
-    window or a block mask; fa_fwd_window with a window, causal, and sinks); outputs on q's device."""
+    window or a block mask; fa_fwd_window with a window, causal, and sinks given, which may be 0); outputs on q's
+    device."""
     if _sinks_allowed(causal, window, sinks, block_mask):
         shape = _window_shape(q, k, v)
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -901,9 +903,9 @@ def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, 
 
 
 def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=None, stream=None, window=0,
-                       block_mask=None, sinks=0):
+                       block_mask=None, sinks=None):
     """dQ, dK, dV = fa_bwd(...) (fa_bwd_masked with a window or a block mask; fa_bwd_window with a window
-    and sinks); outputs (and workspace, unless given) allocated with torch."""
+    and sinks, which may be 0); outputs (and workspace, unless given) allocated with torch."""
     if _sinks_allowed(causal, window, sinks, block_mask):
         lib, dt, dev = load_library(), q.dtype, q.device
         B, H, Hkv, N, d = _window_shape(q, k, v, (o, do), (), (lse,), (workspace,))

@@ -23,7 +23,8 @@ DEBUG_BUILD_DIR = os.path.join(HERE, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(HERE, "libfa_gb300_debug.so")
 
 SOURCES = ["api.cu", "simt.cu", "fwd_tc.cu", "bwd_tc.cu", "noalloc.cu", "decode.cu", "decode_tc.cu", "fp8.cu", "selftest.cu",
-           "pipeline.cu", "kv4.cu", "decode_kv4.cu", "norm_rope.cu", "decode_cache.cu"]
+           "pipeline.cu", "kv4.cu", "decode_kv4.cu", "norm_rope.cu", "decode_cache.cu",
+           "window_delta.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "--expt-relaxed-constexpr"]

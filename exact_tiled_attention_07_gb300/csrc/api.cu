@@ -414,6 +414,9 @@ fa_status bwd_main_impl(const void* Q, const void* K, const void* V, const void*
   a.heads = H;
   a.band = mask.band;
   a.sinks = mask.sinks;
+  if (a.band && window_delta_pays(N, a.window, a.sinks) &&
+      (st = launched(launch_window_delta(a), name)) != FA_OK)
+    return st;
   if (bwd_tc_supported(a.dtype, d)) return launched(launch_bwd_tc(a), "backward (tensor-core kernel)");
   return note_cuda_core_path(launched(launch_bwd_simt(a), "backward (CUDA-core kernels)"), "backward", dtype, d);
 }

@@ -328,6 +328,8 @@ cudaError_t launch_fwd_tc(const FwdArgs& a);
 cudaError_t launch_fwd_simt(const FwdArgs& a);
 cudaError_t launch_bwd_pre(const BwdArgs& a);
 cudaError_t launch_bwd_tc(const BwdArgs& a);
+bool window_delta_pays(int n, int window, int sinks);  // (band) D from the keys that each query sees, not from the rounded O
+cudaError_t launch_window_delta(const BwdArgs& a);
 cudaError_t launch_bwd_simt(const BwdArgs& a);
 cudaError_t launch_dq_convert(const BwdArgs& a);
 

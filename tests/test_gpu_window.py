@@ -268,3 +268,53 @@ def test_refusals(fa):
         fa.attention_forward(q.float(), k.float(), v.float(), causal=True, window=10, sinks=2)
     empty = [t[:, :, :0].contiguous() for t in (q, k, v)]
     assert fa.attention_forward(*empty, causal=True, window=10, sinks=2)[0].shape == (1, 2, 0, 64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("N,window,sinks", [(700, 1, 0), (700, 2, 0), (701, 4, 1), (700, 20, 12), (257, 1, 31), (130, 1000, 3), (256, 100, 90),
+                                            (1, 5, 0), (17, 3, 2)])
+def test_few_keys_in_sight(fa, dtype, d, N, window, sinks):
+    """dS = p (dP - D) where D does not come from the rounded O: dD = (2 ds) sum p |dP| + the error of dP."""
+    B, H, Hkv = 2, 4, 2
+    q, k, v, do = make(B, H, Hkv, N, d, dtype, N + window)
+    scale, e, G = d ** -0.5, EPS[dtype], H // Hkv
+    o, lse = fa.attention_forward(q, k, v, causal=True, window=window, sinks=sinks)
+    grads = fa.attention_backward(q, k, v, o, do, lse, causal=True, window=window, sinks=sinks)
+    fa.fa_check_device_error()
+    for b in range(B):
+        for h in range(Hkv):
+            mine = slice(h * G, (h + 1) * G)
+            q1, k1, v1, do1 = (x.double() for x in (q[b, mine], k[b, h], v[b, h], do[b, mine]))
+            ds = (d / 16 + 8) * 2.0 ** -23 * scale * float(q1.norm(dim=-1).max() * k1.norm(dim=-1).max()) + 2.0 ** -20
+            p = torch.softmax((q1 @ k1.T * scale).masked_fill(~visible(N, window, sinks), -math.inf), -1)
+            dp = do1 @ v1.T
+            g = p * (dp - (p * dp).sum(-1, keepdim=True))
+            dp_tol = (d / 16 + 8) * 2.0 ** -23 * do1.norm(dim=-1, keepdim=True) * v1.norm(dim=-1).max()
+            g_tol = (e + 2 * ds) * g.abs() + p * (2 * ds * (p * dp.abs()).sum(-1, keepdim=True) + 2 * dp_tol)
+            dq, dk = scale * (g @ k1), scale * (g.transpose(-1, -2) @ q1).sum(0)
+            close(grads[0][b, mine], (dq, e * dq.abs() + scale * (g_tol @ k1.abs()) + 2.0 ** -24))
+            close(grads[1][b, h], (dk, e * dk.abs() + scale * (g_tol.transpose(-1, -2) @ q1.abs()).sum(0) + 2.0 ** -24))
+
+
+def test_values_outside_a_small_window_do_not_reach_d(fa):
+    """D sums visible keys alone: a hidden value that is not finite leaves the gradients of the 256-query blocks
+    that do not see its tile of 128 keys, here all but the second.  (A query
+    here meets two tiles at most, whose shares of dQ add up to the same bits in either order.)"""
+    q, k, v, do = make(1, 2, 2, 600, 64, "bf16", 3)
+    o, lse = fa.attention_forward(q, k, v, causal=True, window=8, sinks=0)
+    want = fa.attention_backward(q, k, v, o, do, lse, causal=True, window=8, sinks=0)
+    v2 = v.clone()
+    v2[:, :, 300] = math.nan
+    got = fa.attention_backward(q, k, v2, o, do, lse, causal=True, window=8, sinks=0)
+    assert torch.equal(got[0][:, :, :256], want[0][:, :, :256]) and torch.equal(got[0][:, :, 512:], want[0][:, :, 512:])
+    assert got[0][:, :, 300:308].isnan().all()
+
+
+def test_sinks_given_as_0_are_a_window_alone(fa):
+    q, k, v, do = make(1, 4, 2, 500, 64, "fp16", 5)
+    o, lse = torch.empty_like(q), torch.empty(1, 4, 500, device="cuda")
+    fa.fa_fwd_window(q, k, v, o, lse, 0.125, 70, 0)
+    a = fa.attention_forward(q, k, v, causal=True, window=70, sinks=0)
+    assert torch.equal(a[0], o) and torch.equal(a[1], lse)
+    assert all(torch.equal(x, y) for x, y in zip(fa.attention_forward(q, k, v, window=70, sinks=0), fa.attention_forward(q, k, v, window=70)))
