@@ -782,12 +782,16 @@ def fa_qk_norm_rope_bwd_workspace_size(d) -> int:
 
 def fa_qk_norm_rope_bwd(dQo, dKo, Q, K, wq, wk, table, dQ, dK, dwq, dwk, positions=None, eps=1e-6, interleaved=False,
                         workspace=None, stream=None):
-    """Gradients of fa_qk_norm_rope: dQ, dK (as Q, K) and dwq, dwk ([d] of the weights' dtype, or None) from dQo, dKo."""
-    for w, dw in ((wq, dwq), (wk, dwk)):
-        if dw is not None and (dw.numel() != Q.shape[-1] or (w is not None and dw.dtype != w.dtype)):
-            raise ValueError("weight gradients must be [d] tensors of their weights' dtype")
-    if wq is None and wk is None and (dwq is not None or dwk is not None):
-        raise ValueError("a weight gradient without weights")
+    """Gradients of fa_qk_norm_rope: dQ, dK (as Q, K) and dwq, dwk ([d] of the weights' dtype, or None; where one
+    weight is None, of the other's) from dQo, dKo."""
+    weight = wk if wq is None else wq
+    for dw in (dwq, dwk):
+        if dw is None:
+            continue
+        if weight is None:
+            raise ValueError("a weight gradient without weights")
+        if dw.numel() != Q.shape[-1] or dw.dtype != weight.dtype:  # (the library takes one dtype for both weights)
+            raise ValueError("weight gradients must be [d] tensors of the weights' dtype")
     sizes = _norm_rope_sizes(Q, K, wq, wk, table, positions, eps, interleaved, (dQo, dKo, dQ, dK))
     _ready(dwq, dwk, workspace, strided=(Q,))
     _norm_rope_bwd(dQo, dKo, Q, K, wq, wk, table, positions, dQ, dK, dwq, dwk, workspace,
