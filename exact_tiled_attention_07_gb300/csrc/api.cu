@@ -368,7 +368,7 @@ fa_status fwd_impl(const void* Q, const void* K, const void* V, void* O, float* 
   FwdArgs a{Q, K, V, O, L, B * H, N, d, scale, causal ? 1 : 0, (int)dtype, syms.err, syms.counter,
             static_cast<cudaStream_t>(stream)};
   a.group = H / Hkv;
-  a.window = mask.window;
+  a.window = std::min(mask.window, N);  // (a longer one hides nothing more; kernels add it to row numbers in 32 bits)
   a.block_mask = mask.block_mask;
   a.mask_heads = mask.mask_heads;
   a.heads = H;
@@ -408,7 +408,7 @@ fa_status bwd_main_impl(const void* Q, const void* K, const void* V, const void*
   a.counter = syms.counter;
   a.stream = static_cast<cudaStream_t>(stream);
   a.group = H / Hkv;
-  a.window = mask.window;
+  a.window = std::min(mask.window, N);  // (a longer one hides nothing more; kernels add it to row numbers in 32 bits)
   a.block_mask = mask.block_mask;
   a.mask_heads = mask.mask_heads;
   a.heads = H;
