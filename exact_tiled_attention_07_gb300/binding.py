@@ -170,6 +170,13 @@ def _p(t):
     return t.data_ptr() if t is not None else None
 
 
+def _c_int(x):
+    """x for a C int of the library, one that does not fit as the nearest that does: a window or a count of that size is
+    past every length, or refused, either way.  (ctypes takes the low 32 bits: 2^32 sinks would be none.)"""
+    x = int(x)
+    return max(-0x80000000, min(x, 0x7FFFFFFF))
+
+
 def _shape4(t):
     if t.dim() != 4:
         raise ValueError(f"expected a [B, H, N, d] tensor, got shape {tuple(t.shape)}")
@@ -333,7 +340,7 @@ def fa_bwd_noalloc(Q, K, V, O, dO, L, dQ, dK, dV, scale, causal, stream=None):
 
 
 def fa_fwd_bwd_host_workspace_size(B, H, Hkv, N, d, dtype, chunk=0) -> int:
-    return int(load_library().fa_fwd_bwd_host_workspace_size(B, H, Hkv, N, d, DTYPE_CODES[dtype], int(chunk)))
+    return int(load_library().fa_fwd_bwd_host_workspace_size(B, H, Hkv, N, d, DTYPE_CODES[dtype], _c_int(chunk)))
 
 
 def fa_fwd_bwd_host(Q, K, V, dO, O, L, dQ, dK, dV, workspace, scale, causal, chunk=0, stream=None):
@@ -359,11 +366,11 @@ def fa_fwd_bwd_host(Q, K, V, dO, O, L, dQ, dK, dV, workspace, scale, causal, chu
     _on_device(workspace)
     _check(load_library().fa_fwd_bwd_host(_p(Q), _p(K), _p(V), _p(dO), _p(O), _p(L), _p(dQ), _p(dK), _p(dV),
                                           _p(workspace), workspace.numel() * workspace.element_size(), B, H, Hkv, N,
-                                          d, float(scale), int(bool(causal)), _dt(Q), int(chunk), _stream(stream)))
+                                          d, float(scale), int(bool(causal)), _dt(Q), _c_int(chunk), _stream(stream)))
 
 
 def fa_decode_workspace_size(B, H, Hkv, Nq, Nk, d, splits=0) -> int:
-    return int(load_library().fa_decode_workspace_size(B, H, Hkv, Nq, Nk, d, int(splits)))
+    return int(load_library().fa_decode_workspace_size(B, H, Hkv, Nq, Nk, d, _c_int(splits)))
 
 
 def fa_decode(Q, K, V, O, L, scale, splits=0, workspace=None, stream=None):
@@ -377,7 +384,7 @@ def fa_decode(Q, K, V, O, L, scale, splits=0, workspace=None, stream=None):
     if L.dtype != torch.float32 or L.numel() != B * H * Nq or not L.is_contiguous():
         raise ValueError("L must be a contiguous fp32 tensor of B*H*Nq elements")
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load_library().fa_decode(_p(Q), _p(K), _p(V), _p(O), _p(L), B, H, Hkv, Nq, Nk, d, float(scale), int(splits),
+    _check(load_library().fa_decode(_p(Q), _p(K), _p(V), _p(O), _p(L), B, H, Hkv, Nq, Nk, d, float(scale), _c_int(splits),
                                     _dt(Q), _p(workspace), nbytes, _stream(stream)))
 
 
@@ -446,7 +453,7 @@ def fa_fwd_masked(Q, K, V, O, L, scale, causal, window=0, block_mask=None, strea
     _rows(L, B * H * N)
     mp, mh = _mask_args(block_mask, H)
     _check(load_library().fa_fwd_masked(_p(Q), _p(K), _p(V), _p(O), _p(L), B, H, Hkv, N, d, float(scale),
-                                        int(bool(causal)), int(window), mp, mh, _dt(Q), _stream(stream)))
+                                        int(bool(causal)), _c_int(window), mp, mh, _dt(Q), _stream(stream)))
 
 
 def fa_bwd_masked(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, causal, window=0, block_mask=None, stream=None):
@@ -460,7 +467,7 @@ def fa_bwd_masked(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, causal, windo
     nbytes = workspace.numel() * workspace.element_size()
     _check(load_library().fa_bwd_masked(_p(Q), _p(K), _p(V), _p(O), _p(dO), _p(L), _p(dQ), _p(dK), _p(dV),
                                         _p(workspace), nbytes, B, H, Hkv, N, d, float(scale), int(bool(causal)),
-                                        int(window), mp, mh, _dt(Q), _stream(stream)))
+                                        _c_int(window), mp, mh, _dt(Q), _stream(stream)))
 
 
 def _window_shape(Q, K, V, q_like=(), kv_like=(), rows=(), more=()):
@@ -488,7 +495,7 @@ def fa_fwd_window(Q, K, V, O, L, scale, window, sinks=0, stream=None):
     """Causal forward with a sliding window and the first `sinks` keys always visible."""
     shape = _window_shape(Q, K, V, (O,), (), (L,))
     _check(load_library().fa_fwd_window(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), *shape,
-                                        float(scale), int(window), int(sinks), _dt(Q), _current(stream)))
+                                        float(scale), _c_int(window), _c_int(sinks), _dt(Q), _current(stream)))
 
 
 def fa_bwd_window(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, window, sinks=0, stream=None):
@@ -496,8 +503,8 @@ def fa_bwd_window(Q, K, V, O, dO, L, dQ, dK, dV, workspace, scale, window, sinks
     shape = _window_shape(Q, K, V, (O, dO, dQ), (dK, dV), (L,), (workspace,))
     _check(load_library().fa_bwd_window(Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), L.data_ptr(),
                                         dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), *shape, float(scale), int(window),
-                                        int(sinks), _dt(Q), _current(stream)))
+                                        workspace.numel() * workspace.element_size(), *shape, float(scale), _c_int(window),
+                                        _c_int(sinks), _dt(Q), _current(stream)))
 
 
 def _packed(t, what):
@@ -533,8 +540,8 @@ def _varlen_args(Q, K, V, O, L, cu_seqlens):
     if cu_seqlens.dim() != 1 or n < 1:
         raise ValueError("cu_seqlens must be an int32 tensor of S + 1 elements")
     _int32(cu_seqlens, n, "cu_seqlens")
-    return (Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), cu_seqlens.data_ptr(), n - 1, T, H, Hkv, d,
-            q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs)
+    return (Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), cu_seqlens.data_ptr(), _c_int(n - 1), T, H, Hkv,
+            d, q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs)
 
 
 def fa_fwd_varlen(Q, K, V, O, L, cu_seqlens, scale, causal, stream=None):
@@ -547,7 +554,7 @@ def fa_fwd_varlen(Q, K, V, O, L, cu_seqlens, scale, causal, stream=None):
 def fa_fwd_varlen_window(Q, K, V, O, L, cu_seqlens, scale, window, sinks=0, stream=None):
     """fa_fwd_varlen, causal, with a sliding window and the first `sinks` rows of each sequence always visible."""
     args = _varlen_args(Q, K, V, O, L, cu_seqlens)
-    _check(load_library().fa_fwd_varlen_window(*args, scale, int(window), int(sinks), _dt(Q), _current(stream)))
+    _check(load_library().fa_fwd_varlen_window(*args, scale, _c_int(window), _c_int(sinks), _dt(Q), _current(stream)))
 
 
 def _kv4_shape(cache):
@@ -652,7 +659,7 @@ def fa_kv4_evict(cache, weights, lens, keep, recent, out_cache, out_weights, out
     _int32(lens, B, "lens")
     _int32(out_lens, B, "out_lens")
     _int32(kept, B * Hkv * int(keep), "kept")
-    _check(load_library().fa_kv4_evict(_p(cache), _p(weights), _p(lens), int(keep), int(recent), _p(out_cache),
+    _check(load_library().fa_kv4_evict(_p(cache), _p(weights), _p(lens), _c_int(keep), _c_int(recent), _p(out_cache),
                                        _p(out_weights), _p(out_lens), _p(kept), B, Hkv, capacity, out_capacity, d,
                                        _current(stream)))
 
@@ -704,8 +711,8 @@ def fa_decode_window(Q, K, V, lens, O, L, scale, window=0, sinks=0, workspace=No
     _same(Q, O)
     _rows(L, O.numel() // max(1, O.shape[3]))
     ws = _cache_workspace(workspace, fa_decode_window_workspace_size(*shape), Q, stream)
-    _check(load_library().fa_decode_window(_p(Q), _p(K), _p(V), _p(lens), _p(O), _p(L), *shape, float(scale), int(window),
-                                           int(sinks), _dt(Q), _p(ws), ws.numel() * ws.element_size(), _current(stream)))
+    _check(load_library().fa_decode_window(_p(Q), _p(K), _p(V), _p(lens), _p(O), _p(L), *shape, float(scale), _c_int(window),
+                                           _c_int(sinks), _dt(Q), _p(ws), ws.numel() * ws.element_size(), _current(stream)))
 
 
 def fa_decode_prefix(Q, KP, VP, K, V, lens, O, L, scale, workspace=None, stream=None):
@@ -743,6 +750,8 @@ def _norm_rope_sizes(q, k, wq, wk, table, positions, eps, interleaved, more=()):
     ks = k.shape
     if len(ks) != len(shape) or ks[-1] != d or ks[:-2] != shape[:-2] or k.dtype != dt:
         raise ValueError("the keys must have the queries' batch, tokens, head dimension and dtype")
+    if max(B, N, H, ks[-2]) > 0x7FFFFFFF:
+        raise ValueError(f"too many rows for one call: {tuple(shape)} and {tuple(ks)}")
     for n, t in enumerate(more):
         if t.shape != (ks if n & 1 else shape) or t.dtype != dt:
             raise ValueError("outputs and gradients must have their rows' heads, shape and dtype")
@@ -760,7 +769,7 @@ def _norm_rope_sizes(q, k, wq, wk, table, positions, eps, interleaved, more=()):
     _ready(wq, wk, table, positions, strided=(q, k, *more))
     if wdt not in DTYPE_CODES or dt not in DTYPE_CODES:
         raise ValueError(f"unsupported dtype {dt} or {wdt}")
-    return (B, N, H, ks[-2], d, rotary, bool(interleaved), length, float(eps), DTYPE_CODES[dt], DTYPE_CODES[wdt])
+    return (B, N, H, ks[-2], d, rotary, bool(interleaved), _c_int(length), float(eps), DTYPE_CODES[dt], DTYPE_CODES[wdt])
 
 
 _Strides4, _Strides6 = ctypes.c_int64 * 12, ctypes.c_int64 * 18
@@ -888,7 +897,7 @@ def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, 
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
         _check(load_library().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), *shape,
-                                            shape[4] ** -0.5 if scale is None else float(scale), int(window), int(sinks),
+                                            shape[4] ** -0.5 if scale is None else float(scale), _c_int(window), _c_int(sinks),
                                             _dt(q), _current(stream)))
         _used_on(stream, o, lse)
         return o, lse
@@ -922,7 +931,7 @@ def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=
         _check(lib.fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                                  dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), B, H, Hkv, N, d,
-                                 d ** -0.5 if scale is None else float(scale), int(window), int(sinks), _dt(q),
+                                 d ** -0.5 if scale is None else float(scale), _c_int(window), _c_int(sinks), _dt(q),
                                  _current(stream)))
         _used_on(stream, dq, dk, dv)
         return dq, dk, dv
@@ -997,7 +1006,7 @@ def attention_decode_window(q, k, v, lens, window=0, sinks=0, scale=None, stream
     nbytes = lib.fa_decode_window_workspace_size(*shape)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check(lib.fa_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), *shape,
-                                d ** -0.5 if scale is None else float(scale), int(window), int(sinks), _dt(q),
+                                d ** -0.5 if scale is None else float(scale), _c_int(window), _c_int(sinks), _dt(q),
                                 ws.data_ptr(), nbytes, _current(stream)))
     _used_on(stream, o, lse, ws)
     return o, lse

@@ -18,3 +18,12 @@ def test_a_weight_gradient_without_its_own_weight_has_the_other_weights_dtype(wh
     grads[1 - which] = torch.zeros(64)
     with pytest.raises(ValueError, match="CUDA"):  # nothing else is wrong with it
         fa.fa_qk_norm_rope_bwd(q, k, q, k, *weights, t, q, k, *grads)
+
+
+def test_more_rows_than_a_c_int_counts_are_refused():
+    """(ctypes takes the low 32 bits: 2^32 + 5 tokens would be 5.)"""
+    many = torch.zeros(1).expand(2 ** 32 + 5, 1, 8)
+    with pytest.raises(ValueError, match="too many rows"):
+        fa.qk_norm_rope(many, many, None, None, None)
+    with pytest.raises(ValueError, match="too many rows"):
+        fa.qk_norm_rope_backward(many, many, many, many, None, None, None, out=(many, many))
