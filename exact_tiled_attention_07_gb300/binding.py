@@ -5,6 +5,10 @@ device pointers; shapes come from the tensors.  Nothing here computes: each
 call checks the tensors, hands their pointers to ``libfa_gb300.so`` and turns a
 non-OK status into ``FAError``.  If the library was not built the first call
 raises: there is no fallback path.
+
+``stream``: a torch stream or a handle; None is the current stream.  A call runs there without waiting for the current
+stream: its inputs must be ready on it and stay until it is done.  Results that it allocates are ready on that stream and may be
+used on the current one, too, once that has waited.
 """
 
 from __future__ import annotations
@@ -231,6 +235,26 @@ def _ready(*ts, strided=()):
 def _current(stream):
     """_stream after _ready (CUDA is up)."""
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else _stream(stream)
+
+
+def _new(shape, dtype, device, stream, scratch=False):
+    """A tensor for a call on `stream` (None: the current one) to fill.  It comes from that stream's memory: a block of the current
+    stream's may have been freed with kernels queued that still use it, which a call on another stream does not wait for.  What
+    is returned (all but scratch) is the current stream's to use as well, so its memory is not handed out again before
+    what that stream has queued by then."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _new_workspace(nbytes, device, stream):
+    return _new(nbytes, torch.uint8, device, stream, scratch=True)
 
 
 def _rows(L, n, what="L"):
@@ -620,9 +644,7 @@ def fa_decode_kv4(Q, cache, lens, O, L, scale, causal=False, weights_in=None, we
     _same(Q, O)
     _rows(L, O.numel() // O.shape[3])
     if workspace is None:
-        workspace = torch.empty(fa_decode_kv4_workspace_size(*shape, weights_out is not None), dtype=torch.uint8,
-                                device=Q.device)
-        _used_on(stream, workspace)
+        workspace = _new_workspace(fa_decode_kv4_workspace_size(*shape, weights_out is not None), Q.device, stream)
     nbytes = workspace.numel() * workspace.element_size()
     _check(load_library().fa_decode_kv4(_p(Q), _p(cache), _p(lens), _p(O), _p(L), _p(weights_in), _p(weights_out),
                                         *shape, float(scale), int(bool(causal)), _dt(Q), _p(workspace), nbytes,
@@ -695,13 +717,6 @@ def fa_decode_prefix_workspace_size(B, H, Hkv, Nq, P, capacity, d) -> int:
     return int(load_library().fa_decode_prefix_workspace_size(B, H, Hkv, Nq, P, capacity, d))
 
 
-def _cache_workspace(workspace, nbytes, Q, stream):
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
-        _used_on(stream, workspace)
-    return workspace
-
-
 def fa_decode_window(Q, K, V, lens, O, L, scale, window=0, sinks=0, workspace=None, stream=None):
     """Decode: Q, O [B, H, Nq, d] over caches K, V [B, Hkv, capacity, d] with lens [B] slots in use, the newest of them
     the Nq rows' own; window > 0: each row sees its `window` newest slots and the first `sinks`. L [B, H, Nq]. workspace: of
@@ -710,7 +725,7 @@ def fa_decode_window(Q, K, V, lens, O, L, scale, window=0, sinks=0, workspace=No
     _ready(O, L, Q, workspace)
     _same(Q, O)
     _rows(L, O.numel() // max(1, O.shape[3]))
-    ws = _cache_workspace(workspace, fa_decode_window_workspace_size(*shape), Q, stream)
+    ws = workspace if workspace is not None else _new_workspace(fa_decode_window_workspace_size(*shape), Q.device, stream)
     _check(load_library().fa_decode_window(_p(Q), _p(K), _p(V), _p(lens), _p(O), _p(L), *shape, float(scale), _c_int(window),
                                            _c_int(sinks), _dt(Q), _p(ws), ws.numel() * ws.element_size(), _current(stream)))
 
@@ -721,7 +736,7 @@ def fa_decode_prefix(Q, KP, VP, K, V, lens, O, L, scale, workspace=None, stream=
     _ready(O, L, Q, workspace)
     _same(Q, O)
     _rows(L, O.numel() // max(1, O.shape[3]))
-    ws = _cache_workspace(workspace, fa_decode_prefix_workspace_size(*shape), Q, stream)
+    ws = workspace if workspace is not None else _new_workspace(fa_decode_prefix_workspace_size(*shape), Q.device, stream)
     _check(load_library().fa_decode_prefix(_p(Q), _p(KP), _p(VP), _p(K), _p(V), _p(lens), _p(O), _p(L), *shape, float(scale),
                                            _dt(Q), _p(ws), ws.numel() * ws.element_size(), _current(stream)))
 
@@ -811,8 +826,7 @@ def fa_qk_norm_rope_bwd(dQo, dKo, Q, K, wq, wk, table, dQ, dK, dwq, dwk, positio
 def _norm_rope_bwd(dQo, dKo, Q, K, wq, wk, table, positions, dQ, dK, dwq, dwk, workspace, strides, sizes, stream):
     lib = load_library()
     if workspace is None:
-        workspace = torch.empty(lib.fa_qk_norm_rope_bwd_workspace_size(sizes[4]), dtype=torch.uint8, device=Q.device)
-        _used_on(stream, workspace)
+        workspace = _new_workspace(lib.fa_qk_norm_rope_bwd_workspace_size(sizes[4]), Q.device, stream)
     _check(lib.fa_qk_norm_rope_bwd(dQo.data_ptr(), dKo.data_ptr(), Q.data_ptr(), K.data_ptr(), _p(wq), _p(wk), _p(table),
                                    _p(positions), dQ.data_ptr(), dK.data_ptr(), _p(dwq), _p(dwk), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), _Strides6(*strides), *sizes,
@@ -894,18 +908,17 @@ def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, 
     device."""
     if _sinks_allowed(causal, window, sinks, block_mask):
         shape = _window_shape(q, k, v)
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        o = _new(q.shape, q.dtype, q.device, stream)
+        lse = _new(q.shape[:3], torch.float32, q.device, stream)
         _check(load_library().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), *shape,
                                             shape[4] ** -0.5 if scale is None else float(scale), _c_int(window), _c_int(sinks),
                                             _dt(q), _current(stream)))
-        _used_on(stream, o, lse)
         return o, lse
     B, H, N, d = _shape4(q)
     _warn_cuda_core("fwd", q, d)
     scale = d ** -0.5 if scale is None else scale
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    o = _new(q.shape, q.dtype, q.device, stream)
+    lse = _new((B, H, N), torch.float32, q.device, stream)
     if window or block_mask is not None:
         fa_fwd_masked(q, k, v, o, lse, scale, causal, window, block_mask, stream)
     elif k.shape[1] != H:
@@ -922,26 +935,22 @@ def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=
     if _sinks_allowed(causal, window, sinks, block_mask):
         lib, dt, dev = load_library(), q.dtype, q.device
         B, H, Hkv, N, d = _window_shape(q, k, v, (o, do), (), (lse,), (workspace,))
-        dq = torch.empty(q.shape, dtype=dt, device=dev)
-        dk, dv = torch.empty(k.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+        dq, dk, dv = (_new(shape, dt, dev, stream) for shape in (q.shape, k.shape, k.shape))
         ws = workspace
         if ws is None:
-            ws = torch.empty(max(lib.fa_bwd_workspace_size(B, H, N, d), 16), dtype=torch.uint8, device=dev)
-            _used_on(stream, ws)
+            ws = _new_workspace(max(lib.fa_bwd_workspace_size(B, H, N, d), 16), dev, stream)
         _check(lib.fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                                  dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), B, H, Hkv, N, d,
                                  d ** -0.5 if scale is None else float(scale), _c_int(window), _c_int(sinks), _dt(q),
                                  _current(stream)))
-        _used_on(stream, dq, dk, dv)
         return dq, dk, dv
     B, H, N, d = _shape4(q)
     _warn_cuda_core("bwd", q, d)
     scale = d ** -0.5 if scale is None else scale
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dq, dk, dv = (_new(t.shape, t.dtype, t.device, stream) for t in (q, k, v))
     if workspace is None:
-        nbytes = fa_bwd_workspace_size(B, H, N, d)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new_workspace(max(fa_bwd_workspace_size(B, H, N, d), 16), q.device, stream)
     if window or block_mask is not None:
         fa_bwd_masked(q, k, v, o, do, lse, dq, dk, dv, workspace, scale, causal, window, block_mask, stream)
     elif k.shape[1] != H:
@@ -956,10 +965,10 @@ def attention_decode(q, k, v, scale=None, splits=0, stream=None):
     B, H, Nq, d = _shape4(q)
     _, Hkv, Nk, _ = _shape4(k)
     scale = d ** -0.5 if scale is None else scale
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    o = _new(q.shape, q.dtype, q.device, stream)
+    lse = _new((B, H, Nq), torch.float32, q.device, stream)
     nbytes = fa_decode_workspace_size(B, H, Hkv, Nq, Nk, d, splits)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    ws = _new_workspace(nbytes, q.device, stream) if nbytes else None
     fa_decode(q, k, v, o, lse, scale, splits, ws, stream)
     return o, lse
 
@@ -972,26 +981,13 @@ def attention_forward_varlen(q, k, v, cu_seqlens, causal=False, scale=None, stre
     _sinks_allowed(causal, window, sinks)
     T, H, d, _, _ = _packed(q, "Q")
     scale = d ** -0.5 if scale is None else scale
-    o = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    o = _new((T, H, d), q.dtype, q.device, stream)
+    lse = _new((H, T), torch.float32, q.device, stream)
     if window:
         fa_fwd_varlen_window(q, k, v, o, lse, cu_seqlens, scale, window, sinks, stream)
     else:
         fa_fwd_varlen(q, k, v, o, lse, cu_seqlens, scale, causal, stream)
-    _used_on(stream, o, lse)
     return o, lse
-
-
-def _used_on(stream, *ts):
-    """Tensors allocated here on the current stream and used on `stream`: their memory must not go
-    to another tensor of the current stream before that use is over."""
-    if stream is None:
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    for t in ts:
-        if t is not None:
-            t.record_stream(stream)
 
 
 def attention_decode_window(q, k, v, lens, window=0, sinks=0, scale=None, stream=None):
@@ -1001,14 +997,13 @@ def attention_decode_window(q, k, v, lens, window=0, sinks=0, scale=None, stream
     lib = load_library()
     B, H, _, Nq, _, d = shape
     dev = q.device
-    o = torch.empty((B, H, Nq, d), dtype=q.dtype, device=dev)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    o = _new((B, H, Nq, d), q.dtype, dev, stream)
+    lse = _new((B, H, Nq), torch.float32, dev, stream)
     nbytes = lib.fa_decode_window_workspace_size(*shape)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = _new_workspace(nbytes, dev, stream)
     _check(lib.fa_decode_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(), *shape,
                                 d ** -0.5 if scale is None else float(scale), _c_int(window), _c_int(sinks), _dt(q),
                                 ws.data_ptr(), nbytes, _current(stream)))
-    _used_on(stream, o, lse, ws)
     return o, lse
 
 
@@ -1019,15 +1014,14 @@ def attention_decode_prefix(q, k_prefix, v_prefix, k, v, lens, scale=None, strea
     lib = load_library()
     B, H, _, Nq, _, _, d = shape
     dev = q.device
-    o = torch.empty((B, H, Nq, d), dtype=q.dtype, device=dev)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    o = _new((B, H, Nq, d), q.dtype, dev, stream)
+    lse = _new((B, H, Nq), torch.float32, dev, stream)
     nbytes = lib.fa_decode_prefix_workspace_size(*shape)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = _new_workspace(nbytes, dev, stream)
     _check(lib.fa_decode_prefix(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(),
                                 lens.data_ptr(), o.data_ptr(), lse.data_ptr(), *shape,
                                 d ** -0.5 if scale is None else float(scale), _dt(q), ws.data_ptr(), nbytes,
                                 _current(stream)))
-    _used_on(stream, o, lse, ws)
     return o, lse
 
 
@@ -1047,17 +1041,14 @@ def qk_norm_rope(q, k, q_weight, k_weight, table, positions=None, eps=1e-6, inte
     B, N, H, Hkv, d = sizes[:5]
     dt, dev = q.dtype, q.device
     if q.dim() == 4:
-        qo = torch.empty((B, H, N, d), dtype=dt, device=dev)
-        ko = torch.empty((B, Hkv, N, d), dtype=dt, device=dev)
+        qo, ko = _new((B, H, N, d), dt, dev, stream), _new((B, Hkv, N, d), dt, dev, stream)
         out = (H * N * d, d, N * d, Hkv * N * d, d, N * d)
     else:
-        qo = torch.empty((N, H, d), dtype=dt, device=dev)
-        ko = torch.empty((N, Hkv, d), dtype=dt, device=dev)
+        qo, ko = _new((N, H, d), dt, dev, stream), _new((N, Hkv, d), dt, dev, stream)
         out = (0, H * d, d, 0, Hkv * d, d)
     _check(load_library().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(table), _p(positions),
                                           qo.data_ptr(), ko.data_ptr(), _Strides4(*_token_rows(q), *_token_rows(k), *out),
                                           *sizes, _current(stream)))
-    _used_on(stream, qo, ko)
     return qo, ko
 
 
@@ -1069,10 +1060,8 @@ def qk_norm_rope_backward(dqo, dko, q, k, q_weight, k_weight, table, positions=N
     if out is not None:
         dq, dk = out
     else:
-        dt, dev = q.dtype, q.device
-        dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
-    dwq = None if q_weight is None else torch.empty(q_weight.shape, dtype=q_weight.dtype, device=q.device)
-    dwk = None if k_weight is None else torch.empty(k_weight.shape, dtype=k_weight.dtype, device=q.device)
+        dq, dk = (_new(t.shape, q.dtype, q.device, stream) for t in (q, k))
+    dwq, dwk = (None if w is None else _new(w.shape, w.dtype, q.device, stream) for w in (q_weight, k_weight))
     if dqo.dim() == 4 and dko.dim() == 4:  # [B, heads, N, d]
         sizes = _norm_rope_sizes(q, k, q_weight, k_weight, table, positions, eps, interleaved, (dq, dk))
         B, N, H, Hkv, d = sizes[:5]
@@ -1086,17 +1075,14 @@ def qk_norm_rope_backward(dqo, dko, q, k, q_weight, k_weight, table, positions=N
         outer = (*_token_rows(dqo), *_token_rows(dko))
     _norm_rope_bwd(dqo, dko, q, k, q_weight, k_weight, table, positions, dq, dk, dwq, dwk, None,
                    (*outer, *_token_rows(q), *_token_rows(k), *_token_rows(dq), *_token_rows(dk)), sizes, stream)
-    _used_on(stream, dwq, dwk, *(() if out is not None else (dq, dk)))
     return dq, dk, dwq, dwk
 
 
 def kv4_read(cache, cu_seqlens, lens, total, dtype=torch.bfloat16, stream=None):
     """k, v [total, Hkv, d] = fa_kv4_read(...): the values of the newest slots, packed."""
     _, Hkv, _, d = _kv4_shape(cache)
-    k = torch.empty((total, Hkv, d), dtype=dtype, device=cache.device)
-    v = torch.empty_like(k)
+    k, v = (_new((total, Hkv, d), dtype, cache.device, stream) for _ in range(2))
     fa_kv4_read(cache, cu_seqlens, lens, k, v, stream)
-    _used_on(stream, k, v)
     return k, v
 
 
@@ -1106,23 +1092,22 @@ def attention_decode_kv4(q, cache, lens, causal=False, scale=None, weights_in=No
     shape = B, H, Hkv, Nq, capacity, d = _kv4_decode_shape(q, cache, lens, weights_in, weights_out)
     lib = load_library()
     dev = q.device
-    o = torch.empty((B, H, Nq, d), dtype=q.dtype, device=dev)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    o = _new((B, H, Nq, d), q.dtype, dev, stream)
+    lse = _new((B, H, Nq), torch.float32, dev, stream)
     nbytes = lib.fa_decode_kv4_workspace_size(*shape, weights_out is not None)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    ws = _new_workspace(nbytes, dev, stream) if nbytes else None
     _check(lib.fa_decode_kv4(q.data_ptr(), cache.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr(),
                              _p(weights_in), _p(weights_out), *shape,
                              d ** -0.5 if scale is None else float(scale), int(bool(causal)), _dt(q), _p(ws), nbytes,
                              _current(stream)))
-    _used_on(stream, o, lse, ws)
     return o, lse
 
 
 def quantize_fp8(x, stream=None):
     """(codes, scales) = block quantisation of x [B, H, N, d] (one scale per 128 rows of a head)."""
     B, H, N, d = _shape4(x)
-    x8 = torch.empty((B, H, N, d), dtype=torch.uint8, device=x.device)
-    sc = torch.empty((B, H, (N + 127) // 128), dtype=torch.float32, device=x.device)
+    x8 = _new((B, H, N, d), torch.uint8, x.device, stream)
+    sc = _new((B, H, (N + 127) // 128), torch.float32, x.device, stream)
     fa_quantize_fp8(x, x8, sc, stream)
     return x8, sc
 
@@ -1132,7 +1117,7 @@ def attention_forward_fp8(q8, k8, v8, q_scales, k_scales, v_scales, scale=None, 
     """O, L = fa_fwd_fp8(...) on E4M3 codes and their block scales."""
     B, H, N, d = _shape4(q8)
     scale = d ** -0.5 if scale is None else scale
-    o = torch.empty((B, H, N, d), dtype=out_dtype, device=q8.device)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q8.device)
+    o = _new((B, H, N, d), out_dtype, q8.device, stream)
+    lse = _new((B, H, N), torch.float32, q8.device, stream)
     fa_fwd_fp8(q8, k8, v8, q_scales, k_scales, v_scales, o, lse, scale, causal, stream)
     return o, lse
