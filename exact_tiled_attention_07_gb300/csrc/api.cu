@@ -320,6 +320,7 @@ struct MaskSpec {
   bool band = false;  // causal with `window` and the first `sinks` keys always visible
   int sinks = 0;
   bool any() const { return window > 0 || block_mask != nullptr; }
+  int delta_rows(int n) const { return band ? window_delta_rows(n, window, sinks) : 0; }  // (backward) as in BwdArgs
 };
 
 fa_status check_band(int window, int sinks, const char* what) {
@@ -414,11 +415,30 @@ fa_status bwd_main_impl(const void* Q, const void* K, const void* V, const void*
   a.heads = H;
   a.band = mask.band;
   a.sinks = mask.sinks;
-  if (a.band && window_delta_pays(N, a.window, a.sinks) &&
-      (st = launched(launch_window_delta(a), name)) != FA_OK)
-    return st;
+  a.delta_rows = mask.delta_rows(N);
+  if (a.delta_rows > 0 && (st = launched(launch_window_delta(a), name)) != FA_OK) return st;
   if (bwd_tc_supported(a.dtype, d)) return launched(launch_bwd_tc(a), "backward (tensor-core kernel)");
   return note_cuda_core_path(launched(launch_bwd_simt(a), "backward (CUDA-core kernels)"), "backward", dtype, d);
+}
+
+fa_status bwd_pre_impl(const void* O, const void* dO, const float* L, void* workspace, size_t workspace_bytes, int B, int H,
+                       int N, int d, fa_dtype dtype, void* stream, const char* name, int delta_rows = 0) {
+  bool empty;
+  fa_status st = check_common(B, H, N, d, dtype, &empty);
+  if (st != FA_OK || empty) return st;
+  if ((st = check_ptrs({O, dO, L, workspace}, name)) != FA_OK) return st;
+  BwdArgs a{};
+  if ((st = carve(&a, workspace, workspace_bytes, B, H, N, d)) != FA_OK) return st;
+  a.o = O;
+  a.dout = dO;
+  a.lse = L;
+  a.bh = B * H;
+  a.n = N;
+  a.d = d;
+  a.dtype = (int)dtype;
+  a.delta_rows = delta_rows;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launched(launch_bwd_pre(a), name);
 }
 
 }  // namespace
@@ -443,21 +463,7 @@ size_t fa_bwd_workspace_size(int B, int H, int N, int d) {
 
 fa_status fa_bwd_preprocess(const void* O, const void* dO, const float* L, void* workspace, size_t workspace_bytes,
                             int B, int H, int N, int d, fa_dtype dtype, void* stream) {
-  bool empty;
-  fa_status st = check_common(B, H, N, d, dtype, &empty);
-  if (st != FA_OK || empty) return st;
-  if ((st = check_ptrs({O, dO, L, workspace}, "fa_bwd_preprocess")) != FA_OK) return st;
-  BwdArgs a{};
-  if ((st = carve(&a, workspace, workspace_bytes, B, H, N, d)) != FA_OK) return st;
-  a.o = O;
-  a.dout = dO;
-  a.lse = L;
-  a.bh = B * H;
-  a.n = N;
-  a.d = d;
-  a.dtype = (int)dtype;
-  a.stream = static_cast<cudaStream_t>(stream);
-  return launched(launch_bwd_pre(a), "fa_bwd_preprocess");
+  return bwd_pre_impl(O, dO, L, workspace, workspace_bytes, B, H, N, d, dtype, stream, "fa_bwd_preprocess");
 }
 
 fa_status fa_bwd_main(const void* Q, const void* K, const void* V, const void* dO, void* dK, void* dV,
@@ -558,7 +564,8 @@ fa_status fa_bwd_window(const void* Q, const void* K, const void* V, const void*
   if ((st = check_ptrs({Q, K, V, O, dO, L, dQ, dK, dV, workspace}, "fa_bwd_window")) != FA_OK) return st;
   if ((st = check_scale(scale)) != FA_OK) return st;
   if ((st = check_mask(m, H, Hkv, N, d, dtype, true)) != FA_OK) return st;
-  if ((st = fa_bwd_preprocess(O, dO, L, workspace, workspace_bytes, B, H, N, d, dtype, stream)) != FA_OK) return st;
+  if ((st = bwd_pre_impl(O, dO, L, workspace, workspace_bytes, B, H, N, d, dtype, stream, "fa_bwd_window", m.delta_rows(N))) != FA_OK)
+    return st;
   if ((st = bwd_main_impl(Q, K, V, dO, dK, dV, workspace, workspace_bytes, B, H, Hkv, N, d, scale, 1, dtype, stream,
                           "fa_bwd_window", m)) != FA_OK)
     return st;

@@ -75,6 +75,7 @@ struct BwdArgs {
   bool masked() const { return window > 0 || block_mask != nullptr; }
   bool band = false;  // as in FwdArgs
   int sinks = 0;
+  int delta_rows = 0;  // (16-bit, head dims 64/128/256) first rows of a sequence whose D launch_window_delta writes
 };
 
 // Decode over a key/value cache: Q, O [b][h][nq][d], K, V [b][hkv][nk][d], L [b][h][nq].
@@ -328,7 +329,7 @@ cudaError_t launch_fwd_tc(const FwdArgs& a);
 cudaError_t launch_fwd_simt(const FwdArgs& a);
 cudaError_t launch_bwd_pre(const BwdArgs& a);
 cudaError_t launch_bwd_tc(const BwdArgs& a);
-bool window_delta_pays(int n, int window, int sinks);  // (band) D from the keys that each query sees, not from the rounded O
+int window_delta_rows(int n, int window, int sinks);  // (band) first rows whose D comes from the keys they see, not from the rounded O
 cudaError_t launch_window_delta(const BwdArgs& a);
 cudaError_t launch_bwd_simt(const BwdArgs& a);
 cudaError_t launch_dq_convert(const BwdArgs& a);

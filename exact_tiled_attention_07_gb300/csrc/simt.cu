@@ -342,12 +342,14 @@ __global__ void __launch_bounds__(256) dq_convert(const float* __restrict__ dq_a
 }
 
 // Vectorised variants for 16-bit inputs with d % 8 == 0: each thread moves 16 bytes of
-// input (8 elements); a row of d elements is handled by d / 8 consecutive threads.
+// input (8 elements); a row of d elements is handled by d / 8 consecutive threads.  D of a sequence's first
+// `delta_rows` rows is another kernel's to write, and their O and dO are not read.
 template <typename T>
 __global__ void __launch_bounds__(256) bwd_pre_vec(const T* __restrict__ O, const T* __restrict__ dO,
                                                    const float* __restrict__ lse, float* __restrict__ delta,
                                                    float* __restrict__ lse2, float* __restrict__ dq_acc, int n,
-                                                   int npad, int d, int64_t total_rows, unsigned* __restrict__ sched) {
+                                                   int npad, int d, int64_t total_rows, unsigned* __restrict__ sched,
+                                                   int delta_rows) {
   if (sched && blockIdx.x == 0 && threadIdx.x < 2) sched[threadIdx.x] = 0u;  // the backward's item queue
   const int tpr = d / 8;  // threads per row: 8, 16 or 32 (power of two)
   const int64_t gt = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(256) bwd_pre_vec(const T* __restrict__ O, cons
   const int64_t bh = active ? grow / npad : 0;
   const int row = active ? (int)(grow - bh * npad) : 0;
   float acc = 0.f;
-  if (active && row < n) {
+  if (active && row < n && row >= delta_rows) {
     const int64_t off = (bh * n + row) * d + sub * 8;
     const uint4 a = *reinterpret_cast<const uint4*>(O + off);
     const uint4 b = *reinterpret_cast<const uint4*>(dO + off);
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(256) bwd_pre_vec(const T* __restrict__ O, cons
   for (int o = tpr >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   if (!active) return;
   if (sub == 0) {
-    delta[grow] = row < n ? acc : 0.f;
+    if (row >= delta_rows) delta[grow] = row < n ? acc : 0.f;
     const float lv = row < n ? lse[bh * n + row] : -INFINITY;
     lse2[grow] = lv > -INFINITY ? -lv * 1.4426950408889634f : -INFINITY;
   }
@@ -438,7 +440,8 @@ cudaError_t pre_t(const BwdArgs& a) {
   if (sizeof(T) == 2 && (a.d == 64 || a.d == 128 || a.d == 256)) {
     const int64_t threads = rows * (a.d / 8);
     bwd_pre_vec<T><<<(unsigned)((threads + 255) / 256), 256, 0, a.stream>>>(
-        (const T*)a.o, (const T*)a.dout, a.lse, a.delta, a.lse2, a.dq_acc, a.n, npad, a.d, rows, a.sched);
+        (const T*)a.o, (const T*)a.dout, a.lse, a.delta, a.lse2, a.dq_acc, a.n, npad, a.d, rows, a.sched,
+        a.delta_rows);
     return cudaGetLastError();
   }
   const int64_t blocks = (rows * 32 + 255) / 256;

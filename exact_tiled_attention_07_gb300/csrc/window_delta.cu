@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(THREADS)
 
 template <int D, bool BF16>
 cudaError_t launch_d(const BwdArgs& a) {
-  const int tiles = (a.n + ROWS - 1) / ROWS, smem = 2 * ROWS * D * 2;
+  const int tiles = (a.delta_rows + ROWS - 1) / ROWS, smem = 2 * ROWS * D * 2;
   auto kern = window_delta_kernel<D, BF16>;
   static std::atomic<unsigned long long> allowed;
   cudaError_t e = allow_smem(kern, smem, &allowed);
@@ -159,7 +159,7 @@ cudaError_t launch_d(const BwdArgs& a) {
 }  // namespace
 
 // Queries that see 32 keys or fewer, or short sequences: see above.
-bool window_delta_pays(int n, int window, int sinks) { return (int64_t)window + sinks <= 32 || n <= 256; }
+int window_delta_rows(int n, int window, int sinks) { return (int64_t)window + sinks <= 32 || n <= 256 ? n : 0; }
 
 cudaError_t launch_window_delta(const BwdArgs& a) {
   const bool bf = a.dtype == DT_BF16;
