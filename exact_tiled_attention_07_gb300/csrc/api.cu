@@ -320,7 +320,6 @@ struct MaskSpec {
   bool band = false;  // causal with `window` and the first `sinks` keys always visible
   int sinks = 0;
   bool any() const { return window > 0 || block_mask != nullptr; }
-  int delta_rows(int n) const { return band ? window_delta_rows(n, window, sinks) : 0; }  // (backward) as in BwdArgs
 };
 
 fa_status check_band(int window, int sinks, const char* what) {
@@ -415,8 +414,6 @@ fa_status bwd_main_impl(const void* Q, const void* K, const void* V, const void*
   a.heads = H;
   a.band = mask.band;
   a.sinks = mask.sinks;
-  a.delta_rows = mask.delta_rows(N);
-  if (a.delta_rows > 0 && (st = launched(launch_window_delta(a), name)) != FA_OK) return st;
   if (bwd_tc_supported(a.dtype, d)) return launched(launch_bwd_tc(a), "backward (tensor-core kernel)");
   return note_cuda_core_path(launched(launch_bwd_simt(a), "backward (CUDA-core kernels)"), "backward", dtype, d);
 }
@@ -439,6 +436,31 @@ fa_status bwd_pre_impl(const void* O, const void* dO, const float* L, void* work
   a.delta_rows = delta_rows;
   a.stream = static_cast<cudaStream_t>(stream);
   return launched(launch_bwd_pre(a), name);
+}
+
+// (window) D of a sequence's first `delta_rows` rows; in front of bwd_pre_impl with the same number.
+fa_status window_delta_impl(const void* Q, const void* K, const void* V, const void* dO, const float* L, void* workspace,
+                            size_t workspace_bytes, int B, int H, int Hkv, int N, int d, float scale, int window, int sinks,
+                            fa_dtype dtype, void* stream, int delta_rows) {
+  BwdArgs a{};
+  const fa_status st = carve(&a, workspace, workspace_bytes, B, H, N, d);
+  if (st != FA_OK) return st;
+  a.q = Q;
+  a.k = K;
+  a.v = V;
+  a.dout = dO;
+  a.lse = L;
+  a.bh = B * H;
+  a.n = N;
+  a.d = d;
+  a.scale = scale;
+  a.dtype = (int)dtype;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.group = H / Hkv;
+  a.window = std::min(window, N);
+  a.sinks = sinks;
+  a.delta_rows = delta_rows;
+  return launched(launch_window_delta(a), "fa_bwd_window");
 }
 
 }  // namespace
@@ -564,7 +586,11 @@ fa_status fa_bwd_window(const void* Q, const void* K, const void* V, const void*
   if ((st = check_ptrs({Q, K, V, O, dO, L, dQ, dK, dV, workspace}, "fa_bwd_window")) != FA_OK) return st;
   if ((st = check_scale(scale)) != FA_OK) return st;
   if ((st = check_mask(m, H, Hkv, N, d, dtype, true)) != FA_OK) return st;
-  if ((st = bwd_pre_impl(O, dO, L, workspace, workspace_bytes, B, H, N, d, dtype, stream, "fa_bwd_window", m.delta_rows(N))) != FA_OK)
+  const int delta_rows = window_delta_rows(N, window, sinks);
+  if ((st = window_delta_impl(Q, K, V, dO, L, workspace, workspace_bytes, B, H, Hkv, N, d, scale, window, sinks, dtype, stream,
+                              delta_rows)) != FA_OK)
+    return st;
+  if ((st = bwd_pre_impl(O, dO, L, workspace, workspace_bytes, B, H, N, d, dtype, stream, "fa_bwd_window", delta_rows)) != FA_OK)
     return st;
   if ((st = bwd_main_impl(Q, K, V, dO, dK, dV, workspace, workspace_bytes, B, H, Hkv, N, d, scale, 1, dtype, stream,
                           "fa_bwd_window", m)) != FA_OK)

@@ -75,7 +75,7 @@ struct BwdArgs {
   bool masked() const { return window > 0 || block_mask != nullptr; }
   bool band = false;  // as in FwdArgs
   int sinks = 0;
-  int delta_rows = 0;  // (16-bit, head dims 64/128/256) first rows of a sequence whose D launch_window_delta writes
+  int delta_rows = 0;  // (band) first rows of a sequence whose D launch_window_delta writes, right in front of launch_bwd_pre
 };
 
 // Decode over a key/value cache: Q, O [b][h][nq][d], K, V [b][hkv][nk][d], L [b][h][nq].

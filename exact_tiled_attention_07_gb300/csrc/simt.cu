@@ -342,9 +342,10 @@ __global__ void __launch_bounds__(256) dq_convert(const float* __restrict__ dq_a
 }
 
 // Vectorised variants for 16-bit inputs with d % 8 == 0: each thread moves 16 bytes of
-// input (8 elements); a row of d elements is handled by d / 8 consecutive threads.  D of a sequence's first
-// `delta_rows` rows is another kernel's to write, and their O and dO are not read.
-template <typename T>
+// input (8 elements); a row of d elements is handled by d / 8 consecutive threads.  DELTA: D of a sequence's first
+// `delta_rows` rows is written by the launch in front, beside which this one runs (neither reads what the other writes; it does not
+// end before that one, so that what follows waits for both), and their O and dO are not read.
+template <typename T, bool DELTA>
 __global__ void __launch_bounds__(256) bwd_pre_vec(const T* __restrict__ O, const T* __restrict__ dO,
                                                    const float* __restrict__ lse, float* __restrict__ delta,
                                                    float* __restrict__ lse2, float* __restrict__ dq_acc, int n,
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(256) bwd_pre_vec(const T* __restrict__ O, cons
   const int64_t bh = active ? grow / npad : 0;
   const int row = active ? (int)(grow - bh * npad) : 0;
   float acc = 0.f;
-  if (active && row < n && row >= delta_rows) {
+  if (active && row < n && (!DELTA || row >= delta_rows)) {
     const int64_t off = (bh * n + row) * d + sub * 8;
     const uint4 a = *reinterpret_cast<const uint4*>(O + off);
     const uint4 b = *reinterpret_cast<const uint4*>(dO + off);
@@ -369,15 +370,17 @@ __global__ void __launch_bounds__(256) bwd_pre_vec(const T* __restrict__ O, cons
     for (int i = 0; i < 8; ++i) acc = fmaf(ld(pa, i), ld(pb, i), acc);
   }
   for (int o = tpr >> 1; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (!active) return;
-  if (sub == 0) {
-    if (row >= delta_rows) delta[grow] = row < n ? acc : 0.f;
-    const float lv = row < n ? lse[bh * n + row] : -INFINITY;
-    lse2[grow] = lv > -INFINITY ? -lv * 1.4426950408889634f : -INFINITY;
+  if (active) {
+    if (sub == 0) {
+      if (!DELTA || row >= delta_rows) delta[grow] = row < n ? acc : 0.f;
+      const float lv = row < n ? lse[bh * n + row] : -INFINITY;
+      lse2[grow] = lv > -INFINITY ? -lv * 1.4426950408889634f : -INFINITY;
+    }
+    float4* q = reinterpret_cast<float4*>(dq_acc + grow * d + sub * 8);
+    q[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    q[1] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float4* q = reinterpret_cast<float4*>(dq_acc + grow * d + sub * 8);
-  q[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-  q[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (DELTA) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <typename T>
@@ -439,10 +442,23 @@ cudaError_t pre_t(const BwdArgs& a) {
   const int64_t rows = (int64_t)a.bh * npad;
   if (sizeof(T) == 2 && (a.d == 64 || a.d == 128 || a.d == 256)) {
     const int64_t threads = rows * (a.d / 8);
-    bwd_pre_vec<T><<<(unsigned)((threads + 255) / 256), 256, 0, a.stream>>>(
-        (const T*)a.o, (const T*)a.dout, a.lse, a.delta, a.lse2, a.dq_acc, a.n, npad, a.d, rows, a.sched,
-        a.delta_rows);
-    return cudaGetLastError();
+    const unsigned blocks = (unsigned)((threads + 255) / 256);
+    if (a.delta_rows == 0) {
+      bwd_pre_vec<T, false><<<blocks, 256, 0, a.stream>>>((const T*)a.o, (const T*)a.dout, a.lse, a.delta, a.lse2, a.dq_acc,
+                                                          a.n, npad, a.d, rows, a.sched, 0);
+      return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, bwd_pre_vec<T, true>, (const T*)a.o, (const T*)a.dout, a.lse, a.delta, a.lse2, a.dq_acc,
+                              a.n, npad, a.d, rows, a.sched, a.delta_rows);
   }
   const int64_t blocks = (rows * 32 + 255) / 256;
   bwd_pre<T><<<(unsigned)blocks, 256, 0, a.stream>>>((const T*)a.o, (const T*)a.dout, a.lse, a.delta, a.lse2,

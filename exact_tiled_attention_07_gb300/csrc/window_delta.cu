@@ -4,16 +4,23 @@
 // Why: dS_ij = P_ij (dP_ij - D_i).  With few keys in sight dP and D are of one size and nearly cancel (with one key they are
 // equal and dQ is 0), so that half a step of O is no longer small in dS.
 //
+// Which rows: all where window + sinks <= 32, else the 64 (a block) that each sequence begins with, as query i sees i + 1 keys at most.
+// What dQ is off, relative to its norm, by the number of keys that a query sees (bf16, d = 128; fp16 the same in its steps; its own rounding
+// is 0.0017 of it and that of dS as much again; dK the same within 0.0001):
+//                     2       3       4       6       8       12      16      24      32      48      64      128
+//   D from O          0.0038  0.0032  0.0030  0.0028  0.0027  0.0026  0.0025  0.0025  0.0025  0.0024  0.0024  0.0024
+//   D from the keys   0.0024 (0.00235) at any number
+// 32 keys: up to there the rounded O adds 5 % and more to what the result is off anyway (8 % at 16, 14 % at 8, 60 % at 2), behind it less.
+//
 // Work: a block takes 64 queries of a head, a warp 16 of them, whose Q and dO stay in registers as operands of m16n8k16; tiles
 // of 64 keys and values come to shared memory, and of those a warp multiplies the 16 keys at a time that some of its queries see: 16 +
 // window keys a query and no maximum, as L is known.  (The 128-row tiles of tcgen05 would multiply 128 + window keys a query, and
 // wait for one another; here nothing waits but the block for its own copies.)  No mask but the window's: keys outside it reach nothing.
+// The preprocess, which clears the workspace and writes D of the other rows, is launched to run beside it.
 //
-// Bound: HBM, Q, K, V and dO once.  8 x 16 heads of 4,096 rows, d = 128 (537 MB): 103 us (5.2 TB/s) for a window of 16, 188 for 128.
-// The whole backward with it and without, and what dQ is off with and without (relative to its norm, bf16, where its own
-// rounding is 0.0017 and that of dS as much again): window 2 462, 359 us, 0.0024, 0.0037; 16 461, 358 us, 0.0023, 0.0025; 32 475, 360 us, 0.0024,
-// 0.0025; 128 568, 380 us, 0.0024, 0.0024.  Sequences of 128 under a long window 0.0024, 0.0027, as their first queries see
-// few keys and have the largest gradients.
+// Bound: HBM, Q, K, V and dO once.  8 x 16 heads of 4,096 rows, d = 128 (537 MB), all rows: 103 us (5.2 TB/s) for a window of 16.  The
+// whole backward there with D from the keys and with D from O: windows of 2 to 16 438, 361 us, of 32 449, 361 (d = 64 327, 269; d = 256,
+// 4 x 16 heads, 533, 456).  With the first blocks alone: window 1,024 722, 717; 2 x 16 heads of 1,000, d = 64, window 256 39, 37.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <algorithm>
@@ -73,9 +80,10 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const uint16_t* head, in
 template <int D, bool BF16>
 __global__ void __launch_bounds__(THREADS)
     window_delta_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                        const uint16_t* __restrict__ dout, const float* __restrict__ lse2, float* __restrict__ delta, int n,
+                        const uint16_t* __restrict__ dout, const float* __restrict__ lse, float* __restrict__ delta, int n,
                         int npad, int tiles, int group, float scale_log2, int window, int sinks) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;");
   const uint32_t first = smem_u32(smem), second = first + ROWS * D * 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x / tiles, q0 = (blockIdx.x - head * tiles) * ROWS;
@@ -97,7 +105,10 @@ __global__ void __launch_bounds__(THREADS)
   const int i[2] = {w0 + lane / 4, w0 + lane / 4 + 8};
   float minus_l[2], sum[2] = {0.f, 0.f};
 #pragma unroll
-  for (int r = 0; r < 2; ++r) minus_l[r] = i[r] < n ? lse2[(int64_t)head * npad + i[r]] : 0.f;
+  for (int r = 0; r < 2; ++r) {
+    const float l = i[r] < n ? lse[(int64_t)head * n + i[r]] : -INFINITY;  // (as the preprocess: P = 0 on rows without a finite score)
+    minus_l[r] = l > -INFINITY ? -l * 1.4426950408889634f : -INFINITY;
+  }
 
   const int begin = max(0, q0 - window + 1) / ROWS, end = min(q0 + ROWS - 1, n - 1) / ROWS;  // tiles of the window
   const int sink_tiles = min(begin, min(sinks, n) / ROWS + (min(sinks, n) % ROWS != 0));
@@ -150,7 +161,7 @@ cudaError_t launch_d(const BwdArgs& a) {
   cudaError_t e = allow_smem(kern, smem, &allowed);
   if (e != cudaSuccess) return e;
   auto p = [](const void* x) { return static_cast<const uint16_t*>(x); };
-  kern<<<(unsigned)((int64_t)a.bh * tiles), THREADS, smem, a.stream>>>(p(a.q), p(a.k), p(a.v), p(a.dout), a.lse2, a.delta, a.n,
+  kern<<<(unsigned)((int64_t)a.bh * tiles), THREADS, smem, a.stream>>>(p(a.q), p(a.k), p(a.v), p(a.dout), a.lse, a.delta, a.n,
                                                                        (int)padded_rows(a.n), tiles, a.group,
                                                                        a.scale * 1.4426950408889634f, a.window, a.sinks);
   return cudaGetLastError();
@@ -158,8 +169,8 @@ cudaError_t launch_d(const BwdArgs& a) {
 
 }  // namespace
 
-// Queries that see 32 keys or fewer, or short sequences: see above.
-int window_delta_rows(int n, int window, int sinks) { return (int64_t)window + sinks <= 32 || n <= 256 ? n : 0; }
+// All rows where none sees more than 32 keys, else a block of each sequence's first ones: see above.
+int window_delta_rows(int n, int window, int sinks) { return (int64_t)window + sinks <= 32 ? n : n < ROWS ? n : ROWS; }
 
 cudaError_t launch_window_delta(const BwdArgs& a) {
   const bool bf = a.dtype == DT_BF16;

@@ -247,9 +247,9 @@ FA_API fa_status fa_bwd_masked(const void* Q, const void* K, const void* V, cons
  * sinks >= 0 (either may exceed N: a window of N or more is causal attention). bf16 and fp16 with d in {64, 128, 256}; others
  * return FA_ERR_UNSUPPORTED. Key tiles outside the window and the sinks are neither loaded nor multiplied. (Inside a tile
  * of 128 keys that is visible in part, a hidden key's weight is an exact zero, as in fa_fwd: a V row that is not finite reaches
- * every query of a block of 256, at d = 256 of 128, in which some query sees a key of its tile.) One launch forward, the
- * three of fa_bwd backward, and one more where window + sinks <= 32 or N <= 256: with few keys in sight D is summed from them in
- * 32 bits, as the rounded O would cost dQ and dK precision.
+ * every query of a block of 256, at d = 256 of 128, in which some query sees a key of its tile.) One launch forward, four
+ * backward. D of queries that see few keys is summed from those in 32 bits, as the rounded O would cost dQ and dK precision: of all
+ * where window + sinks <= 32, else of the 64 that each sequence begins with.
  */
 FA_API fa_status fa_fwd_window(const void* Q, const void* K, const void* V, void* O, float* L, int B, int H, int Hkv,
                                int N, int d, float scale, int window, int sinks, fa_dtype dtype, void* stream);

@@ -36,3 +36,31 @@ def test_a_masked_window_past_every_length_hides_nothing(fa, causal, window):
     # (dQ's sums come in no fixed order, in 32 bits: a unit in the last place now and then)
     assert ((grads[0].double() - grads2[0].double()).abs() <= 2.0 ** -7 * grads[0].double().abs() + 1e-5).all()
     fa.fa_check_device_error()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("N,window,sinks", [(257, 300, 0), (1000, 300, 5), (640, 33, 0), (300, 40, 300)])
+def test_first_queries_of_a_sequence_see_few_keys(fa, dtype, d, N, window, sinks):
+    """dQ of a sequence's first 64 queries under a longer window, by the bound of queries whose D does not come from the rounded O:
+    dS = p (dP - D) off by (e + 2 ds) |dS| + p (2 ds sum p |dP| + 2 the error of dP), e the rounding of dS to 16 bits and ds that of
+    a score, (d / 16 + 8) 2^-23 |q| |k| scale + 2^-20; dQ rounded once more."""
+    B, H, Hkv, rows = 6, 8, 4, 64
+    q, k, v, do = make(B, H, Hkv, N, d, N + d, dtype)
+    scale, e = d ** -0.5, torch.finfo(dtype).eps / 2
+    o, lse = fa.attention_forward(q, k, v, causal=True, window=window, sinks=sinks)
+    dq = fa.attention_backward(q, k, v, o, do, lse, causal=True, window=window, sinks=sinks)[0]
+    fa.fa_check_device_error()
+    i, j = torch.arange(rows, device="cuda")[:, None], torch.arange(rows, device="cuda")
+    hidden = (j > i) | ((i - j >= window) & (j >= sinks))
+    q1, do1, got = (x[:, :, :rows].double() for x in (q, do, dq))
+    k1, v1 = (x[:, :, :rows].double().repeat_interleave(H // Hkv, 1) for x in (k, v))
+    ds = (d / 16 + 8) * 2.0 ** -23 * scale * float(q1.norm(dim=-1).max() * k1.norm(dim=-1).max()) + 2.0 ** -20
+    p = torch.softmax((q1 @ k1.transpose(-1, -2) * scale).masked_fill(hidden, float("-inf")), -1)
+    dp = do1 @ v1.transpose(-1, -2)
+    g = p * (dp - (p * dp).sum(-1, keepdim=True))
+    dp_tol = (d / 16 + 8) * 2.0 ** -23 * do1.norm(dim=-1, keepdim=True) * v1.norm(dim=-1).max()
+    g_tol = (e + 2 * ds) * g.abs() + p * (2 * ds * (p * dp.abs()).sum(-1, keepdim=True) + 2 * dp_tol)
+    want = scale * (g @ k1)
+    worst = ((got - want).abs() / (e * want.abs() + scale * (g_tol @ k1.abs()) + 2.0 ** -24)).max()
+    assert worst <= 1, float(worst)
