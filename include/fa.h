@@ -432,10 +432,11 @@ FA_API fa_status fa_kv4_evict(const void* cache, const float* weights, const int
  *             sequence; each row sees all of them. They are read once for up to 128 rows of all sequences.
  *   d         64, 128 or 256; H a positive multiple of Hkv, query head h reads key/value head h / (H / Hkv).
  * A row that sees nothing gets O = 0, L = -inf. (A slot that some of a call's Nq rows see and others do not has weight 0 for the
- * others: what is not finite in its V reaches them, as in fa_fwd.) Probabilities are rounded to dtype before they
- * meet V, sums are in 32 bits. The lengths are read on the device: one captured graph serves any. Results do not depend on
- * timing. Two launches; the workspace takes ..._workspace_size(...) bytes for the same arguments, its contents on entry do not
- * matter, and calls that may overlap on the GPU need workspaces of their own.
+ * others: what is not finite in its V reaches them, as in fa_fwd. An infinite element of V may come out as NaN in the rows that
+ * see it: up to 64 rows a head at d = 64 and 128 are multiplied several times over, with weights of 0 in all copies but one.)
+ * Probabilities are rounded to dtype before they meet V, sums are in 32 bits. The lengths are read on the device: one captured
+ * graph serves any. Results do not depend on timing. Two launches; the workspace takes ..._workspace_size(...) bytes for the same
+ * arguments, its contents on entry do not matter, and calls that may overlap on the GPU need workspaces of their own.
  */
 FA_API size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d);
 FA_API fa_status fa_decode_window(const void* Q, const void* K, const void* V, const int32_t* lens, void* O, float* L, int B,
