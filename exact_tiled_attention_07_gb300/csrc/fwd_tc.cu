@@ -662,10 +662,15 @@ __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
           __syncwarp();
         }
       };
-      // (packed) the V rows of the item's last key tile that lie behind the sequence: zero
+      // V rows at the end of a tile that no query of the item sees: zero, as their values may be anything and 0 x NaN is NaN.  (packed) Those
+      // of the item's last key tile behind the sequence; (window) those behind the sinks in the tiles in front of the item's
+      // windows, which every later query of the head meets.
       auto clear_tail = [&](const Item& w, int j, int vidx) {
-        if constexpr (VARLEN) {
-          const int rem = w.n - tile_at(w, j) * BN;
+        if constexpr (VARLEN || WINDOW) {
+          int rem = BN;
+          if constexpr (VARLEN) rem = w.n - tile_at(w, j) * BN;
+          if constexpr (WINDOW)
+            if (j < w.ns) rem = min(rem, sinks - j * BN);
           if (rem >= BN) return;
           uint8_t* vt = smem + C::OFF_RING + slot_of(vidx) * C::ENTRY_BYTES;
           for (int i = rem * 8 + lane; i < BN * 8; i += 32)

@@ -247,7 +247,9 @@ FA_API fa_status fa_bwd_masked(const void* Q, const void* K, const void* V, cons
  * sinks >= 0 (either may exceed N: a window of N or more is causal attention). bf16 and fp16 with d in {64, 128, 256}; others
  * return FA_ERR_UNSUPPORTED. Key tiles outside the window and the sinks are neither loaded nor multiplied. (Inside a tile
  * of 128 keys that is visible in part, a hidden key's weight is an exact zero, as in fa_fwd: a V row that is not finite reaches
- * every query of a block of 256, at d = 256 of 128, in which some query sees a key of its tile.) One launch forward, four
+ * every query of a block of 256, at d = 256 of 128, in which some query's window holds a key of its tile. Of a tile that a block sees for
+ * its sinks alone, nothing but the sinks reaches the block's O. Backward, a row of K or V that is not finite reaches dQ of every
+ * query that meets its tile: with sinks all later ones, if it lies in theirs.) One launch forward, four
  * backward. D of queries that see few keys is summed from those in 32 bits, as the rounded O would cost dQ and dK precision: of all
  * where window + sinks <= 32, else of the 64 that each sequence begins with.
  */

@@ -51,3 +51,28 @@ def test_decode_a_value_that_is_not_finite_stays_in_its_column_of_the_rows_that_
         vp2[0, slot, 7] = value
         reached(*clean, *fa.attention_decode_prefix(q, kp, vp2, k, v, lens), (slice(None), 0, slice(None), 7))
     fa.fa_check_device_error()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("sinks", [1, 4, 16, 17, 33, 100, 128, 131, 200])
+def test_window_a_value_behind_the_sinks_stays_with_the_queries_whose_window_is_near(fa, d, sinks):
+    """Hidden values in the sinks' own tiles: the queries of a block of 256 that see sinks alone of those tiles do not get them."""
+    N, window, H, Hkv = 1000, 100, 4, 2
+    q, k, v = randn(1, 2, H, N, d), randn(2, 2, Hkv, N, d), randn(3, 2, Hkv, N, d)
+    clean = fa.attention_forward(q, k, v, causal=True, window=window, sinks=sinks)
+    cu = torch.tensor([0, 7, 7 + N, 7 + N + 60], dtype=torch.int32, device="cuda")
+    pack = lambda t: torch.cat((t[0, :, :7], t[1], t[0, :, :60]), 1).transpose(0, 1)  # noqa: E731
+    packed = fa.attention_forward_varlen(pack(q), pack(k), pack(v), cu, causal=True, window=window, sinks=sinks)
+    last = sinks // 128 * 128 + 128  # behind the tile of the first row that is no sink
+    first = (last + window - 1 + 255) // 256 * 256  # of the blocks whose windows lie behind those
+    for rows in (slice(sinks, last), slice(sinks, sinks + 1)):
+        for value in (math.nan, math.inf):
+            v2 = v.clone()
+            v2[:, :, rows] = value
+            o, lse = fa.attention_forward(q, k, v2, causal=True, window=window, sinks=sinks)
+            assert torch.equal(lse, clean[1])
+            assert torch.equal(o[:, :, first:], clean[0][:, :, first:])
+            assert not o[:, :, sinks:sinks + window].isfinite().any()
+            o, lse = fa.attention_forward_varlen(pack(q), pack(k), pack(v2), cu, causal=True, window=window, sinks=sinks)
+            assert torch.equal(lse, packed[1]) and torch.equal(o[7 + first:7 + N], packed[0][7 + first:7 + N])
+    fa.fa_check_device_error()
