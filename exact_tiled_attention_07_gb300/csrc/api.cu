@@ -1085,7 +1085,7 @@ fa_status fa_qk_norm_rope(const void* Q, const void* K, const void* wq, const vo
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
-  // a row of sums for each block, for as many as the largest GPU of this kind takes
+  // a row of sums for each block, for as many as the current device takes at once
   return d < 8 || d > 256 || d % 8 != 0 ? 0 : (size_t)norm_rope_bwd_blocks() * d * 4;
 }
 

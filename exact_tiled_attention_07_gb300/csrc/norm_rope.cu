@@ -226,8 +226,8 @@ struct RopeCfg {
   static constexpr int PIECES = BWD ? 4 : 2;        // of x (and dy) for every lane
   static constexpr int STAGE = kThreads * PIECES * PIECE;
   // Blocks an SM and rows in flight.  Two blocks with 128 registers a thread where a lane has 16 channels (three spill, 102 us
-  // against 93 for norm and rotation of 8 x 4096 tokens, 16 + 16 heads of 128 in bf16), three or four where it has 8; deeper
-  // rings measured the same.
+  // against 93 for norm and rotation of 8 x 4096 tokens, 16 + 16 heads of 128 in bf16), three where it has 8; deeper rings
+  // measured the same.
   static constexpr int OCC = P == 8 ? 2 : 3;
   static constexpr int STAGES = (BWD ? 3 : 4) * 16 / PIECE;
   static constexpr int SMEM = STAGES * STAGE;

@@ -438,7 +438,8 @@ FA_API fa_status fa_kv4_evict(const void* cache, const float* weights, const int
  * see it: up to 64 rows a head at d = 64 and 128 are multiplied several times over, with weights of 0 in all copies but one.)
  * Probabilities are rounded to dtype before they meet V, sums are in 32 bits. The lengths are read on the device: one captured
  * graph serves any. Results do not depend on timing. Two launches; the workspace takes ..._workspace_size(...) bytes for the same
- * arguments, its contents on entry do not matter, and calls that may overlap on the GPU need workspaces of their own.
+ * arguments on the current device (one with more SMs takes more), its contents on entry do not matter, and calls that may overlap
+ * on the GPU need workspaces of their own.
  */
 FA_API size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Nq, int capacity, int d);
 FA_API fa_status fa_decode_window(const void* Q, const void* K, const void* V, const int32_t* lens, void* O, float* L, int B,
@@ -471,7 +472,8 @@ FA_API fa_status fa_decode_prefix(const void* Q, const void* KP, const void* VP,
  * strides and lie side by side inside a token.
  * Backward: dQ, dK (gradients of Q and K from dQo and dKo) and dwq, dwk ([d] weight_dtype; NULL: not wanted), which are sums over
  * all tokens and heads, in 32 bits in an order that does not depend on timing. Two launches; the workspace takes
- * fa_qk_norm_rope_bwd_workspace_size(d) bytes, its contents on entry do not matter. No tokens: dwq and dwk are 0.
+ * fa_qk_norm_rope_bwd_workspace_size(d) bytes on the current device (one with more SMs takes more), its contents on entry do not
+ * matter. No tokens: dwq and dwk are 0.
  */
 FA_API fa_status fa_qk_norm_rope(const void* Q, const void* K, const void* wq, const void* wk, const float* table,
                                  const int32_t* positions, void* Qo, void* Ko, const int64_t* strides, int B, int N, int H,
