@@ -6,6 +6,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
+from test_gpu_window import run  # noqa: E402
+
 
 @pytest.fixture(scope="module")
 def fa():
@@ -64,3 +66,10 @@ def test_first_queries_of_a_sequence_see_few_keys(fa, dtype, d, N, window, sinks
     want = scale * (g @ k1)
     worst = ((got - want).abs() / (e * want.abs() + scale * (g_tol @ k1.abs()) + 2.0 ** -24)).max()
     assert worst <= 1, float(worst)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,Hkv,N,window,sinks", [(8, 1, 4097, 256, 4), (16, 2, 2500, 700, 300), (12, 1, 3001, 1, 1)])
+def test_many_query_heads_over_a_long_sequence(fa, d, H, Hkv, N, window, sinks):
+    """The key tiles with sinks meet all later queries of all heads of their group: thousands of steps of one block in the backward."""
+    run(fa, 1, H, Hkv, N, d, "bf16", window, sinks)
