@@ -905,7 +905,8 @@ def _sinks_allowed(causal, window, sinks, block_mask=None):
 def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, block_mask=None, sinks=None):
     """O, L = fa_fwd(q, k, v) (fa_fwd_gqa when k, v have fewer heads than q; fa_fwd_masked with a
     window or a block mask; fa_fwd_window with a window, causal, and sinks given, which may be 0); outputs on q's
-    device."""
+    device. sinks=None: the kernels that a window took before there were sinks, so that results stay as they were to the
+    bit; 0 is the same mask on the faster ones (the same O, L and dV; dK and dQ by unrounded probabilities, and d = 256 too)."""
     if _sinks_allowed(causal, window, sinks, block_mask):
         shape = _window_shape(q, k, v)
         o = _new(q.shape, q.dtype, q.device, stream)
@@ -931,7 +932,7 @@ def attention_forward(q, k, v, causal=False, scale=None, stream=None, window=0, 
 def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=None, stream=None, window=0,
                        block_mask=None, sinks=None):
     """dQ, dK, dV = fa_bwd(...) (fa_bwd_masked with a window or a block mask; fa_bwd_window with a window
-    and sinks, which may be 0); outputs (and workspace, unless given) allocated with torch."""
+    and sinks, which may be 0: see attention_forward); outputs (and workspace, unless given) allocated with torch."""
     if _sinks_allowed(causal, window, sinks, block_mask):
         lib, dt, dev = load_library(), q.dtype, q.device
         B, H, Hkv, N, d = _window_shape(q, k, v, (o, do), (), (lse,), (workspace,))

@@ -457,7 +457,8 @@ FA_API fa_status fa_decode_prefix(const void* Q, const void* KP, const void* VP,
  *             heads (its pointers are then not looked at)
  *   Qo, Ko    out: the same, normed and rotated: y = x w / sqrt(mean(x^2) + eps) over the row's d elements, then each of
  *             the rotary / 2 pairs of channels (a, b) becomes (a cos - b sin, b cos + a sin). In 32 bits, rounded once. (A row
- *             of zeros is NaN with eps = 0. What is not finite in a row stays in it and, backward, in dwq or dwk.)
+ *             of zeros is NaN with eps = 0; one whose squares add up past 3.4e38 comes out as zeros. What is not finite in a
+ *             row stays in it and, backward, in dwq or dwk.)
  *   wq, wk    [d] weight_dtype (fp32 or dtype), or NULL: ones
  *   table     [table_len][rotary] fp32: cos of the rotary / 2 pairs' angles at a position, then their sin
  *   positions device int32 [B][N], or NULL: token n of every sequence is at position n (then N <= table_len). A position

@@ -76,3 +76,18 @@ def test_window_a_value_behind_the_sinks_stays_with_the_queries_whose_window_is_
             o, lse = fa.attention_forward_varlen(pack(q), pack(k), pack(v2), cu, causal=True, window=window, sinks=sinks)
             assert torch.equal(lse, packed[1]) and torch.equal(o[7 + first:7 + N], packed[0][7 + first:7 + N])
     fa.fa_check_device_error()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_of_rows_whose_squares_pass_32_bits(fa, dtype):
+    x = randn(1, 5, 3, 64, dtype=dtype)
+    x[2, 1] *= 1e30
+    k = x[:, :1].contiguous()
+    w, table = torch.ones(64, device="cuda"), fa.rope_table(5, 64)
+    y, _ = fa.qk_norm_rope(x, k, w, w, table)
+    clean = x.clone()
+    clean[2, 1] = 1.0
+    want, _ = fa.qk_norm_rope(clean, k, w, w, table)
+    assert (y[2, 1] == 0).all()
+    want[2, 1] = 0
+    assert torch.equal(y, want)
