@@ -936,7 +936,8 @@ def attention_backward(q, k, v, o, do, lse, causal=False, scale=None, workspace=
     if _sinks_allowed(causal, window, sinks, block_mask):
         lib, dt, dev = load_library(), q.dtype, q.device
         B, H, Hkv, N, d = _window_shape(q, k, v, (o, do), (), (lse,), (workspace,))
-        dq, dk, dv = (_new(shape, dt, dev, stream) for shape in (q.shape, k.shape, k.shape))
+        dq = _new(q.shape, dt, dev, stream)
+        dk, dv = _new(k.shape, dt, dev, stream), _new(k.shape, dt, dev, stream)
         ws = workspace
         if ws is None:
             ws = _new_workspace(max(lib.fa_bwd_workspace_size(B, H, N, d), 16), dev, stream)
@@ -1061,8 +1062,10 @@ def qk_norm_rope_backward(dqo, dko, q, k, q_weight, k_weight, table, positions=N
     if out is not None:
         dq, dk = out
     else:
-        dq, dk = (_new(t.shape, q.dtype, q.device, stream) for t in (q, k))
-    dwq, dwk = (None if w is None else _new(w.shape, w.dtype, q.device, stream) for w in (q_weight, k_weight))
+        dt, dev = q.dtype, q.device
+        dq, dk = _new(q.shape, dt, dev, stream), _new(k.shape, dt, dev, stream)
+    dwq = None if q_weight is None else _new(q_weight.shape, q_weight.dtype, q.device, stream)
+    dwk = None if k_weight is None else _new(k_weight.shape, k_weight.dtype, q.device, stream)
     if dqo.dim() == 4 and dko.dim() == 4:  # [B, heads, N, d]
         sizes = _norm_rope_sizes(q, k, q_weight, k_weight, table, positions, eps, interleaved, (dq, dk))
         B, N, H, Hkv, d = sizes[:5]
