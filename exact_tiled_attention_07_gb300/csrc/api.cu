@@ -233,9 +233,12 @@ bool rows_meet(const RowTensor& a, const RowTensor& b, int B, int N, int d, int 
   const int64_t off = (int64_t)((reinterpret_cast<uintptr_t>(hi.p) - reinterpret_cast<uintptr_t>(lo.p)) / eb);
   const int64_t lo_end = (lo.heads - 1) * lo.st.head + d, hi_end = off + (hi.heads - 1) * hi.st.head + d;
   if (off < lo_end) return true;
-  if (a.st.head == b.st.head && a.st.head > 0 && off % a.st.head == 0 && off / a.st.head >= lo.heads &&
-      rows_apart(lo.st, off / a.st.head + hi.heads, B, N, d))
-    return false;
+  // heads of one tensor (the stride of one head alone is open: the other's, or where both are alone what lies between them)
+  if (lo.heads == 1 || hi.heads == 1 || lo.st.head == hi.st.head) {
+    NormRopeStrides st = lo.st;
+    st.head = lo.heads > 1 ? lo.st.head : (hi.heads > 1 ? hi.st.head : off);
+    if (st.head > 0 && off % st.head == 0 && off / st.head >= lo.heads && rows_apart(st, off / st.head + hi.heads, B, N, d)) return false;
+  }
   // the smaller step of the token and the batch dimension repeats the pattern; the larger one has to leave room for it
   int64_t small = INT64_MAX, large = INT64_MAX;
   int n_small = 1;
