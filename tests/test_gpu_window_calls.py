@@ -73,3 +73,44 @@ def test_first_queries_of_a_sequence_see_few_keys(fa, dtype, d, N, window, sinks
 def test_many_query_heads_over_a_long_sequence(fa, d, H, Hkv, N, window, sinks):
     """The key tiles with sinks meet all later queries of all heads of their group: thousands of steps of one block in the backward."""
     run(fa, 1, H, Hkv, N, d, "bf16", window, sinks)
+
+
+@pytest.mark.parametrize("window", [1, 8, 32, 300])
+def test_backward_in_graphs_that_share_a_workspace_and_on_streams_of_their_own(fa, window):
+    """D's launch and the preprocess beside it: replayed, in turn with another call over the same workspace, and side by side with
+    calls over others. dV and dK do not depend on the run, dQ's sums (in no fixed order, in 32 bits) on a unit in the last place."""
+    shapes = [(2, 4, 2, 700, 128), (1, 8, 8, 1500, 64)]
+    calls = []
+    ws = torch.empty(max(fa.fa_bwd_workspace_size(B, H, N, d) for B, H, _, N, d in shapes), dtype=torch.uint8, device="cuda")
+    for i, (B, H, Hkv, N, d) in enumerate(shapes):
+        q, k, v, do = make(B, H, Hkv, N, d, i)
+        o, lse = fa.attention_forward(q, k, v, causal=True, window=window, sinks=0)
+        kw = {"causal": True, "window": window, "sinks": 0}
+        calls.append(lambda a=(q, k, v, o, do, lse), kw=kw, **more: fa.attention_backward(*a, **kw, **more))
+    want = [call() for call in calls]
+
+    def same(got, ref):
+        assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
+        assert ((got[0].double() - ref[0].double()).abs() <= 2.0 ** -7 * ref[0].double().abs() + 1e-5).all()
+
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for call in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call(workspace=ws))
+        graphs.append(graph)
+    ws.fill_(255)
+    for _ in range(3):
+        for i in (0, 1):
+            graphs[i].replay()
+            same(calls[1 - i](workspace=ws), want[1 - i])
+            same(outs[i], want[i])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    many = [[call(stream=s) for s in streams] for _ in range(4) for call in calls]
+    torch.cuda.synchronize()
+    for n, outs in enumerate(many):
+        for got in outs:
+            same(got, want[n % 2])
+    fa.fa_check_device_error()
