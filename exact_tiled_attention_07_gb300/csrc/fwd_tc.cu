@@ -183,8 +183,8 @@ struct VarlenSpec {
 // window / 128 + 2 tiles the first is masked whole.
 // Bound: tensor and softmax, as the plain kernel, and an item's latencies (about 2.6 us, which ten tiles make up for less than
 // thirty).  Measured: 8 x 16 heads of 4,096 rows, window 1,024, 4 sinks, d = 128 250 us (76 % of the tiles' scores are visible,
-// 1,270 TFLOP/s on all of them; masked tiles by one general comparison: 264), d = 64 201 (232); prompts of 16,384 and
-// less, 32 heads on 8, window 2,048 735 us (768).
+// 1,270 TFLOP/s on all of them; masked tiles by one general comparison: 264), d = 64 204 (232); prompts of 16,384 and
+// less, 32 heads on 8, window 2,048 746 us (768).
 template <int D, bool BF16, bool MASKED, bool QUEUE, bool F8 = false, bool VARLEN = false, bool WINDOW = false>
 __global__ void __launch_bounds__(FwdCfg<D, F8>::THREADS, 1)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
