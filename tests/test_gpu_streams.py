@@ -169,3 +169,40 @@ def test_results_of_another_stream_may_be_read_later(fa):
         fa.attention_forward(q * 2, k, v, causal=True, window=300, sinks=4, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(later, want)
+
+
+@pytest.mark.parametrize("name", ["forward_sinks", "backward_sinks", "decode_window", "norm_backward", "decode_kv4"])
+def test_a_stream_that_joins_a_capture(fa, name):
+    """Results and workspaces of a call on another stream inside a capture belong to the graph."""
+    call, _ = CALLS[name](fa)
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    call(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        first = call(side)
+        call(side)  # (results that are dropped inside the capture)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for t in first:
+            t.fill_(0)
+        others = [torch.full_like(t, 7) for t in first for _ in range(4)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, want))
+        assert all((t == 7).all() for t in others)
+    fa.fa_check_device_error()
+
+
+def test_the_default_stream_by_its_handle(fa):
+    q, k, v = qkv()
+    want = fa.attention_forward(q, k, v, causal=True, window=300, sinks=4)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = fa.attention_forward(q, k, v, causal=True, window=300, sinks=4, stream=0)
+        torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+        got = [t.clone() for t in got]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
